@@ -71,8 +71,10 @@ enum tv_status {
   TV_ERR_CAPACITY = -7,     /* block table too short for prefix_len + N slots */
   TV_ERR_BAD_BLOCK = -8,    /* a block-table entry outside [0, num_blocks), or (compaction)
                                two logical blocks of the tree's window on one physical block */
-  TV_ERR_SCRATCH = -9       /* tv_tree_attn_static: the call needs more than
+  TV_ERR_SCRATCH = -9,      /* tv_tree_attn_static: the call needs more than
                                TV_STATIC_SCRATCH_BYTES of scratch */
+  TV_ERR_BAD_SEQLEN = -10   /* tv_linear_attn_prompt: cu_seqlens decreases, leaves [0, T], or
+                               holds a prompt longer than max_len */
 };
 
 enum tv_dtype { TV_F32 = 0, TV_BF16 = 1 };
@@ -500,6 +502,111 @@ TV_API int tv_kv_compact_remap(void* k_cache, void* v_cache, int num_blocks, con
 TV_API int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, const int32_t* target_tokens,
                           int B, int N, int Lmax, int32_t* accepted_path, int32_t* accepted_len,
                           int32_t* next_token, int32_t* err, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_linear_attn_prompt -- linear attention with a decay over whole prompts.
+ *
+ * The pages have no counterpart: they verify draft trees from a committed state.  This call
+ * makes such a state from a prompt, for layers whose recurrence decays without a delta
+ * correction -- the gated delta rule above with its (I - beta k k^T) left out:
+ *     S_t = alpha_t S_{t-1} + v_t k_t^T,     o_t = S_t (q_scale q_t),
+ * S [dv, dk] with the value index as its row, as everywhere in this library.
+ *
+ * B prompts lie back to back: prompt b is tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1 of T.  A
+ * prompt may be empty (its S is then its S0).  Query and key heads may be shared: value head h
+ * reads query and key head h / (H / Hk).
+ *
+ *   q, k        [T, Hk, dk] io_dtype   in   token t's heads start at q + t * q_stride (elements);
+ *   v           [T, H, dv]  io_dtype   in   k_stride, v_stride, out_stride alike: slices of one
+ *                                           projection's output need no copy
+ *   alpha       fp32                   in   decay in [0, 1] of token t, head h at
+ *                                           alpha[t * alpha_stride + h]; alpha_stride 0: [H], one
+ *                                           decay for each head
+ *   S0          [B, H, dv, dk] state_dtype  in   state before the prompt; NULL: zero
+ *   cu_seqlens  [B + 1] int32          in
+ *   max_len     an upper bound of the prompts' lengths (T serves; closer is faster)
+ *   out         [T, H, dv]  io_dtype   out  rows of no prompt are not written
+ *   S           [B, H, dv, dk] state_dtype  out  state after the prompt; may be S0 itself
+ *   workspace   device scratch of at least tv_linear_attn_workspace_size(...) bytes, 16-byte
+ *               aligned (may be NULL when that is 0); contents on entry are ignored.  Calls that
+ *               share a workspace must not overlap in time.
+ *   err         [B] int32              out  0, or TV_ERR_BAD_SEQLEN in every entry when cu_seqlens
+ *                                           decreases, leaves [0, T] or holds a prompt longer than
+ *                                           max_len (nothing else is written then); or
+ *                                           TV_ERR_TIMEOUT (a bounded device wait gave up; that
+ *                                           prompt's outputs are then unspecified)
+ * Rounding: products accumulate in fp32; bf16 operands that are themselves sums or scaled
+ * (scores, decayed keys, states) enter the matrix units as a bf16 pair, value and remainder.
+ * A non-finite input makes later tokens of its prompt and head non-finite, and may make earlier
+ * ones of the same 128-token chunk so; other prompts are not touched.
+ * Supported: dk, dv in {64, 128}; H a multiple of Hk; (io, state) as tv_gdn_tree_verify_fork.
+ * Strides: at least the dense row (Hk * dk or H * dv; alpha H or 0) and whole multiples of 16
+ * bytes (alpha: any), else TV_ERR_INVALID_ARG.
+ * ---------------------------------------------------------------------------------------- */
+TV_API size_t tv_linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int dv, int io_dtype);
+TV_API int tv_linear_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, const float* alpha, int64_t alpha_stride, const void* S0,
+                                 const int32_t* cu_seqlens, int B, int T, int max_len, int Hk, int H, int dk, int dv,
+                                 int io_dtype, int state_dtype, float q_scale, void* out, int64_t out_stride, void* S,
+                                 void* workspace, size_t workspace_bytes, int32_t* err, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_linear_attn_step -- the same recurrence for one new token of every sequence.
+ *
+ * S <- alpha S + v k^T in place, out = S (q_scale q).  The output uses the fp32 state before its
+ * rounding to state_dtype.
+ *
+ *   q, k        [B, Hk, dk] io_dtype, v [B, H, dv] io_dtype   in   strides as tv_linear_attn_prompt
+ *   alpha       [B, H] (alpha_stride) or [H] (alpha_stride 0) fp32   in
+ *   live        [B] int32, optional (NULL: all)   in   a sequence with live[b] = 0 is skipped: its
+ *               state and output rows are left as they are (rows of a padded batch)
+ *   out         [B, H, dv] io_dtype               out
+ *   S           [B, H, dv, dk] state_dtype        in/out
+ * Supported sizes and types as tv_linear_attn_prompt.
+ * ---------------------------------------------------------------------------------------- */
+TV_API int tv_linear_attn_step(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const float* alpha, int64_t alpha_stride, const int32_t* live, int B,
+                               int Hk, int H, int dk, int dv, int io_dtype, int state_dtype, float q_scale, void* out,
+                               int64_t out_stride, void* S, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_gated_rmsnorm -- a mixer's output, normalised per head and multiplied by its gate.
+ *
+ * With n(x) = x / sqrt(mean(x^2) + eps) * (weight_offset + weight) over the d columns of a head and
+ * silu(g) = g / (1 + exp(-g)):
+ *     gate_first = 0:  out = n(x) silu(gate)          gate_first = 1:  out = n(x silu(gate))
+ *
+ *   x, gate, out  [rows, H, d] io_dtype   row r starts at x + r * x_stride (elements); gate may be
+ *                 NULL (factor 1); out may be x itself
+ *   weight        [d] io_dtype, or NULL (out is not scaled by a weight, and weight_offset is not used)
+ * Arithmetic is fp32, rounded once on store.  Any d from 1 to 32768 and any stride of at least H * d;
+ * base addresses need only their element's alignment.  rows * H < 2^31.
+ * ---------------------------------------------------------------------------------------- */
+TV_API int tv_gated_rmsnorm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
+                            const void* weight, int rows, int H, int d, int io_dtype, float eps, float weight_offset,
+                            int gate_first, void* out, int64_t out_stride, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_residual_rmsnorm -- a block's output into the residual stream, and the next block's norm.
+ *
+ *     t   = y, or n(y) with post_weight          (the norm after the block)
+ *     r   = residual + scale * gate * t          (gate NULL: 1)
+ *     residual_out = r,  out = n(r) with weight  (the norm before the next block)
+ * n as above, over the D columns; out is taken from the fp32 r before its rounding.
+ *
+ *   y, gate, out             [rows, D] io_dtype; out may be NULL (weight is then ignored)
+ *   residual, residual_out   [rows, D] residual_dtype
+ *   post_weight, weight      [D] io_dtype; post_weight NULL: no norm after the block; weight NULL: n
+ *                            without a weight
+ * residual_out may be residual itself, and out may be y itself.  Supported: (io, residual) in
+ * {(F32,F32), (BF16,BF16), (BF16,F32)}; 1 <= D <= 32768; strides of at least D elements; base
+ * addresses need only their element's alignment.
+ * ---------------------------------------------------------------------------------------- */
+TV_API int tv_residual_rmsnorm(const void* y, int64_t y_stride, const void* residual, int64_t residual_stride,
+                               const void* post_weight, const void* gate, int64_t gate_stride, float scale,
+                               const void* weight, int rows, int D, int io_dtype, int residual_dtype, float eps,
+                               float weight_offset, void* residual_out, int64_t residual_out_stride, void* out,
+                               int64_t out_stride, tv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * tv_test_bounded_wait -- test support for the bounded device waits.

@@ -30,6 +30,7 @@ TV_ERR_TIMEOUT = -6
 TV_ERR_CAPACITY = -7
 TV_ERR_BAD_BLOCK = -8
 TV_ERR_SCRATCH = -9
+TV_ERR_BAD_SEQLEN = -10
 TV_F32 = 0
 TV_BF16 = 1
 TV_MODE_FORK = 0
@@ -44,12 +45,14 @@ EXPORTED = ("tv_status_string", "tv_last_cuda_error", "tv_version", "tv_tree_pre
             "tv_accept_walk", "tv_gdn_tree_verify_fork_selective", "tv_gdn_commit_selective",
             "tv_gdn_tree_verify_wy_lazy", "tv_gdn_fork_workspace_size", "tv_gdn_tree_verify_fork_ws",
             "tv_gdn_fork_materialize", "tv_gdn_fork_materialize_selective", "tv_gdn_commit_layers",
-            "tv_kv_compact_remap", "tv_test_bounded_wait")
+            "tv_kv_compact_remap", "tv_linear_attn_workspace_size", "tv_linear_attn_prompt",
+            "tv_linear_attn_step", "tv_gated_rmsnorm", "tv_residual_rmsnorm", "tv_test_bounded_wait")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 
 _SIGNATURES = {
     "tv_status_string": (ctypes.c_char_p, [_I]),
@@ -81,6 +84,13 @@ _SIGNATURES = {
     "tv_kv_compact": (_I, [_P, _P, _I, _P, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
     "tv_kv_compact_remap": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
                                  _P]),
+    "tv_linear_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
+    "tv_linear_attn_prompt": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F,
+                                   _P, _L, _P, _P, _Z, _P, _P]),
+    "tv_linear_attn_step": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _L, _P,
+                                 _P]),
+    "tv_gated_rmsnorm": (_I, [_P, _L, _P, _L, _P, _I, _I, _I, _I, _F, _F, _I, _P, _L, _P]),
+    "tv_residual_rmsnorm": (_I, [_P, _L, _P, _L, _P, _P, _L, _F, _P, _I, _I, _I, _I, _F, _F, _P, _L, _P, _L, _P]),
     "tv_test_bounded_wait": (_I, [ctypes.c_uint, _I, _P, _P, _P]),
 }
 
@@ -118,6 +128,27 @@ def _ptr(t):
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError("tensors passed to the library must be contiguous CUDA tensors")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t):
+    """Pointer and row stride (elements) of a tensor whose rows -- everything past the first
+    dimension -- are dense; the rows themselves may lie apart, as in a slice of a projection."""
+    if t is None:
+        return None, 0
+    dense = 1
+    for n, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and stride != dense:
+            raise ValueError("the rows of tensors passed to the library must be dense")
+        dense *= n
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the library must be CUDA tensors")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else dense
+
+
+def _same(what: str, t, shape, dtype=None) -> None:
+    """The library sees pointers and sizes only: a tensor of another shape or type is caught here."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{what}: expected {tuple(shape)} {dtype or ''}, got {tuple(t.shape)} {t.dtype}")
 
 
 def _stream(stream):
@@ -336,6 +367,90 @@ def tv_accept_walk(parents, draft_tokens, target_tokens, accepted_path, accepted
     _check(lib.tv_accept_walk(_ptr(parents), _ptr(draft_tokens), _ptr(target_tokens), B, N, accepted_path.shape[1],
                               _ptr(accepted_path), _ptr(accepted_len), _ptr(next_token), _ptr(err), _stream(stream)),
            "tv_accept_walk")
+
+
+def tv_linear_attn_workspace_size(B, T, max_len, H, dk, dv, io_dtype=torch.bfloat16) -> int:
+    return int(lib.tv_linear_attn_workspace_size(B, T, max_len, H, dk, dv, _DTYPES[io_dtype]))
+
+
+def _alpha(alpha, n, H):
+    """One decay per head, [H], or per token and head, [n, H]."""
+    _same("alpha", alpha, (H,) if alpha.dim() == 1 else (n, H), torch.float32)
+    return (_ptr(alpha), 0) if alpha.dim() == 1 else _rows(alpha)
+
+
+def tv_linear_attn_prompt(q, k, v, alpha, cu_seqlens, out, S, err, S0=None, max_len: int | None = None,
+                          workspace=None, q_scale: float = 1.0, stream=None) -> None:
+    """S_t = alpha_t S_{t-1} + v_t k_t^T, out_t = S_t (q_scale q_t) over packed prompts: q, k
+    [T, Hk, dk] and v, out [T, H, dv] (token stride free, so slices of one projection serve), alpha
+    [T, H] or [H] fp32, cu_seqlens [B + 1] int32, S (and S0, which may be S) [B, H, dv, dk].
+    Without a ``workspace`` one is taken from torch's allocator when the call needs it."""
+    T, H, dv = v.shape
+    Hk, dk = q.shape[1:]
+    B = cu_seqlens.shape[0] - 1
+    for name, t, shape, dtype in (("q", q, (T, Hk, dk), v.dtype), ("k", k, (T, Hk, dk), v.dtype),
+                                  ("out", out, (T, H, dv), v.dtype), ("S", S, (B, H, dv, dk), None),
+                                  ("S0", S0, (B, H, dv, dk), S.dtype), ("cu_seqlens", cu_seqlens, (B + 1,), torch.int32),
+                                  ("err", err, (B,), torch.int32)):
+        _same(name, t, shape, dtype)
+    (pq, sq), (pk, sk), (pv, sv), (po, so), (pa, sa) = _rows(q), _rows(k), _rows(v), _rows(out), _alpha(alpha, T, H)
+    max_len = T if max_len is None else int(max_len)
+    if workspace is None:
+        need = lib.tv_linear_attn_workspace_size(B, T, min(max_len, T), H, dk, dv, _DTYPES[v.dtype])
+        if need:
+            on = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(on):
+                workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.tv_linear_attn_prompt(
+        pq, sq, pk, sk, pv, sv, pa, sa, _ptr(S0), _ptr(cu_seqlens), B, T, max_len, Hk, H, dk, dv, _DTYPES[v.dtype],
+        _DTYPES[S.dtype], float(q_scale), po, so, _ptr(S), _ptr(workspace), size, _ptr(err), _stream(stream)),
+        "tv_linear_attn_prompt")
+
+
+def tv_linear_attn_step(q, k, v, alpha, S, out, live=None, q_scale: float = 1.0, stream=None) -> None:
+    """One token of every sequence: S [B, H, dv, dk] in place; q, k [B, Hk, dk], v, out [B, H, dv],
+    alpha [B, H] or [H]; sequences with live[b] = 0 are left alone."""
+    B, H, dv = v.shape
+    Hk, dk = q.shape[1:]
+    for name, t, shape, dtype in (("q", q, (B, Hk, dk), v.dtype), ("k", k, (B, Hk, dk), v.dtype),
+                                  ("out", out, (B, H, dv), v.dtype), ("S", S, (B, H, dv, dk), None),
+                                  ("live", live, (B,), torch.int32)):
+        _same(name, t, shape, dtype)
+    (pq, sq), (pk, sk), (pv, sv), (po, so), (pa, sa) = _rows(q), _rows(k), _rows(v), _rows(out), _alpha(alpha, B, H)
+    _check(lib.tv_linear_attn_step(
+        pq, sq, pk, sk, pv, sv, pa, sa, _ptr(live), B, Hk, H, dk, dv, _DTYPES[v.dtype], _DTYPES[S.dtype],
+        float(q_scale), po, so, _ptr(S), _stream(stream)), "tv_linear_attn_step")
+
+
+def tv_gated_rmsnorm(x, gate, weight, out, eps: float, gate_first: bool = False, weight_offset: float = 0.0,
+                     stream=None) -> None:
+    """x, gate, out [rows, H, d] (row stride free): rmsnorm over d, times silu(gate); with
+    ``gate_first`` the norm is taken of x * silu(gate).  gate and weight [d] may be None."""
+    rows, H, d = x.shape
+    for name, t, shape in (("gate", gate, x.shape), ("out", out, x.shape), ("weight", weight, (d,))):
+        _same(name, t, shape, x.dtype)
+    (px, sx), (pg, sg), (po, so) = _rows(x), _rows(gate), _rows(out)
+    _check(lib.tv_gated_rmsnorm(px, sx, pg, sg, _ptr(weight), rows, H, d, _DTYPES[x.dtype], float(eps),
+                                float(weight_offset), int(bool(gate_first)), po, so, _stream(stream)),
+           "tv_gated_rmsnorm")
+
+
+def tv_residual_rmsnorm(y, residual, residual_out, eps: float, out=None, weight=None, post_weight=None, gate=None,
+                        scale: float = 1.0, weight_offset: float = 0.0, stream=None) -> None:
+    """residual_out = residual + scale * gate * (y, or rmsnorm(y) with post_weight); out (optional) =
+    rmsnorm(residual_out) with weight.  All [rows, D] (row stride free), weights [D]."""
+    rows, D = y.shape
+    for name, t, shape, dtype in (("residual", residual, (rows, D), None), ("out", out, (rows, D), y.dtype),
+                                  ("residual_out", residual_out, (rows, D), residual.dtype),
+                                  ("gate", gate, (rows, D), y.dtype), ("weight", weight, (D,), y.dtype),
+                                  ("post_weight", post_weight, (D,), y.dtype)):
+        _same(name, t, shape, dtype)
+    (py, sy), (pr, sr), (pg, sg), (pro, sro), (po, so) = (_rows(y), _rows(residual), _rows(gate), _rows(residual_out),
+                                                          _rows(out))
+    _check(lib.tv_residual_rmsnorm(py, sy, pr, sr, _ptr(post_weight), pg, sg, float(scale), _ptr(weight), rows, D,
+                                   _DTYPES[y.dtype], _DTYPES[residual.dtype], float(eps), float(weight_offset), pro,
+                                   sro, po, so, _stream(stream)), "tv_residual_rmsnorm")
 
 
 def tv_test_bounded_wait(max_polls: int, arrive: bool, status, elapsed_ns, stream=None) -> None:

@@ -1,0 +1,337 @@
+// Linear attention with a decay per head: S_t = alpha_t S_{t-1} + v_t k_t^T, o_t = S_t (q_scale q_t).
+//
+//   linear_attn_kernel       whole prompts, token by token, on the CUDA cores: every supported type
+//                            and size
+//   linear_attn_scan_kernel  the states that the segments of a cut prompt start from
+//   linear_attn_step_kernel  one token of every sequence
+//
+// Row r of S needs k_t, q_t, alpha_t and v_t[r] only, so rows are independent: a CTA of the prompt
+// kernel keeps kRows rows in registers, eight lanes a row, and walks the tokens.
+#include "linear_attn.cuh"
+
+namespace tv {
+namespace {
+
+// ------------------------------------------------------------------ prompts, token by token
+constexpr int kThreads = 128;
+constexpr int kLPR = 8;                                // lanes per state row
+constexpr int kRPL = 2;                                // rows per lane
+constexpr int kRows = kThreads / kLPR * kRPL;          // rows per CTA
+constexpr int kBlock = 16;                             // tokens staged at a time
+
+// Eight elements as stored, then as floats.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const bf16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* o) const { unpack8(w, o); }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* o) const {
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+  }
+};
+
+// Sums v[0..7] over eight consecutive lanes; lane l of the eight receives the total of v[l].
+// Halving the values with every exchange takes 7 shuffles where eight sums one by one take 24.
+__device__ __forceinline__ float sum8(const float* v, int l) {
+  float x[4], y[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float mine = (l & 4) ? v[i + 4] : v[i], give = (l & 4) ? v[i] : v[i + 4];
+    x[i] = mine + __shfl_xor_sync(0xffffffffu, give, 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float mine = (l & 2) ? x[i + 2] : x[i], give = (l & 2) ? x[i] : x[i + 2];
+    y[i] = mine + __shfl_xor_sync(0xffffffffu, give, 2);
+  }
+  const float mine = (l & 1) ? y[1] : y[0], give = (l & 1) ? y[0] : y[1];
+  return mine + __shfl_xor_sync(0xffffffffu, give, 1);
+}
+
+// One segment of one prompt, kRows rows of one head's state.  STATE_ONLY: the segment's own
+// contribution to the state (from zero) and its total decay, into the workspace.
+template <typename TIO, typename TST, int DK, int DV, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
+  constexpr int CPL = DK / kLPR;         // columns per lane: four at 4 l + 32 j
+  constexpr int kSlabs = DV / kRows;
+  constexpr int kVec = kBlock * DK / 8 / kThreads;   // 8-column vectors of k (and of q) per thread
+  constexpr int kVPT = kBlock * kRows / kThreads;    // values of v per thread
+  __shared__ float s_k[kBlock][DK], s_q[STATE_ONLY ? 1 : kBlock][DK], s_v[kBlock][kRows], s_a[kBlock];
+  __shared__ float s_o[STATE_ONLY ? 1 : kBlock][kRows];
+
+  const int tid = threadIdx.x;
+  const int slab = blockIdx.x % kSlabs, h = blockIdx.x / kSlabs % a.H, g = blockIdx.x / kSlabs / a.H;
+  const bool ok = check_seqlens(a);
+  if (blockIdx.x == 0 && !STATE_ONLY)
+    for (int b = tid; b < a.B; b += kThreads) a.err[b] = ok ? 0 : TV_ERR_BAD_SEQLEN;
+  if (!ok) return;
+  const Segment seg = find_segment(a, g);
+  if (seg.b < 0 || (STATE_ONLY && seg.index + 1 == seg.count)) return;
+
+  const int hk = h / (a.H / a.Hk);
+  const TIO* kp = static_cast<const TIO*>(a.k) + hk * DK;
+  const TIO* qp = static_cast<const TIO*>(a.q) + hk * DK;
+  const TIO* vp = static_cast<const TIO*>(a.v) + h * DV + slab * kRows;
+  TIO* op = static_cast<TIO*>(a.out) + h * DV + slab * kRows;
+
+  const int l = tid % kLPR, row0 = tid / kLPR * kRPL;  // this lane's first row of the slab
+  float s[kRPL][CPL];
+  const size_t head = (size_t)seg.b * a.H + h, slot = (size_t)g * a.H + h;
+#pragma unroll
+  for (int r = 0; r < kRPL; ++r) {
+    const int at = (slab * kRows + row0 + r) * DK + 4 * l;
+#pragma unroll
+    for (int j = 0; j < CPL / 4; ++j) {
+      if (!STATE_ONLY && seg.count > 1) {
+        load_vec_rw<4>(a.slots + slot * DV * DK + at + 32 * j, s[r] + 4 * j);
+      } else if (!STATE_ONLY && a.S0 != nullptr) {
+        load_vec_rw<4>(static_cast<const TST*>(a.S0) + head * DV * DK + at + 32 * j, s[r] + 4 * j);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[r][4 * j + c] = 0.f;
+      }
+    }
+  }
+  float total = 1.f;
+
+  Raw8<TIO> rk[kVec], rq[kVec];
+  TIO rv[kVPT];
+  float ra = 1.f;
+  // Tokens past the segment's end enter as k = q = v = 0 and alpha = 1: they leave the state alone.
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int e = tid + i * kThreads, tok = t + e / (DK / 8), c = e % (DK / 8) * 8;
+      if (tok < seg.t1) {
+        rk[i].load(kp + tok * a.k_stride + c);
+        if (!STATE_ONLY) rq[i].load(qp + tok * a.q_stride + c);
+      } else {
+        rk[i].zero();
+        rq[i].zero();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kVPT; ++i) {
+      const int e = tid + i * kThreads, tok = t + e / kRows;
+      rv[i] = tok < seg.t1 ? vp[tok * a.v_stride + e % kRows] : from_f32<TIO>(0.f);
+    }
+    if (tid < kBlock) ra = t + tid < seg.t1 ? __ldg(a.alpha + (t + tid) * a.alpha_stride + h) : 1.f;
+  };
+  fetch(seg.t0);
+  for (int t = seg.t0; t < seg.t1; t += kBlock) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int e = tid + i * kThreads, tok = e / (DK / 8), c = e % (DK / 8) * 8;
+      float x[8];
+      rk[i].get(x);
+      store_vec<8>(&s_k[tok][c], x);
+      if (!STATE_ONLY) {
+        rq[i].get(x);
+        store_vec<8>(&s_q[tok][c], x);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kVPT; ++i) {
+      const int e = tid + i * kThreads;
+      s_v[e / kRows][e % kRows] = to_f32(rv[i]);
+    }
+    if (tid < kBlock) s_a[tid] = ra;
+    __syncthreads();
+    if (t + kBlock < seg.t1) fetch(t + kBlock);
+#pragma unroll
+    for (int u = 0; u < kBlock; u += 8) {
+      float dot[kRPL][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float al = s_a[u + i];
+        float v[kRPL];
+#pragma unroll
+        for (int r = 0; r < kRPL; ++r) {
+          v[r] = s_v[u + i][row0 + r];
+          dot[r][i] = 0.f;
+        }
+        if (STATE_ONLY) total *= al;
+#pragma unroll
+        for (int j = 0; j < CPL / 4; ++j) {
+          const float4 k4 = *reinterpret_cast<const float4*>(&s_k[u + i][4 * l + 32 * j]);
+          const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+          float4 q4 = make_float4(0, 0, 0, 0);
+          if (!STATE_ONLY) q4 = *reinterpret_cast<const float4*>(&s_q[u + i][4 * l + 32 * j]);
+          const float qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+          for (int r = 0; r < kRPL; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float& x = s[r][4 * j + c];
+              x = fmaf(v[r], kk[c], al * x);
+              if (!STATE_ONLY) dot[r][i] = fmaf(x, qq[c], dot[r][i]);
+            }
+        }
+      }
+      if (!STATE_ONLY)
+#pragma unroll
+        for (int r = 0; r < kRPL; ++r) s_o[u + l][row0 + r] = sum8(dot[r], l) * a.q_scale;
+    }
+    if (!STATE_ONLY) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kVPT / 4; ++i) {
+        const int e = (tid + i * kThreads) * 4, tok = t + e / kRows;
+        if (tok < seg.t1) store_vec<4>(op + tok * a.out_stride + e % kRows, &s_o[e / kRows][e % kRows]);
+      }
+    }
+  }
+  const bool last = seg.index + 1 == seg.count;
+  if (!STATE_ONLY && !last) return;
+#pragma unroll
+  for (int r = 0; r < kRPL; ++r) {
+    const int at = (slab * kRows + row0 + r) * DK + 4 * l;
+#pragma unroll
+    for (int j = 0; j < CPL / 4; ++j) {
+      if (STATE_ONLY) store_vec<4>(a.slots + slot * DV * DK + at + 32 * j, s[r] + 4 * j);
+      else store_vec<4>(static_cast<TST*>(a.S) + head * DV * DK + at + 32 * j, s[r] + 4 * j);
+    }
+  }
+  if (STATE_ONLY && slab == 0 && tid == 0) a.decay[slot] = total;
+}
+
+// ------------------------------------------------------------------ states between segments
+// Slot s of a cut prompt holds the segment's own contribution dS_s and receives the state that
+// segment s starts from: X_0 = S0, X_{s+1} = decay_s X_s + dS_s.  Four columns a thread.  S0 itself
+// is copied into slot 0, so that the last segment may write S over it while the first one runs.
+template <typename TST>
+__global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, int parts) {
+  if (!check_seqlens(a)) return;
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.H, b = blockIdx.x / parts / a.H;
+  const int n = segments_of(__ldg(a.cu + b + 1) - __ldg(a.cu + b), a.seg_len);
+  if (n == 1) return;
+  const int first = first_segment(a, b);
+  const size_t size = (size_t)a.dv * a.dk, at = ((size_t)part * 256 + threadIdx.x) * 4;
+  if (at >= size) return;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.S0 != nullptr) load_vec_rw<4>(static_cast<const TST*>(a.S0) + ((size_t)b * a.H + h) * size + at, x);
+  for (int s = 0; s < n; ++s) {
+    const size_t slot = (size_t)(first + s) * a.H + h;
+    float* p = a.slots + slot * size + at;
+    float d[4];
+    if (s + 1 < n) load_vec_rw<4>(p, d);
+    store_vec<4>(p, x);
+    if (s + 1 < n) {
+      const float f = a.decay[slot];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = fmaf(f, x[c], d[c]);
+    }
+  }
+}
+
+template <typename TIO, typename TST, int DK, int DV>
+cudaError_t prompt_simt(const LinAttnArgs& a, cudaStream_t s) {
+  const long long segments = a.seg_len > 0 ? (long long)a.B + a.T / a.seg_len : a.B;
+  const long long grid = segments * a.H * (DV / kRows);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (a.seg_len > 0) {
+    linear_attn_kernel<TIO, TST, DK, DV, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    const int parts = (DK * DV / 4 + 255) / 256;
+    linear_attn_scan_kernel<TST><<<(unsigned)(a.B * a.H * parts), 256, 0, s>>>(a, parts);
+  }
+  linear_attn_kernel<TIO, TST, DK, DV, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TIO, typename TST>
+cudaError_t prompt_dims(const LinAttnArgs& a, cudaStream_t s) {
+  if (a.dk == 64) return a.dv == 64 ? prompt_simt<TIO, TST, 64, 64>(a, s) : prompt_simt<TIO, TST, 64, 128>(a, s);
+  return a.dv == 64 ? prompt_simt<TIO, TST, 128, 64>(a, s) : prompt_simt<TIO, TST, 128, 128>(a, s);
+}
+
+// ------------------------------------------------------------------ one token
+// Eight columns a thread, DK / 8 lanes a row, NP rows a thread: a CTA updates NP * (1024 / DK) rows of
+// one head's state.  The state is read and written once, straight through registers; k and q are the
+// same for every row and come from L1 after the first.
+template <typename TIO, typename TST, int DK, int NP>
+__global__ void __launch_bounds__(kThreads) linear_attn_step_kernel(LinStepArgs a) {
+  constexpr int LPR = DK / 8, RPP = kThreads / LPR;  // lanes per row, rows per pass
+  const int slabs = a.dv / (RPP * NP);
+  const int slab = blockIdx.x % slabs, h = blockIdx.x / slabs % a.H, b = blockIdx.x / slabs / a.H;
+  if (a.live != nullptr && __ldg(a.live + b) == 0) return;
+  const int l = threadIdx.x % LPR, row0 = slab * RPP * NP + threadIdx.x / LPR;
+  const int hk = h / (a.H / a.Hk);
+  TST* sp = static_cast<TST*>(a.S) + (((size_t)b * a.H + h) * a.dv + row0) * DK + 8 * l;
+  const TIO* vp = static_cast<const TIO*>(a.v) + b * a.v_stride + h * a.dv + row0;
+  float s[NP][8], v[NP], k[8], q[8];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) load_vec_rw<8>(sp + p * RPP * DK, s[p]);
+  load_vec<8>(static_cast<const TIO*>(a.k) + b * a.k_stride + hk * DK + 8 * l, k);
+  load_vec<8>(static_cast<const TIO*>(a.q) + b * a.q_stride + hk * DK + 8 * l, q);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) v[p] = to_f32(vp[p * RPP]);
+  const float al = __ldg(a.alpha + b * a.alpha_stride + h);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    float dot = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      s[p][c] = fmaf(v[p], k[c], al * s[p][c]);
+      dot = fmaf(s[p][c], q[c], dot);
+    }
+    store_vec<8>(sp + p * RPP * DK, s[p]);
+    dot = group_sum<LPR>(dot) * a.q_scale;
+    if (l == 0)
+      static_cast<TIO*>(a.out)[b * a.out_stride + h * a.dv + row0 + p * RPP] = from_f32<TIO>(dot);
+  }
+}
+
+template <typename TIO, typename TST, int DK>
+cudaError_t step_rows(const LinStepArgs& a, cudaStream_t s) {
+  constexpr int RPP = kThreads * 8 / DK;
+  constexpr int NP = 4;
+  const long long grid = (long long)a.B * a.H * (a.dv / (RPP * NP));
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  linear_attn_step_kernel<TIO, TST, DK, NP><<<(unsigned)grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename TIO, typename TST>
+cudaError_t step_dims(const LinStepArgs& a, cudaStream_t s) {
+  return a.dk == 64 ? step_rows<TIO, TST, 64>(a, s) : step_rows<TIO, TST, 128>(a, s);
+}
+
+}  // namespace
+
+int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io) {
+  (void)B; (void)dk; (void)io;
+  const long long ctas = 4LL * device_sm_count();
+  long long seg = ((long long)T * H * (dv / kRows) + ctas - 1) / ctas;
+  seg = (seg + 127) / 128 * 128;
+  return max_len > 3 * seg ? (int)seg : 0;
+}
+
+size_t linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int dv, int io) {
+  if (max_len > T) max_len = T;
+  const int seg = linear_attn_segment(B, T, max_len, H, dk, dv, io);
+  if (seg == 0) return 0;
+  const size_t segments = (size_t)B + T / seg;
+  return segments * H * ((size_t)dv * dk + 4) * sizeof(float);
+}
+
+cudaError_t launch_linear_attn_prompt(const LinAttnArgs& a, cudaStream_t s) {
+  if (a.io == TV_F32) return prompt_dims<float, float>(a, s);
+  return a.state == TV_BF16 ? prompt_dims<bf16, bf16>(a, s) : prompt_dims<bf16, float>(a, s);
+}
+
+cudaError_t launch_linear_attn_step(const LinStepArgs& a, cudaStream_t s) {
+  if (a.io == TV_F32) return step_dims<float, float>(a, s);
+  return a.state == TV_BF16 ? step_dims<bf16, bf16>(a, s) : step_dims<bf16, float>(a, s);
+}
+
+}  // namespace tv

@@ -76,6 +76,7 @@ const char* tv_status_string(int status) {
     case TV_ERR_TIMEOUT: return "device wait timed out";
     case TV_ERR_CAPACITY: return "block table too short for prefix_len + N slots";
     case TV_ERR_BAD_BLOCK: return "block-table entry outside the cache";
+    case TV_ERR_BAD_SEQLEN: return "cu_seqlens decreases, leaves [0, T] or holds a prompt longer than max_len";
     case TV_ERR_SCRATCH: return "request needs more than the static scratch of TV_STATIC_SCRATCH_BYTES";
     default: return "unknown status";
   }
@@ -360,6 +361,132 @@ int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, const in
   if (N > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
   tv::AcceptArgs a{parents, draft_tokens, target_tokens, B, N, Lmax, accepted_path, accepted_len, next_token, err};
   return cuda_status(tv::launch_accept_walk(a, stream));
+}
+
+size_t tv_linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int dv, int io_dtype) {
+  if (B < 1 || T < 0 || max_len < 0 || H < 1 || !dim_ok(dk) || !dim_ok(dv)) return 0;
+  return tv::linear_attn_workspace_size(B, T, max_len, H, dk, dv, io_dtype);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Types, sizes and the token strides shared by the prompt and the single-token call.
+int linear_attn_common(int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t alpha_stride, int64_t out_stride,
+                       int Hk, int H, int dk, int dv, int io, int state, float q_scale) {
+  if (Hk < 1 || H < 1 || H % Hk || !isfinite(q_scale)) return TV_ERR_INVALID_ARG;
+  if (!dim_ok(dk) || !dim_ok(dv)) return TV_ERR_UNSUPPORTED;
+  const int st = gdn_dtypes(io, state);
+  if (st != TV_OK) return st;
+  const int64_t per16 = io == TV_BF16 ? 8 : 4, qk = (int64_t)Hk * dk, vo = (int64_t)H * dv;
+  if (q_stride < qk || k_stride < qk || v_stride < vo || out_stride < vo || q_stride % per16 || k_stride % per16 ||
+      v_stride % per16 || out_stride % per16 || (alpha_stride != 0 && alpha_stride < H))
+    return TV_ERR_INVALID_ARG;
+  return TV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tv_linear_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const float* alpha, int64_t alpha_stride, const void* S0,
+                          const int32_t* cu_seqlens, int B, int T, int max_len, int Hk, int H, int dk, int dv,
+                          int io_dtype, int state_dtype, float q_scale, void* out, int64_t out_stride, void* S,
+                          void* workspace, size_t workspace_bytes, int32_t* err, tv_stream_t stream) {
+  // With no token at all (T = 0) the token tensors may be null.
+  if (T > 0 && (!a16(q) || !a16(k) || !a16(v) || !a4(alpha) || !a16(out))) return TV_ERR_INVALID_ARG;
+  if ((S0 != nullptr && !a16(S0)) || !a16(S) || !a4(cu_seqlens) || !a4(err) || B < 1 || T < 0 || max_len < 0)
+    return TV_ERR_INVALID_ARG;
+  const int st = linear_attn_common(q_stride, k_stride, v_stride, alpha_stride, out_stride, Hk, H, dk, dv, io_dtype,
+                                    state_dtype, q_scale);
+  if (st != TV_OK) return st;
+  if ((long long)B * H > (1 << 24)) return TV_ERR_UNSUPPORTED;
+  if (max_len > T) max_len = T;
+  const size_t need = tv::linear_attn_workspace_size(B, T, max_len, H, dk, dv, io_dtype);
+  if (need > 0 && (!a16(workspace) || workspace_bytes < need)) return TV_ERR_INVALID_ARG;
+  tv::LinAttnArgs a{q, k, v, q_stride, k_stride, v_stride, alpha, alpha_stride, S0, cu_seqlens,
+                    B, T, max_len, Hk, H, dk, dv, io_dtype, state_dtype, q_scale, out, out_stride, S, err,
+                    0, nullptr, nullptr};
+  if (need > 0) {
+    a.seg_len = tv::linear_attn_segment(B, T, max_len, H, dk, dv, io_dtype);
+    const size_t segments = (size_t)B + T / a.seg_len;
+    a.slots = static_cast<float*>(workspace);
+    a.decay = a.slots + segments * H * dv * dk;
+  }
+  return cuda_status(tv::launch_linear_attn_prompt(a, stream));
+}
+
+int tv_linear_attn_step(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const float* alpha, int64_t alpha_stride, const int32_t* live, int B, int Hk,
+                        int H, int dk, int dv, int io_dtype, int state_dtype, float q_scale, void* out,
+                        int64_t out_stride, void* S, tv_stream_t stream) {
+  if (!a16(q) || !a16(k) || !a16(v) || !a4(alpha) || !a16(out) || !a16(S) || (live != nullptr && !a4(live)) || B < 1)
+    return TV_ERR_INVALID_ARG;
+  const int st = linear_attn_common(q_stride, k_stride, v_stride, alpha_stride, out_stride, Hk, H, dk, dv, io_dtype,
+                                    state_dtype, q_scale);
+  if (st != TV_OK) return st;
+  if ((long long)B * H > (1 << 24)) return TV_ERR_UNSUPPORTED;
+  tv::LinStepArgs a{q, k, v, q_stride, k_stride, v_stride, alpha, alpha_stride, live, B, Hk, H, dk, dv,
+                    io_dtype, state_dtype, q_scale, out, out_stride, S};
+  return cuda_status(tv::launch_linear_attn_step(a, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kNormMax = 32768;  // widest row: 1024 threads of four 8-column vectors
+
+bool el(const void* p, int dtype) {  // aligned to its element
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype == TV_F32 ? 3u : 1u)) == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tv_gated_rmsnorm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, const void* weight,
+                     int rows, int H, int d, int io_dtype, float eps, float weight_offset, int gate_first, void* out,
+                     int64_t out_stride, tv_stream_t stream) {
+  if (io_dtype != TV_F32 && io_dtype != TV_BF16) return TV_ERR_INVALID_ARG;
+  if (rows < 0 || H < 1 || d < 1 || !(eps >= 0.f) || !isfinite(eps) || !isfinite(weight_offset) || gate_first < 0 ||
+      gate_first > 1)
+    return TV_ERR_INVALID_ARG;
+  if (d > kNormMax || (long long)rows * H > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if (rows == 0) return TV_OK;
+  const int64_t row = (int64_t)H * d;
+  if (!el(x, io_dtype) || !el(out, io_dtype) || (gate != nullptr && !el(gate, io_dtype)) ||
+      (weight != nullptr && !el(weight, io_dtype)) || x_stride < row || out_stride < row ||
+      (gate != nullptr && gate_stride < row))
+    return TV_ERR_INVALID_ARG;
+  tv::GatedNormArgs a{x, gate, weight, out, x_stride, gate_stride, out_stride, rows, H, d, io_dtype, eps,
+                      weight_offset, gate_first};
+  return cuda_status(tv::launch_gated_rmsnorm(a, stream));
+}
+
+int tv_residual_rmsnorm(const void* y, int64_t y_stride, const void* residual, int64_t residual_stride,
+                        const void* post_weight, const void* gate, int64_t gate_stride, float scale,
+                        const void* weight, int rows, int D, int io_dtype, int residual_dtype, float eps,
+                        float weight_offset, void* residual_out, int64_t residual_out_stride, void* out,
+                        int64_t out_stride, tv_stream_t stream) {
+  const int st = gdn_dtypes(io_dtype, residual_dtype);
+  if (st != TV_OK) return st;
+  if (rows < 0 || D < 1 || !(eps >= 0.f) || !isfinite(eps) || !isfinite(weight_offset) || !isfinite(scale))
+    return TV_ERR_INVALID_ARG;
+  if (D > kNormMax) return TV_ERR_UNSUPPORTED;
+  if (rows == 0) return TV_OK;
+  if (!el(y, io_dtype) || !el(residual, residual_dtype) || !el(residual_out, residual_dtype) ||
+      (post_weight != nullptr && !el(post_weight, io_dtype)) || (gate != nullptr && !el(gate, io_dtype)) ||
+      (weight != nullptr && !el(weight, io_dtype)) || (out != nullptr && !el(out, io_dtype)) || y_stride < D ||
+      residual_stride < D || residual_out_stride < D || (gate != nullptr && gate_stride < D) ||
+      (out != nullptr && out_stride < D))
+    return TV_ERR_INVALID_ARG;
+  tv::ResidualNormArgs a{y, residual, post_weight, gate, weight, residual_out, out, y_stride, residual_stride,
+                         gate_stride, residual_out_stride, out_stride, rows, D, io_dtype, residual_dtype, scale, eps,
+                         weight_offset};
+  return cuda_status(tv::launch_residual_rmsnorm(a, stream));
 }
 
 }  // extern "C"

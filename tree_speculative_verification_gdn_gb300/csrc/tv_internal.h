@@ -168,4 +168,72 @@ struct AcceptArgs {
 };
 cudaError_t launch_accept_walk(const AcceptArgs& a, cudaStream_t s);
 
+// Linear attention with a decay.  Strides are in elements, per token.
+struct LinAttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const float* alpha;
+  long long alpha_stride;  // 0: one decay per head
+  const void* S0;          // nullptr: zero
+  const int32_t* cu;       // [B + 1]
+  int B, T, max_len, Hk, H, dk, dv, io, state;
+  float q_scale;
+  void* out;
+  long long out_stride;
+  void* S;
+  int32_t* err;
+  // Prompts longer than seg_len are cut into segments of that many tokens that run side by side
+  // (0: no prompt is cut).  slots [segments, H, dv, dk] fp32 holds each segment's own contribution
+  // to the state, then the state it starts from; decay [segments, H] its total decay.
+  int seg_len;
+  float* slots;
+  float* decay;
+};
+// Segment length for these sizes, 0 for none; host-only.
+int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io);
+size_t linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int dv, int io);
+cudaError_t launch_linear_attn_prompt(const LinAttnArgs& a, cudaStream_t s);
+struct LinStepArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const float* alpha;
+  long long alpha_stride;
+  const int32_t* live;
+  int B, Hk, H, dk, dv, io, state;
+  float q_scale;
+  void* out;
+  long long out_stride;
+  void* S;
+};
+cudaError_t launch_linear_attn_step(const LinStepArgs& a, cudaStream_t s);
+
+struct GatedNormArgs {
+  const void* x;
+  const void* gate;
+  const void* weight;
+  void* out;
+  long long x_stride, gate_stride, out_stride;
+  int rows, H, d, io;
+  float eps, weight_offset;
+  int gate_first;
+};
+cudaError_t launch_gated_rmsnorm(const GatedNormArgs& a, cudaStream_t s);
+struct ResidualNormArgs {
+  const void* y;
+  const void* residual;
+  const void* post_weight;
+  const void* gate;
+  const void* weight;
+  void* residual_out;
+  void* out;
+  long long y_stride, residual_stride, gate_stride, residual_out_stride, out_stride;
+  int rows, D, io, res;
+  float scale, eps, weight_offset;
+};
+cudaError_t launch_residual_rmsnorm(const ResidualNormArgs& a, cudaStream_t s);
+
 }  // namespace tv
