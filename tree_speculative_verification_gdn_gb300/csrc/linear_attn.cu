@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
   const int tid = threadIdx.x;
   const int slab = blockIdx.x % kSlabs, h = blockIdx.x / kSlabs % a.H, g = blockIdx.x / kSlabs / a.H;
   const bool ok = check_seqlens(a);
-  if (blockIdx.x == 0 && !STATE_ONLY)
+  if (blockIdx.x == 0 && (STATE_ONLY || a.seg_len == 0))
     for (int b = tid; b < a.B; b += kThreads) a.err[b] = ok ? 0 : TV_ERR_BAD_SEQLEN;
   if (!ok) return;
   const Segment seg = find_segment(a, g);
@@ -242,8 +242,8 @@ cudaError_t prompt_simt(const LinAttnArgs& a, cudaStream_t s) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (a.seg_len > 0) {
     linear_attn_kernel<TIO, TST, DK, DV, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    const int parts = (DK * DV / 4 + 255) / 256;
-    linear_attn_scan_kernel<TST><<<(unsigned)(a.B * a.H * parts), 256, 0, s>>>(a, parts);
+    const cudaError_t e = launch_linear_attn_scan(a, s);
+    if (e != cudaSuccess) return e;
   }
   linear_attn_kernel<TIO, TST, DK, DV, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
@@ -309,9 +309,17 @@ cudaError_t step_dims(const LinStepArgs& a, cudaStream_t s) {
 }  // namespace
 
 int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io) {
-  (void)B; (void)dk; (void)io;
-  const long long ctas = 4LL * device_sm_count();
-  long long seg = ((long long)T * H * (dv / kRows) + ctas - 1) / ctas;
+  (void)B; (void)dk;
+  const int sms = device_sm_count();
+  if (io == TV_BF16) {
+    // One CTA per SM walks whole (segment, head) units: cut when the longest prompt alone takes over
+    // twice the balanced time, into as many pieces as make two rounds of units.
+    if ((long long)max_len * sms <= 2LL * T * H) return 0;
+    const int pieces = 2 * sms / H > 1 ? 2 * sms / H : 1;
+    const int seg = ((T + pieces - 1) / pieces + 127) / 128 * 128;
+    return max_len > seg ? seg : 0;
+  }
+  long long seg = ((long long)T * H * (dv / kRows) + 4 * sms - 1) / (4 * sms);
   seg = (seg + 127) / 128 * 128;
   return max_len > 3 * seg ? (int)seg : 0;
 }
@@ -324,7 +332,17 @@ size_t linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int 
   return segments * H * ((size_t)dv * dk + 4) * sizeof(float);
 }
 
+cudaError_t launch_linear_attn_scan(const LinAttnArgs& a, cudaStream_t s) {
+  const int parts = (a.dk * a.dv / 4 + 255) / 256;
+  const long long grid = (long long)a.B * a.H * parts;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (a.state == TV_BF16) linear_attn_scan_kernel<bf16><<<(unsigned)grid, 256, 0, s>>>(a, parts);
+  else linear_attn_scan_kernel<float><<<(unsigned)grid, 256, 0, s>>>(a, parts);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_linear_attn_prompt(const LinAttnArgs& a, cudaStream_t s) {
+  if (a.io == TV_BF16 && a.T > 0) return launch_linear_attn_tc(a, s);
   if (a.io == TV_F32) return prompt_dims<float, float>(a, s);
   return a.state == TV_BF16 ? prompt_dims<bf16, bf16>(a, s) : prompt_dims<bf16, float>(a, s);
 }

@@ -195,6 +195,9 @@ struct LinAttnArgs {
 int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io);
 size_t linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int dv, int io);
 cudaError_t launch_linear_attn_prompt(const LinAttnArgs& a, cudaStream_t s);
+// The tensor-core form (bf16 I/O, T > 0); the scan between its passes is linear_attn.cu's.
+cudaError_t launch_linear_attn_tc(const LinAttnArgs& a, cudaStream_t s);
+cudaError_t launch_linear_attn_scan(const LinAttnArgs& a, cudaStream_t s);
 struct LinStepArgs {
   const void* q;
   const void* k;
