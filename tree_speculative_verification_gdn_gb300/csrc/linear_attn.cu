@@ -70,15 +70,15 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
   __shared__ float s_o[STATE_ONLY ? 1 : kBlock][kRows];
 
   const int tid = threadIdx.x;
-  const int slab = blockIdx.x % kSlabs, h = blockIdx.x / kSlabs % a.H, g = blockIdx.x / kSlabs / a.H;
+  const int slab = blockIdx.x % kSlabs, u = blockIdx.x / kSlabs;
   const bool ok = check_seqlens(a);
   if (blockIdx.x == 0 && (STATE_ONLY || a.seg_len == 0))
     for (int b = tid; b < a.B; b += kThreads) a.err[b] = ok ? 0 : TV_ERR_BAD_SEQLEN;
   if (!ok) return;
-  const Segment seg = find_segment(a, g);
+  const Segment seg = find_segment(a, u);
   if (seg.b < 0 || (STATE_ONLY && seg.index + 1 == seg.count)) return;
 
-  const int hk = h / (a.H / a.Hk);
+  const int h = seg.h, hk = h / (a.H / a.Hk);
   const TIO* kp = static_cast<const TIO*>(a.k) + hk * DK;
   const TIO* qp = static_cast<const TIO*>(a.q) + hk * DK;
   const TIO* vp = static_cast<const TIO*>(a.v) + h * DV + slab * kRows;
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
 
   const int l = tid % kLPR, row0 = tid / kLPR * kRPL;  // this lane's first row of the slab
   float s[kRPL][CPL];
-  const size_t head = (size_t)seg.b * a.H + h, slot = (size_t)g * a.H + h;
+  const size_t head = (size_t)seg.b * a.H + h, slot = u;
 #pragma unroll
   for (int r = 0; r < kRPL; ++r) {
     const int at = (slab * kRows + row0 + r) * DK + 4 * l;

@@ -21,6 +21,7 @@ __device__ __forceinline__ bool check_seqlens(const LinAttnArgs& a) {
 
 struct Segment {
   int b;        // prompt; -1: no such segment
+  int h;        // value head
   int index;    // segment of the prompt
   int count;    // segments of the prompt
   int t0, t1;   // its tokens
@@ -30,11 +31,13 @@ __device__ __forceinline__ int segments_of(int len, int seg_len) {
   return seg_len > 0 && len > seg_len ? (len + seg_len - 1) / seg_len : 1;
 }
 
-// Segment number g over all prompts.  Executed by a whole warp, the same answer in every lane;
-// cu_seqlens has passed check_seqlens.
-__device__ __forceinline__ Segment find_segment(const LinAttnArgs& a, int g) {
+// Unit u is head u % H of segment u / H, segments counted over all prompts.  Executed by a whole warp,
+// the same answer in every lane; cu_seqlens has passed check_seqlens.
+static __device__ __noinline__ Segment find_segment(const LinAttnArgs& a, int u) {
+  const int g = u / a.H;
   Segment s;
   s.b = -1;
+  s.h = u - g * a.H;
   if (a.seg_len == 0) {
     if (g < a.B) {
       s.b = g;

@@ -5,23 +5,30 @@
 // state before the chunk (dv x dk):
 //     P_ij = 2^(g_i - g_j) q_scale q_i.k_j  (j <= i),       O = P V + diag(2^g q_scale) Q S^T,
 //     S   <- 2^g_C S + V^T K',                              k'_j = 2^(g_C - g_j) k_j.
-// Four products a chunk, all C x 128 x 128, operands in shared memory as TMA lays them (128-byte
-// swizzle), accumulators and the state in the 512 columns of tensor memory:
-//     QK: scores [token i, token j]      A = Q, B = K
-//     QS: O_inter [token i, value]       A = Q, B = S          (bf16 pair)
-//     ST: S [value, key column]          A = V^T, B = K'       (bf16 pair), added to the state
-//     PV: O_intra [token i, value]       A = P (bf16 pair, tensor memory, over the scores), B = V
+// Four products a chunk, all C x 128 x 128.  Q, K and V lie in shared memory as TMA lays them (128-byte
+// swizzle); accumulators, the state's transpose, P and K' fill the 512 columns of tensor memory:
+//     QK: scores [token i, token j]      A = Q,    B = K
+//     QS: O [token i, value]             A = Q,    B = S^T     (bf16 pair); its rows then scaled in place
+//     ST: S^T [key column, value]        A = K'^T, B = V       (bf16 pair, tensor memory), added to the state
+//     PV: O, added to                    A = P,    B = V       (bf16 pair, tensor memory, over the scores)
 // P, K' and S are fp32 results and enter as value + remainder, two bf16 each (2^-16 left out): one
 // bf16 alone would put an error as large as the output's own rounding on every output, and 2^-9 on
 // an fp32 state.  Exponents only ever go down: within 32 x 32 diagonal blocks each 2^(g_i - g_j) is
 // taken directly, elsewhere as 2^(g_i - g_r) 2^(g_r - g_j) with r the first row of i's block, so no
-// factor exceeds 1 however fast the decay.  g is summed in 64 bits and kept as two floats: after a
-// reset (alpha near 0) small differences of large sums remain.
+// factor exceeds 1 however fast the decay.  g is summed and kept as two floats: after a reset (alpha
+// near 0) small differences of large sums remain.
 //
-// Twelve warps: four turn scores into P and write outputs (thread = token), four own the state
-// (thread = value row) and scale the keys, one issues TMA loads, one the MMAs, one sums the decays.
-// A ring of whole tiles (Q, K, V, Q, ...) feeds them; every tile is given back by the MMA that reads
-// it last.  One CTA per SM, since the state, its bf16 pair and four 32 KB tiles fill shared memory.
+// An MMA of this shape reads shared memory at the rate shared memory has (8 KB per 64 clocks), so it,
+// not the tensor pipe, is what the products share with TMA and the state's conversion: that is why P
+// and K' go through tensor memory (K transposed on the way by ldmatrix) and only S through shared
+// memory.
+//
+// Nineteen warps: four turn scores into P (thread = token), four scale and write outputs (thread =
+// token), four own the state (thread = key column), four scale the keys; one issues TMA loads, one the
+// MMAs, one sums the decays.  A ring of whole tiles (Q, K, V, Q, ...) feeds them; every tile is given
+// back by the MMA that reads it last.  One CTA per SM, since five 32 KB tiles and the state's bf16 pair
+// fill shared memory.  A chunk runs every role's code once, and together it has to stay in the
+// instruction cache: hence loops that are not unrolled and waits that are not inlined.
 #include "linear_attn.cuh"
 #include "tv_async.cuh"
 #include "tv_tc.cuh"
@@ -30,22 +37,24 @@
 namespace tv {
 namespace {
 
-constexpr int kC = 128;         // tokens per chunk
-constexpr int kThreads = 352;   // 4 + 4 warps, TMA, MMA and decay warps
-constexpr int kHalf = kC * 128; // bytes of 64 columns of a 128-token tile
+constexpr int kC = 128;          // tokens per chunk
+constexpr int kThreads = 608;    // four roles of four warps, and the TMA, MMA and decay warps
+constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 6;
 
 // TMEM columns
-constexpr uint32_t kColQK = 0, kColS = 128, kColIntra = 256, kColInter = 384;
+constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 
 struct Shared {
-  float2 g[2][kC];            // g_i as two floats, by chunk parity
-  float f[192];               // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
+  float2 g[2][kC];  // g_i as two floats, by chunk parity
+  float f[192];     // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t g_full[2], g_empty[2];
-  uint64_t qk_done, s_ready, k_ready, p_ready, st_done, o_done, o_free, drain;
+  uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
+  uint64_t s_ready, k_ready, p_ready, o_ready, o_free;  // operands written, outputs read
+  uint64_t drain;
   uint32_t tmem;
   int fail;
 };
@@ -53,13 +62,37 @@ struct Shared {
 template <int DK, int DV, bool STATE_ONLY>
 struct Plan {
   static constexpr int slot = kC * 2 * (DK > DV ? DK : DV);
-  static constexpr int lo = kC * 2 * DK;                    // remainders of K'
-  static constexpr int s = STATE_ONLY ? 0 : DV * DK * 2;    // the state's bf16 values; as much for its remainders
-  static constexpr int room = kSmemMax - lo - 2 * s - (int)sizeof(Shared);
+  static constexpr int s = STATE_ONLY ? 0 : DV * DK * 2;  // the state's bf16 values; as much for its remainders
+  static constexpr int room = kSmemMax - 2 * s - (int)sizeof(Shared);
   static constexpr int slots = room / slot < kMaxSlots ? room / slot : kMaxSlots;
-  static constexpr int bytes = slots * slot + lo + 2 * s + (int)sizeof(Shared);
-  static_assert(slots >= 3, "a chunk's tiles fit");
+  static constexpr int bytes = slots * slot + 2 * s + (int)sizeof(Shared);
+  static_assert(slots >= 5, "a chunk's tiles and the next one's first two fit");
 };
+
+// Place of a tile in the ring: its slot, and the parity of the slot's use.
+template <int SLOTS>
+struct Place {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ Place next(int tiles) const {  // tiles <= SLOTS
+    Place p{slot + tiles, parity};
+    if (p.slot >= SLOTS) {
+      p.slot -= SLOTS;
+      p.parity ^= 1;
+    }
+    return p;
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
 
 __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
@@ -72,23 +105,22 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Waits for the phase of that parity; false once this or another warp has given up.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-  for (uint32_t it = 0; it < kPolls; ++it) {
-    if (try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(&sh.fail)) return false;
+// Waits for the phase of that parity; false once this or another warp has given up.  Executed by a
+// whole warp, one answer for all of it.
+__device__ __noinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t it = 0; it < kPolls && !ok; ++it) {
+    ok = try_wait(bar, parity);
+    if (!ok && *reinterpret_cast<volatile int*>(&sh.fail)) break;
   }
-  *reinterpret_cast<volatile int*>(&sh.fail) = 1;
-  return false;
-}
-
-// The same for a whole warp, one answer for all of it.
-__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity) {
-  const bool ok = wait(sh, bar, parity);
+  if (!ok) *reinterpret_cast<volatile int*>(&sh.fail) = 1;
   return __all_sync(0xffffffffu, ok);
 }
+// The library's wait, out of line: for the paths after a wait gave up.
+__device__ __noinline__ void wait_out(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity); }
 
-// 32 columns of this thread's lane; tmem_join() before their first use.
+// 32 columns of this thread's lane; tmem_wait_ld() and tmem_join() before their first use.
 __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
   tmem_ld16_nowait(at, r);
   tmem_ld16_nowait(at + 16, r + 16);
@@ -98,7 +130,12 @@ __device__ __forceinline__ void tmem_join(uint32_t* r) {
 #pragma unroll
   for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
 }
-// 16 columns, without the wait.
+// 8 and 16 columns, without the wait.
+__device__ __forceinline__ void tmem_st8_nowait(uint32_t at, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16_nowait(uint32_t at, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
@@ -106,17 +143,58 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t at, const uint32_t* v)
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// 16 lanes x 32 columns: register 4 i + 2 y + x of lane l holds lane 8 x + l / 4, column 8 i + 4 y + l % 4
+// -- what transposing 8 x 8 loads of shared memory leave, two 16-bit rows a register.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t at, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// x as value and remainder, two columns a word.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x0, x1);
-  lo = pack_bf16x2(x0 - bf16lo(hi), x1 - bf16hi(hi));
+// Four 8 x 8 tiles of 16-bit values, transposed; lane l gives the address of row l % 8 of tile l / 8.
+__device__ __forceinline__ void ldsm4t(uint32_t at, uint32_t* v) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(at)
+               : "memory");
 }
 
-__device__ __forceinline__ float exp2_gap(float2 a, float2 b) { return exp2f((a.x - b.x) + (a.y - b.y)); }
+// Words of two bf16 to global memory, 16 columns: one 32-byte store where rows are so aligned (a
+// thread writes its own row, and whole sectors halve the lines that a warp's store touches).
+__device__ __forceinline__ void store16(bf16* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 
-constexpr uint32_t kIdescAMn = 1u << 15;  // A with its M dimension contiguous
+__device__ __forceinline__ float2 pair_of(const uint32_t* s) {
+  return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+// x as value and remainder, two columns a word.
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  const float2 rest = __ffma2_rn(make_float2(bf16lo(hi), bf16hi(hi)), make_float2(-1.f, -1.f), x);
+  lo = pack_bf16x2(rest.x, rest.y);
+}
+
+// Sums of two floats: hi + lo with |lo| at most half a step of hi.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return make_float2(s, (a - (s - t)) + (b - t));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  const float2 s = two_sum(a.x, b.x);
+  const float e = s.y + (a.y + b.y), hi = s.x + e;
+  return make_float2(hi, e - (hi - s.x));
+}
+__device__ __forceinline__ float exp2_gap(float2 a, float2 b) { return ex2_approx((a.x - b.x) + (a.y - b.y)); }
 
 template <int DK, int DV, typename TST, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -126,8 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTiles = STATE_ONLY ? 2 : 3;  // tiles per chunk: (Q,) K, V
   constexpr int kK = kTiles - 2, kV = kTiles - 1;
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* s_lo = smem + L::slots * L::slot;
-  unsigned char* s_hi = s_lo + L::lo;  // state values, then their remainders
+  unsigned char* s_hi = smem + L::slots * L::slot;  // the state's values, then their remainders
   Shared& sh = *reinterpret_cast<Shared*>(s_hi + 2 * L::s);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
@@ -143,379 +220,519 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.g_full[i], 1);
-      mbar_init(&sh.g_empty[i], STATE_ONLY ? 4 : 8);
+      mbar_init(&sh.g_empty[i], STATE_ONLY ? 8 : 16);
     }
     mbar_init(&sh.qk_done, 1);
+    mbar_init(&sh.qs_done, 1);
+    mbar_init(&sh.st_done, 1);
+    mbar_init(&sh.o_done, 1);
     mbar_init(&sh.s_ready, 128);
     mbar_init(&sh.k_ready, 128);
     mbar_init(&sh.p_ready, 128);
-    mbar_init(&sh.st_done, 1);
-    mbar_init(&sh.o_done, 1);
+    mbar_init(&sh.o_ready, 128);
     mbar_init(&sh.o_free, 128);
     mbar_init(&sh.drain, 1);
     sh.fail = 0;
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(&sh.tmem, 512);
+  if (warp == 17) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  const uint32_t quad = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // the lanes this warp may touch
 
-  // Every role walks the same units and chunks; n counts chunks over all units, m tiles.
+  // Every role walks the same units and chunks; n counts chunks over all units.
   int n = 0;
+  Place<L::slots> at;  // of the chunk's first tile
   bool good = true;
   if (warp < 4) {
-    // ------------------------------------------------ scores to P, outputs (thread = token)
+    // ------------------------------------------------ scores to P (thread = token)
     if constexpr (!STATE_ONLY) {
-      const uint32_t row = tmem + ((uint32_t)(32 * warp) << 16);
+      const uint32_t qk = quad + kColQK;
       float* f = sh.f + (warp == 2 ? 32 : warp == 3 ? 96 : 0);  // 32 * warp entries
+#pragma unroll 1
       for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
-        const Segment seg = find_segment(a, u / a.H);
+        const Segment seg = find_segment(a, u);
         if (seg.b < 0) break;
-        bf16* out = static_cast<bf16*>(a.out) + (long long)(u % a.H) * DV;
+#pragma unroll 1
         for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
           const float2* g = sh.g[n & 1];
-          if (!(good = wait_warp(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+          if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
           const float2 gi = g[tid], gr = g[32 * warp];
-          const float into = exp2f(gi.x + gi.y) * a.q_scale;  // of the state before the chunk
           const float ei = exp2_gap(gi, gr) * a.q_scale;
           __syncwarp();  // the last chunk's readers of f are done
+#pragma unroll 1
           for (int p = 0; p < warp; ++p) f[lane + 32 * p] = exp2_gap(gr, g[lane + 32 * p]);
           __syncwarp();
-          if (!(good = wait_warp(sh, &sh.qk_done, n & 1))) break;
+          if (!(good = wait(sh, &sh.qk_done, n & 1))) break;
           tc_fence_after();
-          // P of columns 32 p .. + 31: values to columns 16 p, remainders to 64 + 16 p, over scores
-          // already read; remainders wait in registers for that.
-          uint32_t lo[4][16];
+          // P of tokens 16 p .. + 15 takes the columns of its own scores, values in the first 8, their
+          // remainders in the other 8.
+          uint32_t s[16];
+          tmem_ld16_nowait(qk, s);
+#pragma unroll 1
+          for (int p = 0; p < 8; ++p) {
+            uint32_t hi[8], lo[8];
+            const int far = 16 * p - 32 * warp;  // columns of these tokens past the warp's first row
+            if (far >= 32) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint32_t s[32], hi[16];
-            if (p > warp) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) hi[c] = lo[p][c] = 0;
+              for (int c = 0; c < 8; ++c) hi[c] = lo[c] = 0;
             } else {
-              tmem_ld32(row + kColQK + 32 * p, s);
               tmem_wait_ld();
-              tmem_join<32>(s);
-              float x[32];
-              if (p < warp) {
+              tmem_join<16>(s);
+              if (far < 0) {
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                  const float4 fj = *reinterpret_cast<const float4*>(f + 32 * p + c);
-                  x[c] = __uint_as_float(s[c]) * fj.x * ei;
-                  x[c + 1] = __uint_as_float(s[c + 1]) * fj.y * ei;
-                  x[c + 2] = __uint_as_float(s[c + 2]) * fj.z * ei;
-                  x[c + 3] = __uint_as_float(s[c + 3]) * fj.w * ei;
+                for (int c = 0; c < 8; ++c) {
+                  const float2 x = __fmul2_rn(pair_of(s + 2 * c), *reinterpret_cast<const float2*>(f + 16 * p + 2 * c));
+                  split2(__fmul2_rn(x, make_float2(ei, ei)), hi[c], lo[c]);
                 }
               } else {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  const float e = exp2_gap(gi, g[32 * p + c]) * a.q_scale;
-                  x[c] = c <= lane ? __uint_as_float(s[c]) * e : 0.f;
+                for (int c = 0; c < 8; ++c) {
+                  const float4 gj = *reinterpret_cast<const float4*>(g + 16 * p + 2 * c);
+                  const float e0 = exp2_gap(gi, make_float2(gj.x, gj.y)), e1 = exp2_gap(gi, make_float2(gj.z, gj.w));
+                  const float x0 = __uint_as_float(s[2 * c]) * (e0 * a.q_scale);
+                  const float x1 = __uint_as_float(s[2 * c + 1]) * (e1 * a.q_scale);
+                  split2(make_float2(2 * c <= lane - far ? x0 : 0.f, 2 * c < lane - far ? x1 : 0.f), hi[c], lo[c]);
                 }
               }
-#pragma unroll
-              for (int c = 0; c < 16; ++c) split2(x[2 * c], x[2 * c + 1], hi[c], lo[p][c]);
+              if (far < 16) tmem_ld16_nowait(qk + 16 * p + 16, s);
             }
-            tmem_st16_nowait(row + kColQK + 16 * p, hi);
+            tmem_st8_nowait(qk + 16 * p, hi);
+            tmem_st8_nowait(qk + 16 * p + 8, lo);
           }
-#pragma unroll
-          for (int p = 0; p < 4; ++p) tmem_st16_nowait(row + kColQK + 64 + 16 * p, lo[p]);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&sh.p_ready);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
-          if (!(good = wait_warp(sh, &sh.o_done, n & 1))) break;
-          tc_fence_after();
-          bf16* o = out + (t + tid) * a.out_stride;
-#pragma unroll
-          for (int c = 0; c < DV; c += 32) {
-            uint32_t x[32], y[32];
-            tmem_ld32(row + kColInter + c, x);
-            tmem_ld32(row + kColIntra + c, y);
-            tmem_wait_ld();
-            tmem_join<32>(x);
-            tmem_join<32>(y);
-            if (c + 32 == DV) {
-              tc_fence_before();
-              mbar_arrive(&sh.o_free);
-            }
-            if (t + tid < seg.t1) {
-              float z[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = fmaf(into, __uint_as_float(x[i]), __uint_as_float(y[i]));
-              store_vec<32>(o + c, z);
-            }
-          }
         }
       }
     }
   } else if (warp < 8) {
-    // ------------------------------------------------ the state (thread = value row) and K'
-    const int r = tid - 128;
-    const uint32_t row = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + kColS;
-    const bool mine = 32 * (warp - 4) < DV;  // warp-uniform
+    // ------------------------------------------------ outputs (thread = token)
+    if constexpr (!STATE_ONLY) {
+      const uint32_t acc = quad + kColO;
+      const int r = tid - 128;
+      const bool wide = a.out_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+#pragma unroll 1
+      for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+        const Segment seg = find_segment(a, u);
+        if (seg.b < 0) break;
+        bf16* out = static_cast<bf16*>(a.out) + seg.h * DV;
+#pragma unroll 1
+        for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+          if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+          const float2 gi = sh.g[n & 1][r];
+          const float into = ex2_approx(gi.x + gi.y) * a.q_scale;  // of the state before the chunk
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+          if (!(good = wait(sh, &sh.qs_done, n & 1))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < DV; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(acc + c, x);
+            tmem_wait_ld();
+            tmem_join<32>(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * into);
+            tmem_st16_nowait(acc + c, x);
+            tmem_st16_nowait(acc + c + 16, x + 16);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&sh.o_ready);
+          if (!(good = wait(sh, &sh.o_done, n & 1))) break;
+          tc_fence_after();
+          // Read and round everything first: the next chunk's products wait for the accumulator.
+          uint32_t w[DV / 2];
+#pragma unroll
+          for (int c = 0; c < DV; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(acc + c, x);
+            tmem_wait_ld();
+            tmem_join<32>(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = pair_of(x + 2 * i);
+              w[c / 2 + i] = pack_bf16x2(y.x, y.y);
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&sh.o_free);
+          if (t + r < seg.t1) {
+            bf16* o = out + (t + r) * a.out_stride;
+#pragma unroll
+            for (int c = 0; c < DV; c += 16) store16(o + c, w + c / 2, wide);
+          }
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------ the state (thread = key column)
+    const int r = tid - 256;
+    const uint32_t row = quad + kColS;
+    const bool mine = 32 * (warp - 8) < DK;  // warp-uniform
+#pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
-      const Segment seg = find_segment(a, u / a.H);
+      const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       const bool last = seg.index + 1 == seg.count;
       if (STATE_ONLY && last) continue;
-      const size_t head = ((size_t)seg.b * a.H + u % a.H) * DV * DK + r * DK, slot = (size_t)u * DV * DK + r * DK;
+      const size_t head = ((size_t)seg.b * a.H + seg.h) * DV * DK + r, slot = (size_t)u * DV * DK + r;
       float total = 1.f;
       if (mine) {
-#pragma unroll
-        for (int c = 0; c < DK; c += 16) {
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 16) {
           float x[16];
-          if (!STATE_ONLY && seg.count > 1) {
-            load_vec_rw<16>(a.slots + slot + c, x);
-          } else if (!STATE_ONLY && a.S0 != nullptr) {
-            load_vec_rw<16>(static_cast<const TST*>(a.S0) + head + c, x);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = 0.f;
+          for (int i = 0; i < 16; ++i) {
+            if (!STATE_ONLY && seg.count > 1) x[i] = a.slots[slot + (c + i) * DK];
+            else if (!STATE_ONLY && a.S0 != nullptr) x[i] = to_f32(static_cast<const TST*>(a.S0)[head + (c + i) * DK]);
+            else x[i] = 0.f;
           }
           tmem_st16_nowait(row + c, reinterpret_cast<const uint32_t*>(x));
         }
         tmem_wait_st();
       }
+#pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-        const float2* g = sh.g[n & 1];
-        if (!(good = wait_warp(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
-        if (t > seg.t0 && !(good = wait_warp(sh, &sh.st_done, (n - 1) & 1))) break;
-        tc_fence_after();
-        const float2 gc = g[kC - 1];
-        const float keep = exp2f(gc.x + gc.y);
+        if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+        const float2 gc = sh.g[n & 1][kC - 1];
+        const float keep = ex2_approx(gc.x + gc.y);
         if (STATE_ONLY) total *= keep;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+        if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
+        tc_fence_after();
         if (mine) {
-#pragma unroll
-          for (int c = 0; c < DK; c += 32) {
-            uint32_t s[32];
-            tmem_ld32(row + c, s);
+          uint32_t s[16];
+          tmem_ld16_nowait(row, s);
+#pragma unroll 1
+          for (int c = 0; c < DV; c += 16) {
+            uint32_t x[16];
             tmem_wait_ld();
-            tmem_join<32>(s);
-            if (!STATE_ONLY) {
-              unsigned char* to = s_hi + (c / 64) * (DV * 128) + r * 128;
+            tmem_join<16>(s);
 #pragma unroll
-              for (int v = 0; v < 4; ++v) {
+            for (int i = 0; i < 16; ++i) x[i] = s[i];
+            if (c + 16 < DV) tmem_ld16_nowait(row + c + 16, s);
+            if (!STATE_ONLY) {
+              unsigned char* to = s_hi + (c / 64) * (DK * 128) + r * 128;
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
                 uint4 hi, lo;
-                split2(__uint_as_float(s[8 * v]), __uint_as_float(s[8 * v + 1]), hi.x, lo.x);
-                split2(__uint_as_float(s[8 * v + 2]), __uint_as_float(s[8 * v + 3]), hi.y, lo.y);
-                split2(__uint_as_float(s[8 * v + 4]), __uint_as_float(s[8 * v + 5]), hi.z, lo.z);
-                split2(__uint_as_float(s[8 * v + 6]), __uint_as_float(s[8 * v + 7]), hi.w, lo.w);
-                const int at = ((c % 64 / 8 + v) ^ (r & 7)) * 16;
-                *reinterpret_cast<uint4*>(to + at) = hi;
-                *reinterpret_cast<uint4*>(to + L::s + at) = lo;
+                split2(pair_of(x + 8 * v), hi.x, lo.x);
+                split2(pair_of(x + 8 * v + 2), hi.y, lo.y);
+                split2(pair_of(x + 8 * v + 4), hi.z, lo.z);
+                split2(pair_of(x + 8 * v + 6), hi.w, lo.w);
+                const int off = ((c % 64 / 8 + v) ^ (r & 7)) * 16;
+                *reinterpret_cast<uint4*>(to + off) = hi;
+                *reinterpret_cast<uint4*>(to + L::s + off) = lo;
               }
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * keep);
-            tmem_st16_nowait(row + c, s);
-            tmem_st16_nowait(row + c + 16, s + 16);
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
+            tmem_st16_nowait(row + c, x);
           }
           tmem_wait_st();
         }
         fence_proxy_async();
         tc_fence_before();
         mbar_arrive(&sh.s_ready);
-        // Keys: 16 bytes at a time where TMA left them, row j = (tid / 8 + 16 i) % 128.  Rows past the
-        // segment's end hold another prompt's tokens, or none: K' and V rows there become zero.
-        const int m = n * kTiles, ks = (m + kK) % L::slots;
-        const int rows = seg.t1 - t;
-        float scale[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) scale[i] = exp2_gap(gc, g[r / 8 + 16 * i]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
-        if (!(good = wait_warp(sh, STATE_ONLY ? &sh.full[ks] : &sh.qk_done, STATE_ONLY ? ((m + kK) / L::slots) & 1 : n & 1)))
-          break;
-        if (rows < kC) {
-          const int vs = (m + kV) % L::slots;
-          if (!(good = wait_warp(sh, &sh.full[vs], ((m + kV) / L::slots) & 1))) break;
-          for (int i = r; i < kC * DV / 8; i += 128)
-            if (i / 8 % kC >= rows) reinterpret_cast<uint4*>(smem + vs * L::slot)[i] = make_uint4(0, 0, 0, 0);
-        }
-        uint4* kt = reinterpret_cast<uint4*>(smem + ks * L::slot);
-        uint4* lt = reinterpret_cast<uint4*>(s_lo);
-        for (int half = 0; half < DK / 64; ++half)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int at = (half * 8 + i) * 128 + r;
-            float x[8];
-            unpack8(kt[at], x);
-            const bool in = r / 8 + 16 * i < rows;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = in ? x[c] * scale[i] : 0.f;
-            uint4 hi, lo;
-            split2(x[0], x[1], hi.x, lo.x);
-            split2(x[2], x[3], hi.y, lo.y);
-            split2(x[4], x[5], hi.z, lo.z);
-            split2(x[6], x[7], hi.w, lo.w);
-            kt[at] = hi;
-            lt[at] = lo;
-          }
-        fence_proxy_async();
-        mbar_arrive(&sh.k_ready);
       }
       if (!good) break;
       if (seg.t1 > seg.t0) {
-        if (!(good = wait_warp(sh, &sh.st_done, (n - 1) & 1))) break;
+        if (!(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
         tc_fence_after();
       }
       if (mine && (STATE_ONLY || last)) {
-#pragma unroll
-        for (int c = 0; c < DK; c += 32) {
-          uint32_t s[32];
-          tmem_ld32(row + c, s);
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 16) {
+          uint32_t s[16];
+          tmem_ld16_nowait(row + c, s);
           tmem_wait_ld();
-          tmem_join<32>(s);
-          if (STATE_ONLY) store_vec<32>(a.slots + slot + c, reinterpret_cast<const float*>(s));
-          else store_vec<32>(static_cast<TST*>(a.S) + head + c, reinterpret_cast<const float*>(s));
+          tmem_join<16>(s);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (STATE_ONLY) a.slots[slot + (c + i) * DK] = __uint_as_float(s[i]);
+            else static_cast<TST*>(a.S)[head + (c + i) * DK] = from_f32<TST>(__uint_as_float(s[i]));
+          }
         }
       }
       if (STATE_ONLY && r == 0) a.decay[u] = total;
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------ TMA loads
-    int m = 0;
+  } else if (warp < 16) {
+    // ------------------------------------------------ K', transposed into tensor memory
+    // Lane l of a transposing load holds tokens 2 (l % 4) and + 1 of an 8 x 8 tile, key column l / 4.
+    // Rows past the segment's end hold another prompt's tokens, or none: K and V rows there become zero.
+    const int r = tid - 384;
+    const uint32_t keys = quad + kColK;
+    const bool mine = 32 * (warp - 12) < DK;  // warp-uniform
+#pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
-      const Segment seg = find_segment(a, u / a.H);
+      const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
-      const int h = u % a.H, hk = h / (a.H / a.Hk);
-      if (lane == 0) {
-        for (int t = seg.t0; t < seg.t1 && good; t += kC) {
-          for (int tile = 0; tile < kTiles; ++tile, ++m) {
-            const int s = m % L::slots;
-            if (m >= L::slots && !(good = wait(sh, &sh.empty[s], (m / L::slots - 1) & 1))) break;
-            const bool is_v = tile == kV;
-            const int halves = (is_v ? DV : DK) / 64;
-            mbar_arrive_expect_tx(&sh.full[s], halves * kHalf);
-            const CUtensorMap* map = is_v ? &mv : tile == kK ? &mk : &mq;
-            for (int x = 0; x < halves; ++x)
-              tma_load_3d(smem + s * L::slot + x * kHalf, map, 64 * x, is_v ? h : hk, t, &sh.full[s]);
-          }
-        }
-      }
-      good = __shfl_sync(0xffffffffu, good, 0);
-    }
-    if (!good && lane == 0)  // leave no copy in flight behind
-      for (int i = m > L::slots ? m - L::slots : 0; i < m; ++i)
-        mbar_wait(&sh.full[i % L::slots], (i / L::slots) & 1);
-  } else if (warp == 9) {
-    // ------------------------------------------------ MMAs
-    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
-      const Segment seg = find_segment(a, u / a.H);
-      if (seg.b < 0) break;
-      if (STATE_ONLY && seg.index + 1 == seg.count) continue;
-      if (lane == 0) {
-        for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-          const int m = n * kTiles;
-          const int qs = m % L::slots, ks = (m + kK) % L::slots, vs = (m + kV) % L::slots;
-          const uint32_t q = smem_addr(smem + qs * L::slot), k = smem_addr(smem + ks * L::slot),
-                         v = smem_addr(smem + vs * L::slot), lo = smem_addr(s_lo), st = smem_addr(s_hi);
-          if (!STATE_ONLY) {
-            if (!(good = wait(sh, &sh.full[qs], (m / L::slots) & 1))) break;
-            if (!(good = wait(sh, &sh.full[ks], ((m + kK) / L::slots) & 1))) break;
-            tc_fence_after();
-            constexpr uint32_t id = idesc_bf16_f32(kC, kC);
-            for (int c = 0; c < DK; c += 16) {
-              const uint32_t at = c / 64 * kHalf + c % 64 * 2;
-              mma_bf16(tmem + kColQK, sw128_desc(q + at), sw128_desc(k + at), id, c > 0);
-            }
-            mma_commit(&sh.qk_done);
-            if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
-            if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
-            tc_fence_after();
-            constexpr uint32_t ids = idesc_bf16_f32(kC, DV);
-            for (int part = 0; part < 2; ++part)
-              for (int c = 0; c < DK; c += 16)
-                mma_bf16(tmem + kColInter, sw128_desc(q + c / 64 * kHalf + c % 64 * 2),
-                         sw128_desc(st + part * L::s + c / 64 * (DV * 128) + c % 64 * 2), ids, part + c > 0);
-            mma_commit(&sh.empty[qs]);
-          } else if (!(good = wait(sh, &sh.s_ready, n & 1))) {
-            break;
-          }
-          if (!(good = wait(sh, &sh.k_ready, n & 1))) break;
-          if (!(good = wait(sh, &sh.full[vs], ((m + kV) / L::slots) & 1))) break;
-          tc_fence_after();
-          // M = 128 value rows; with dv = 64 the upper 64 read what lies behind the tile and land in
-          // tensor-memory lanes that nobody reads.
-          constexpr uint32_t idt = idesc_bf16_f32(kC, DK, true) | kIdescAMn;
-          for (int part = 0; part < 2; ++part)
-            for (int c = 0; c < kC; c += 16)
-              mma_bf16(tmem + kColS, sw128_mn_desc(v + c * 128, kHalf), sw128_mn_desc((part ? lo : k) + c * 128, kHalf),
-                       idt, 1);
-          mma_commit(&sh.st_done);
-          mma_commit(&sh.empty[ks]);
-          if (STATE_ONLY) {
-            mma_commit(&sh.empty[vs]);
-          } else {
-            if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
-            tc_fence_after();
-            constexpr uint32_t idp = idesc_bf16_f32(kC, DV, true);
-            for (int part = 0; part < 2; ++part)
-              for (int c = 0; c < kC; c += 16)
-                mma_bf16_tmem_a(tmem + kColIntra, tmem + kColQK + 64 * part + c / 2,
-                                sw128_mn_desc(v + c * 128, kHalf), idp, part + c > 0);
-            mma_commit(&sh.o_done);
-            mma_commit(&sh.empty[vs]);
-          }
-        }
-      }
-      good = __shfl_sync(0xffffffffu, good, 0);
-      n = __shfl_sync(0xffffffffu, n, 0);
-    }
-  } else {
-    // ------------------------------------------------ decays: lane l sums tokens 4 l .. 4 l + 3
-    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
-      const Segment seg = find_segment(a, u / a.H);
-      if (seg.b < 0) break;
-      if (STATE_ONLY && seg.index + 1 == seg.count) continue;
-      const float* al = a.alpha + u % a.H;
+#pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-        double sum[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = t + 4 * lane + i;
-          const float x = tok < seg.t1 ? __ldg(al + tok * a.alpha_stride) : 1.f;
-          // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
-          sum[i] = x == 0.f ? -1000.f : log2f(x);
-          if (i > 0) sum[i] += sum[i - 1];
+        const Place<L::slots> pk = at.next(kK), pv = at.next(kV);
+        at = at.next(kTiles);
+        const int rows = seg.t1 - t;
+        const float2* g = sh.g[n & 1];
+        if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+        if (!(good = wait(sh, &sh.full[pk.slot], pk.parity))) break;
+        if (n > 0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;  // it has read the last K'
+        tc_fence_after();
+        if (rows < kC) {
+          if (!(good = wait(sh, &sh.full[pv.slot], pv.parity))) break;
+          uint4* kt = reinterpret_cast<uint4*>(smem + pk.slot * L::slot);
+          uint4* vt = reinterpret_cast<uint4*>(smem + pv.slot * L::slot);
+#pragma unroll 1
+          for (int i = r; i < kC * DK / 8; i += 128)
+            if (i / 8 % kC >= rows) kt[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int i = r; i < kC * DV / 8; i += 128)
+            if (i / 8 % kC >= rows) vt[i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+          asm volatile("bar.sync 1, 128;" ::: "memory");
         }
-        double up = sum[3];
+        if (mine) {
+          const float2 gc = g[kC - 1];
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {  // 64 tokens
+            float2 scale[8];                      // of tokens 8 i + 2 (lane % 4) and + 1
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double below = __shfl_up_sync(0xffffffffu, up, o);
-          if (lane >= o) up += below;
+            for (int i = 0; i < 8; ++i) {
+              const float4 gj = *reinterpret_cast<const float4*>(g + 64 * part + 8 * i + 2 * (lane & 3));
+              scale[i] = make_float2(exp2_gap(gc, make_float2(gj.x, gj.y)), exp2_gap(gc, make_float2(gj.z, gj.w)));
+            }
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {  // 16 key columns
+              const int c = 32 * (warp - 12) + 16 * half + (lane & 8), j0 = (lane & 7) + (lane & 16) / 2;
+              const uint32_t from = smem_addr(smem + pk.slot * L::slot) + c / 64 * kHalf + (64 * part + j0) * 128 +
+                                    (((c % 64 / 8) ^ (j0 & 7)) << 4);
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {  // 16 tokens
+                uint32_t w[4];
+                ldsm4t(from + 16 * i * 128, w);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  split2(__fmul2_rn(make_float2(bf16lo(w[x]), bf16hi(w[x])), scale[2 * i + x / 2]), hi[4 * i + x],
+                         lo[4 * i + x]);
+              }
+              const uint32_t to = keys + ((uint32_t)(16 * half) << 16) + 32 * part;
+              tmem_st_16x32(to, hi);
+              tmem_st_16x32(to + 64, lo);
+            }
+          }
+          tmem_wait_st();
         }
-        up -= sum[3];
-        if (n >= 2 && !(good = wait_warp(sh, &sh.g_empty[n & 1], ((n >> 1) - 1) & 1))) break;
+        tc_fence_before();
+        mbar_arrive(&sh.k_ready);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+      }
+    }
+  } else if (warp == 16) {
+    // ------------------------------------------------ TMA loads
+    int issued = 0;  // up to the ring's size: the first tiles find their slots empty
+#pragma unroll 1
+    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+      const Segment seg = find_segment(a, u);
+      if (seg.b < 0) break;
+      if (STATE_ONLY && seg.index + 1 == seg.count) continue;
+      const int h = seg.h, hk = h / (a.H / a.Hk);
+#pragma unroll 1
+      for (int t = seg.t0; t < seg.t1 && good; t += kC) {
+#pragma unroll 1
+        for (int tile = 0; tile < kTiles; ++tile) {
+          if (issued == L::slots) {
+            if (!(good = wait(sh, &sh.empty[at.slot], at.parity ^ 1))) break;
+          } else {
+            ++issued;
+          }
+          if (lane == 0) {
+            const bool is_v = tile == kV;
+            const CUtensorMap* map = is_v ? &mv : tile == kK ? &mk : &mq;
+            unsigned char* to = smem + at.slot * L::slot;
+            mbar_arrive_expect_tx(&sh.full[at.slot], (is_v ? DV : DK) / 64 * kHalf);
+            tma_load_3d(to, map, 0, is_v ? h : hk, t, &sh.full[at.slot]);
+            if ((is_v ? DV : DK) > 64) tma_load_3d(to + kHalf, map, 64, is_v ? h : hk, t, &sh.full[at.slot]);
+          }
+          __syncwarp();
+          at = at.next(1);
+        }
+      }
+    }
+    if (!good)  // leave no copy in flight behind: the last `issued` tiles, oldest first
+#pragma unroll 1
+      for (int i = 0; i < issued; ++i) {
+        const Place<L::slots> p = issued == L::slots ? at.next(i) : Place<L::slots>{i, 0};
+        wait_out(&sh.full[p.slot], issued == L::slots ? p.parity ^ 1 : 0);
+      }
+  } else if (warp == 17) {
+    // ------------------------------------------------ MMAs
+    // The next unit that has tokens, from u on; its number, and its chunks in `chunks`.
+    auto find = [&](int u, int& chunks) {
+#pragma unroll 1
+      for (; u < units; u += gridDim.x) {
+        const Segment seg = find_segment(a, u);
+        if (seg.b < 0) break;
+        chunks = (seg.t1 - seg.t0 + kC - 1) / kC;
+        if (chunks > 0 && !(STATE_ONLY && seg.index + 1 == seg.count)) return u;
+      }
+      chunks = 0;
+      return units;
+    };
+    const uint32_t base = smem_addr(smem), st = smem_addr(s_hi);
+    // Descriptors count 16 bytes; only their start differs, so the others are these plus an offset.
+    const uint64_t by_rows = sw128_desc(0), by_columns = sw128_mn_desc(0, kHalf), state = sw128_mn_desc(st, DK * 128);
+    auto start = [&](int slot) { return __shfl_sync(0xffffffffu, (base + slot * L::slot) >> 4, 0); };
+    // Scores of the chunk whose tiles lie at p, once they have landed.
+    auto scores = [&](Place<L::slots> p) {
+      const Place<L::slots> pk = p.next(kK);
+      if (!wait(sh, &sh.full[p.slot], p.parity) || !wait(sh, &sh.full[pk.slot], pk.parity)) return false;
+      tc_fence_after();
+      constexpr uint32_t id = idesc_bf16_f32(kC, kC);
+      const uint64_t dq = by_rows + start(p.slot), dk = by_rows + start(pk.slot);
+      if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const double x = up + sum[i];
-          const float hi = (float)x;
-          sh.g[n & 1][4 * lane + i] = make_float2(hi, (float)(x - hi));
+        for (int c = 0; c < DK; c += 16) {
+          const int off = (c / 64 * kHalf + c % 64 * 2) >> 4;
+          mma_bf16(tmem + kColQK, dq + off, dk + off, id, c > 0);
+        }
+        mma_commit(&sh.qk_done);
+      }
+      __syncwarp();
+      return true;
+    };
+    int chunks, later;
+    int u = find(blockIdx.x, chunks);
+    if (!STATE_ONLY && u < units) good = scores(at);
+#pragma unroll 1
+    while (u < units && good) {
+      const int next = find(u + gridDim.x, later);
+#pragma unroll 1
+      for (int i = 0; i < chunks; ++i, ++n) {
+        const Place<L::slots> pk = at.next(kK), pv = at.next(kV);
+        if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
+        if (!STATE_ONLY) {
+          if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
+          tc_fence_after();
+          constexpr uint32_t ids = idesc_bf16_f32(kC, DV, true);
+          const uint64_t dq = by_rows + start(at.slot);
+          if (elect_one()) {
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int c = 0; c < DK; c += 16)
+                mma_bf16(tmem + kColO, dq + ((c / 64 * kHalf + c % 64 * 2) >> 4), state + ((part * L::s + c * 128) >> 4),
+                         ids, part + c > 0);
+            mma_commit(&sh.qs_done);
+            mma_commit(&sh.empty[at.slot]);
+          }
+          __syncwarp();
+        }
+        if (!(good = wait(sh, &sh.k_ready, n & 1))) break;
+        if (!(good = wait(sh, &sh.full[pv.slot], pv.parity))) break;
+        tc_fence_after();
+        // M = 128 key columns; with dk = 64 the upper 64 are whatever those lanes hold, and nobody reads
+        // them.
+        constexpr uint32_t idv = idesc_bf16_f32(kC, DV, true);
+        const uint64_t dv = by_columns + start(pv.slot);
+        if (elect_one()) {
+          mma_commit(&sh.empty[pk.slot]);  // the scores and K' have read K
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int c = 0; c < kC; c += 16)
+              mma_bf16_tmem_a(tmem + kColS, tmem + kColK + 64 * part + c / 2, dv + c * 8, idv, 1);
+          mma_commit(&sh.st_done);
+          if (STATE_ONLY) mma_commit(&sh.empty[pv.slot]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
+        at = at.next(kTiles);
+        if (STATE_ONLY) continue;
+        if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
+        if (!(good = wait(sh, &sh.o_ready, n & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int c = 0; c < kC; c += 16)
+              mma_bf16_tmem_a(tmem + kColO, tmem + kColQK + c + 8 * part, dv + c * 8, idv, 1);
+          mma_commit(&sh.o_done);
+          mma_commit(&sh.empty[pv.slot]);
+        }
+        __syncwarp();
+        if ((i + 1 < chunks || next < units) && !(good = scores(at))) break;
+      }
+      u = next;
+      chunks = later;
+    }
+  } else {
+    // ------------------------------------------------ decays: 32 tokens at a time
+#pragma unroll 1
+    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+      const Segment seg = find_segment(a, u);
+      if (seg.b < 0) break;
+      if (STATE_ONLY && seg.index + 1 == seg.count) continue;
+      const float* al = a.alpha + seg.h;
+      auto fetch = [&](int t) { return t + lane < seg.t1 ? __ldg(al + (t + lane) * a.alpha_stride) : 1.f; };
+      float ahead[4];  // the next 128 tokens' decays
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ahead[i] = fetch(seg.t0 + 32 * i);
+      float2 before = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int t = seg.t0; t < seg.t1; t += 32) {
+        // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
+        float2 sum = make_float2(ahead[0] == 0.f ? -1000.f : log2f(ahead[0]), 0.f);
+        ahead[0] = ahead[1];
+        ahead[1] = ahead[2];
+        ahead[2] = ahead[3];
+        ahead[3] = fetch(t + kC);
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const float2 below = make_float2(__shfl_up_sync(0xffffffffu, sum.x, o), __shfl_up_sync(0xffffffffu, sum.y, o));
+          if (lane >= o) sum = add2(below, sum);
+        }
+        const int part = (t - seg.t0) % kC;
+        if (part == 0) {
+          if (n >= 2 && !(good = wait(sh, &sh.g_empty[n & 1], ((n >> 1) - 1) & 1))) break;
+          before = make_float2(0.f, 0.f);
+        }
+        sum = add2(before, sum);
+        sh.g[n & 1][part + lane] = sum;
+        before = make_float2(__shfl_sync(0xffffffffu, sum.x, 31), __shfl_sync(0xffffffffu, sum.y, 31));
+        if (part + 32 == kC || t + 32 >= seg.t1) {
+          // past the prompt's end nothing decays
+#pragma unroll 1
+          for (int i = part + 32; i < kC; i += 32) sh.g[n & 1][i + lane] = before;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
+          ++n;
+        }
       }
     }
   }
   __syncwarp();
-  // Every MMA has completed: the state's owners waited for the last of each unit, the outputs' for
-  // theirs; after a wait that gave up the last ones issued may still run, so wait for them too.
-  if (warp == 9 && lane == 0 && *reinterpret_cast<volatile int*>(&sh.fail)) {
-    mma_commit(&sh.drain);
-    mbar_wait(&sh.drain, 0);
+  // Every MMA has completed: the state's and the outputs' warps waited for their last.  After a wait
+  // that gave up the last ones issued may still run, so wait for them too.
+  if (warp == 17 && *reinterpret_cast<volatile int*>(&sh.fail)) {
+    if (lane == 0) mma_commit(&sh.drain);
+    __syncwarp();
+    wait_out(&sh.drain, 0);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
   if (sh.fail && warp == 0)
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const Segment seg = find_segment(a, u / a.H);
+      const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       if (lane == 0) a.err[seg.b] = TV_ERR_TIMEOUT;
     }
