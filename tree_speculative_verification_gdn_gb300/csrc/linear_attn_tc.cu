@@ -25,9 +25,10 @@
 //
 // Nineteen warps: four turn scores into P (thread = token), four scale and write outputs (thread =
 // token), four own the state (thread = key column), four scale the keys; one issues TMA loads, one the
-// MMAs, one sums the decays.  A ring of whole tiles (Q, K, V, Q, ...) feeds them; every tile is given
-// back by the MMA that reads it last.  One CTA per SM, since five 32 KB tiles and the state's bf16 pair
-// fill shared memory.  A chunk runs every role's code once, and together it has to stay in the
+// MMAs, one sums the decays.  Two tiles of Q, one of K (it is free again as soon as the scores and K'
+// have read it) and two of V are in flight; a chunk's outputs leave through its Q tile by a TMA store
+// (stores of a row by each thread held up every other shared-memory access of the SM).  One CTA per SM,
+// since five 32 KB tiles and the state's bf16 pair fill shared memory.  A chunk runs every role's code once, and together it has to stay in the
 // instruction cache: hence loops that are not unrolled and waits that are not inlined.
 #include "linear_attn.cuh"
 #include "tv_async.cuh"
@@ -41,8 +42,7 @@ constexpr int kC = 128;          // tokens per chunk
 constexpr int kThreads = 608;    // four roles of four warps, and the TMA, MMA and decay warps
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
-constexpr int kSmemMax = 232448;
-constexpr int kMaxSlots = 6;
+constexpr int kSmemMax = 232448;  // per block
 
 // TMEM columns
 constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
@@ -50,7 +50,7 @@ constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 struct Shared {
   float2 g[2][kC];  // g_i as two floats, by chunk parity
   float f[192];     // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full[2], q_empty[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t g_full[2], g_empty[2];
   uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
   uint64_t s_ready, k_ready, p_ready, o_ready, o_free;  // operands written, outputs read
@@ -61,28 +61,20 @@ struct Shared {
 
 template <int DK, int DV, bool STATE_ONLY>
 struct Plan {
-  static constexpr int slot = kC * 2 * (DK > DV ? DK : DV);
+  static constexpr int k = kC * 2 * DK, v = kC * 2 * DV;  // bytes of a tile
+  static constexpr int q = k > v ? k : v;                 // outputs leave through it
+  static constexpr int nq = STATE_ONLY ? 0 : 2, nk = STATE_ONLY ? 3 : DK + DV == 256 ? 1 : 2, nv = STATE_ONLY ? 3 : 2;
+  static constexpr int at_k = nq * q, at_v = at_k + nk * k, at_s = at_v + nv * v;
   static constexpr int s = STATE_ONLY ? 0 : DV * DK * 2;  // the state's bf16 values; as much for its remainders
-  static constexpr int room = kSmemMax - 2 * s - (int)sizeof(Shared);
-  static constexpr int slots = room / slot < kMaxSlots ? room / slot : kMaxSlots;
-  static constexpr int bytes = slots * slot + 2 * s + (int)sizeof(Shared);
-  static_assert(slots >= 5, "a chunk's tiles and the next one's first two fit");
+  static constexpr int bytes = at_s + 2 * s + (int)sizeof(Shared);
+  static_assert(bytes <= kSmemMax, "fits an SM");
 };
 
-// Place of a tile in the ring: its slot, and the parity of the slot's use.
-template <int SLOTS>
-struct Place {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ Place next(int tiles) const {  // tiles <= SLOTS
-    Place p{slot + tiles, parity};
-    if (p.slot >= SLOTS) {
-      p.slot -= SLOTS;
-      p.parity ^= 1;
-    }
-    return p;
-  }
-};
+// A chunk's place among N tiles, and the parity of that place's use.
+template <int N>
+__device__ __forceinline__ int place(int n) { return N > 1 ? n % N : 0; }
+template <int N>
+__device__ __forceinline__ uint32_t turn(int n) { return (n / (N > 0 ? N : 1)) & 1; }
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -161,19 +153,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t at, uint32_t* v) {
                : "memory");
 }
 
-// Words of two bf16 to global memory, 16 columns: one 32-byte store where rows are so aligned (a
-// thread writes its own row, and whole sectors halve the lines that a warp's store touches).
-__device__ __forceinline__ void store16(bf16* p, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
 __device__ __forceinline__ float2 pair_of(const uint32_t* s) {
   return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
@@ -199,12 +178,11 @@ __device__ __forceinline__ float exp2_gap(float2 a, float2 b) { return ex2_appro
 template <int DK, int DV, typename TST, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ LinAttnArgs a, int units, const __grid_constant__ CUtensorMap mq,
-                          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+                          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                          const __grid_constant__ CUtensorMap mo) {
   using L = Plan<DK, DV, STATE_ONLY>;
-  constexpr int kTiles = STATE_ONLY ? 2 : 3;  // tiles per chunk: (Q,) K, V
-  constexpr int kK = kTiles - 2, kV = kTiles - 1;
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* s_hi = smem + L::slots * L::slot;  // the state's values, then their remainders
+  unsigned char* s_hi = smem + L::at_s;  // the state's values, then their remainders
   Shared& sh = *reinterpret_cast<Shared*>(s_hi + 2 * L::s);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
@@ -214,9 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok) return;
 
   if (tid == 0) {
-    for (int i = 0; i < L::slots; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      if (i < 2) mbar_init(&sh.q_full[i], 1), mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 4);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.g_full[i], 1);
@@ -244,7 +225,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Every role walks the same units and chunks; n counts chunks over all units.
   int n = 0;
-  Place<L::slots> at;  // of the chunk's first tile
   bool good = true;
   if (warp < 4) {
     // ------------------------------------------------ scores to P (thread = token)
@@ -315,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!STATE_ONLY) {
       const uint32_t acc = quad + kColO;
       const int r = tid - 128;
-      const bool wide = a.out_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
 #pragma unroll 1
       for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
         const Segment seg = find_segment(a, u);
@@ -362,10 +341,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           mbar_arrive(&sh.o_free);
-          if (t + r < seg.t1) {
-            bf16* o = out + (t + r) * a.out_stride;
+          // PV has run, so QK and QS of this chunk have read its Q tile.
+          const int slot = place<2>(n);
+          if (t + kC <= seg.t1) {
+            unsigned char* o = smem + slot * L::q;
 #pragma unroll
-            for (int c = 0; c < DV; c += 16) store16(o + c, w + c / 2, wide);
+            for (int c = 0; c < DV / 8; ++c)
+              *reinterpret_cast<uint4*>(o + c / 8 * kHalf + r * 128 + ((c % 8) ^ (r & 7)) * 16) =
+                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            fence_proxy_async();
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+            if (r == 0) {
+#pragma unroll
+              for (int c = 0; c < DV; c += 64) tma_store_3d(&mo, c, seg.h, t, o + c / 64 * kHalf);
+              bulk_commit();
+              bulk_wait_read<0>();
+              mbar_arrive(&sh.q_empty[slot]);
+            }
+            __syncwarp();
+          } else {  // a whole tile would write into the next prompt's rows
+            if (t + r < seg.t1) {
+              uint4* o = reinterpret_cast<uint4*>(out + (t + r) * a.out_stride);
+#pragma unroll
+              for (int c = 0; c < DV / 8; ++c) o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            }
+            if (r == 0) mbar_arrive(&sh.q_empty[slot]);
+            __syncwarp();
           }
         }
       }
@@ -477,18 +478,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
 #pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-        const Place<L::slots> pk = at.next(kK), pv = at.next(kV);
-        at = at.next(kTiles);
         const int rows = seg.t1 - t;
+        unsigned char* k_tile = smem + L::at_k + place<L::nk>(n) * L::k;
         const float2* g = sh.g[n & 1];
         if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
-        if (!(good = wait(sh, &sh.full[pk.slot], pk.parity))) break;
+        if (!(good = wait(sh, &sh.k_full[place<L::nk>(n)], turn<L::nk>(n)))) break;
         if (n > 0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;  // it has read the last K'
         tc_fence_after();
         if (rows < kC) {
-          if (!(good = wait(sh, &sh.full[pv.slot], pv.parity))) break;
-          uint4* kt = reinterpret_cast<uint4*>(smem + pk.slot * L::slot);
-          uint4* vt = reinterpret_cast<uint4*>(smem + pv.slot * L::slot);
+          if (!(good = wait(sh, &sh.v_full[place<L::nv>(n)], turn<L::nv>(n)))) break;
+          uint4* kt = reinterpret_cast<uint4*>(k_tile);
+          uint4* vt = reinterpret_cast<uint4*>(smem + L::at_v + place<L::nv>(n) * L::v);
 #pragma unroll 1
           for (int i = r; i < kC * DK / 8; i += 128)
             if (i / 8 % kC >= rows) kt[i] = make_uint4(0, 0, 0, 0);
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {  // 16 key columns
               const int c = 32 * (warp - 12) + 16 * half + (lane & 8), j0 = (lane & 7) + (lane & 16) / 2;
-              const uint32_t from = smem_addr(smem + pk.slot * L::slot) + c / 64 * kHalf + (64 * part + j0) * 128 +
+              const uint32_t from = smem_addr(k_tile) + c / 64 * kHalf + (64 * part + j0) * 128 +
                                     (((c % 64 / 8) ^ (j0 & 7)) << 4);
               uint32_t hi[16], lo[16];
 #pragma unroll
@@ -534,11 +534,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.k_ready);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+        // K is free as soon as the scores have read it too, for the next one to land in time.
+        if (!STATE_ONLY && !(good = wait(sh, &sh.qk_done, n & 1))) break;
+        if (lane == 0) mbar_arrive(&sh.k_empty[place<L::nk>(n)]);
       }
     }
   } else if (warp == 16) {
     // ------------------------------------------------ TMA loads
-    int issued = 0;  // up to the ring's size: the first tiles find their slots empty
+    auto load = [&](const CUtensorMap* map, unsigned char* to, int columns, int h, int t, uint64_t* full) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full, columns / 64 * kHalf);
+        tma_load_3d(to, map, 0, h, t, full);
+        if (columns > 64) tma_load_3d(to + kHalf, map, 64, h, t, full);
+      }
+      __syncwarp();
+    };
+    int loads[3] = {0, 0, 0};  // of Q, K and V
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -546,33 +557,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const int h = seg.h, hk = h / (a.H / a.Hk);
 #pragma unroll 1
-      for (int t = seg.t0; t < seg.t1 && good; t += kC) {
-#pragma unroll 1
-        for (int tile = 0; tile < kTiles; ++tile) {
-          if (issued == L::slots) {
-            if (!(good = wait(sh, &sh.empty[at.slot], at.parity ^ 1))) break;
-          } else {
-            ++issued;
-          }
-          if (lane == 0) {
-            const bool is_v = tile == kV;
-            const CUtensorMap* map = is_v ? &mv : tile == kK ? &mk : &mq;
-            unsigned char* to = smem + at.slot * L::slot;
-            mbar_arrive_expect_tx(&sh.full[at.slot], (is_v ? DV : DK) / 64 * kHalf);
-            tma_load_3d(to, map, 0, is_v ? h : hk, t, &sh.full[at.slot]);
-            if ((is_v ? DV : DK) > 64) tma_load_3d(to + kHalf, map, 64, is_v ? h : hk, t, &sh.full[at.slot]);
-          }
-          __syncwarp();
-          at = at.next(1);
+      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+        if (!STATE_ONLY) {
+          const int i = place<2>(n);
+          if (n >= 2 && !(good = wait(sh, &sh.q_empty[i], turn<2>(n) ^ 1))) break;
+          load(&mq, smem + i * L::q, DK, hk, t, &sh.q_full[i]);
+          loads[0] = n + 1;
         }
+        const int iv = place<L::nv>(n), ik = place<L::nk>(n);
+        if (n >= L::nv && !(good = wait(sh, &sh.v_empty[iv], turn<L::nv>(n) ^ 1))) break;
+        load(&mv, smem + L::at_v + iv * L::v, DV, h, t, &sh.v_full[iv]);
+        loads[2] = n + 1;
+        if (n >= L::nk && !(good = wait(sh, &sh.k_empty[ik], turn<L::nk>(n) ^ 1))) break;
+        load(&mk, smem + L::at_k + ik * L::k, DK, hk, t, &sh.k_full[ik]);
+        loads[1] = n + 1;
       }
     }
-    if (!good)  // leave no copy in flight behind: the last `issued` tiles, oldest first
+    if (!good) {  // leave no copy in flight behind: the last ones of each kind
+      if (!STATE_ONLY && loads[0] > 0) wait_out(&sh.q_full[place<2>(loads[0] - 1)], turn<2>(loads[0] - 1));
+      if (!STATE_ONLY && loads[0] > 1) wait_out(&sh.q_full[place<2>(loads[0] - 2)], turn<2>(loads[0] - 2));
 #pragma unroll 1
-      for (int i = 0; i < issued; ++i) {
-        const Place<L::slots> p = issued == L::slots ? at.next(i) : Place<L::slots>{i, 0};
-        wait_out(&sh.full[p.slot], issued == L::slots ? p.parity ^ 1 : 0);
+      for (int i = 1; i <= 3; ++i) {
+        if (i <= L::nk && loads[1] >= i) wait_out(&sh.k_full[place<L::nk>(loads[1] - i)], turn<L::nk>(loads[1] - i));
+        if (i <= L::nv && loads[2] >= i) wait_out(&sh.v_full[place<L::nv>(loads[2] - i)], turn<L::nv>(loads[2] - i));
       }
+    }
   } else if (warp == 17) {
     // ------------------------------------------------ MMAs
     // The next unit that has tokens, from u on; its number, and its chunks in `chunks`.
@@ -590,14 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = smem_addr(smem), st = smem_addr(s_hi);
     // Descriptors count 16 bytes; only their start differs, so the others are these plus an offset.
     const uint64_t by_rows = sw128_desc(0), by_columns = sw128_mn_desc(0, kHalf), state = sw128_mn_desc(st, DK * 128);
-    auto start = [&](int slot) { return __shfl_sync(0xffffffffu, (base + slot * L::slot) >> 4, 0); };
-    // Scores of the chunk whose tiles lie at p, once they have landed.
-    auto scores = [&](Place<L::slots> p) {
-      const Place<L::slots> pk = p.next(kK);
-      if (!wait(sh, &sh.full[p.slot], p.parity) || !wait(sh, &sh.full[pk.slot], pk.parity)) return false;
+    auto start = [&](int offset) { return __shfl_sync(0xffffffffu, (base + offset) >> 4, 0); };
+    // Scores of chunk n, once its tiles have landed.
+    auto scores = [&](int n) {
+      const int iq = place<2>(n), ik = place<L::nk>(n);
+      if (!wait(sh, &sh.q_full[iq], turn<2>(n)) || !wait(sh, &sh.k_full[ik], turn<L::nk>(n))) return false;
       tc_fence_after();
       constexpr uint32_t id = idesc_bf16_f32(kC, kC);
-      const uint64_t dq = by_rows + start(p.slot), dk = by_rows + start(pk.slot);
+      const uint64_t dq = by_rows + start(iq * L::q), dk = by_rows + start(L::at_k + ik * L::k);
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < DK; c += 16) {
@@ -611,19 +620,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int chunks, later;
     int u = find(blockIdx.x, chunks);
-    if (!STATE_ONLY && u < units) good = scores(at);
+    if (!STATE_ONLY && u < units) good = scores(0);
 #pragma unroll 1
     while (u < units && good) {
       const int next = find(u + gridDim.x, later);
 #pragma unroll 1
       for (int i = 0; i < chunks; ++i, ++n) {
-        const Place<L::slots> pk = at.next(kK), pv = at.next(kV);
+        const int iv = place<L::nv>(n);
         if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
         if (!STATE_ONLY) {
           if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
           tc_fence_after();
           constexpr uint32_t ids = idesc_bf16_f32(kC, DV, true);
-          const uint64_t dq = by_rows + start(at.slot);
+          const uint64_t dq = by_rows + start(place<2>(n) * L::q);
           if (elect_one()) {
 #pragma unroll 1
             for (int part = 0; part < 2; ++part)
@@ -632,29 +641,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_bf16(tmem + kColO, dq + ((c / 64 * kHalf + c % 64 * 2) >> 4), state + ((part * L::s + c * 128) >> 4),
                          ids, part + c > 0);
             mma_commit(&sh.qs_done);
-            mma_commit(&sh.empty[at.slot]);
           }
           __syncwarp();
         }
         if (!(good = wait(sh, &sh.k_ready, n & 1))) break;
-        if (!(good = wait(sh, &sh.full[pv.slot], pv.parity))) break;
+        if (!(good = wait(sh, &sh.v_full[iv], turn<L::nv>(n)))) break;
         tc_fence_after();
         // M = 128 key columns; with dk = 64 the upper 64 are whatever those lanes hold, and nobody reads
         // them.
         constexpr uint32_t idv = idesc_bf16_f32(kC, DV, true);
-        const uint64_t dv = by_columns + start(pv.slot);
+        const uint64_t dv = by_columns + start(L::at_v + iv * L::v);
         if (elect_one()) {
-          mma_commit(&sh.empty[pk.slot]);  // the scores and K' have read K
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColS, tmem + kColK + 64 * part + c / 2, dv + c * 8, idv, 1);
           mma_commit(&sh.st_done);
-          if (STATE_ONLY) mma_commit(&sh.empty[pv.slot]);
+          if (STATE_ONLY) mma_commit(&sh.v_empty[iv]);
         }
         __syncwarp();
-        at = at.next(kTiles);
         if (STATE_ONLY) continue;
         if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
         if (!(good = wait(sh, &sh.o_ready, n & 1))) break;
@@ -666,10 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColO, tmem + kColQK + c + 8 * part, dv + c * 8, idv, 1);
           mma_commit(&sh.o_done);
-          mma_commit(&sh.empty[pv.slot]);
+          mma_commit(&sh.v_empty[iv]);
         }
         __syncwarp();
-        if ((i + 1 < chunks || next < units) && !(good = scores(at))) break;
+        if ((i + 1 < chunks || next < units) && !(good = scores(n + 1))) break;
       }
       u = next;
       chunks = later;
@@ -683,24 +689,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const float* al = a.alpha + seg.h;
       auto fetch = [&](int t) { return t + lane < seg.t1 ? __ldg(al + (t + lane) * a.alpha_stride) : 1.f; };
-      float ahead[4];  // the next 128 tokens' decays
+      float now[4], next[4];  // this chunk's decays, and the next one's on their way
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ahead[i] = fetch(seg.t0 + 32 * i);
+      for (int i = 0; i < 4; ++i) next[i] = fetch(seg.t0 + 32 * i);
       float2 before = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += 32) {
+        const int part = (t - seg.t0) % kC;
+        if (part == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) now[i] = next[i];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next[i] = fetch(t + kC + 32 * i);
+        }
+        const float x = part == 0 ? now[0] : part == 32 ? now[1] : part == 64 ? now[2] : now[3];
         // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
-        float2 sum = make_float2(ahead[0] == 0.f ? -1000.f : log2f(ahead[0]), 0.f);
-        ahead[0] = ahead[1];
-        ahead[1] = ahead[2];
-        ahead[2] = ahead[3];
-        ahead[3] = fetch(t + kC);
+        float2 sum = make_float2(x == 0.f ? -1000.f : log2f(x), 0.f);
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const float2 below = make_float2(__shfl_up_sync(0xffffffffu, sum.x, o), __shfl_up_sync(0xffffffffu, sum.y, o));
           if (lane >= o) sum = add2(below, sum);
         }
-        const int part = (t - seg.t0) % kC;
         if (part == 0) {
           if (n >= 2 && !(good = wait(sh, &sh.g_empty[n & 1], ((n >> 1) - 1) & 1))) break;
           before = make_float2(0.f, 0.f);
@@ -754,15 +763,15 @@ cudaError_t go(const LinAttnArgs& a, int units, const CUtensorMap* m, cudaStream
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count();
-  fn<<<units < sms ? units : sms, kThreads, L::bytes, s>>>(a, units, m[0], m[1], m[2]);
+  fn<<<units < sms ? units : sms, kThreads, L::bytes, s>>>(a, units, m[0], m[1], m[2], m[3]);
   return cudaGetLastError();
 }
 
 template <int DK, int DV, typename TST>
 cudaError_t prompt_tc(const LinAttnArgs& a, cudaStream_t s) {
-  CUtensorMap m[3];
+  CUtensorMap m[4];
   if (!token_map(&m[0], a.q, DK, a.Hk, a.T, a.q_stride) || !token_map(&m[1], a.k, DK, a.Hk, a.T, a.k_stride) ||
-      !token_map(&m[2], a.v, DV, a.H, a.T, a.v_stride))
+      !token_map(&m[2], a.v, DV, a.H, a.T, a.v_stride) || !token_map(&m[3], a.out, DV, a.H, a.T, a.out_stride))
     return cudaErrorInvalidValue;
   const long long units = (a.seg_len > 0 ? (long long)a.B + a.T / a.seg_len : a.B) * a.H;
   if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
