@@ -23,10 +23,10 @@
 // and K' go through tensor memory (K transposed on the way by ldmatrix) and only S through shared
 // memory.
 //
-// Nineteen warps: four turn scores into P (thread = token), four scale and write outputs (thread =
-// token), four own the state (thread = key column), four scale the keys; one issues TMA loads, one the
-// MMAs, one sums the decays.  Two tiles of Q, one of K (it is free again as soon as the scores and K'
-// have read it) and two of V are in flight; a chunk's outputs leave through its Q tile by a TMA store
+// Twenty warps: four turn scores into P (thread = token), four scale and write outputs (thread =
+// token), four own the state (thread = key column), four scale the keys; one loads Q and V, one K, one
+// issues the MMAs, one sums the decays.  Two tiles of Q, one of K (free again as soon as the scores and K'
+// have read it; the next one waits for it in L2) and two of V are in flight; a chunk's outputs leave through its Q tile by a TMA store
 // (stores of a row by each thread held up every other shared-memory access of the SM).  One CTA per SM,
 // since five 32 KB tiles and the state's bf16 pair fill shared memory.  A chunk runs every role's code once, and together it has to stay in the
 // instruction cache: hence loops that are not unrolled and waits that are not inlined.
@@ -39,7 +39,7 @@ namespace tv {
 namespace {
 
 constexpr int kC = 128;          // tokens per chunk
-constexpr int kThreads = 608;    // four roles of four warps, and the TMA, MMA and decay warps
+constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two TMA warps
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sh.k_empty[place<L::nk>(n)]);
       }
     }
-  } else if (warp == 16) {
+  } else if (warp == 16 || warp == 19) {
     // ------------------------------------------------ TMA loads
     auto load = [&](const CUtensorMap* map, unsigned char* to, int columns, int h, int t, uint64_t* full) {
       if (lane == 0) {
@@ -549,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    int loads[3] = {0, 0, 0};  // of Q, K and V
+    const bool keys = warp == 19;
+    int loads = 0, v_loads = 0;  // of K or Q, of V
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -558,30 +559,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = seg.h, hk = h / (a.H / a.Hk);
 #pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-        if (!STATE_ONLY) {
-          const int i = place<2>(n);
-          if (n >= 2 && !(good = wait(sh, &sh.q_empty[i], turn<2>(n) ^ 1))) break;
-          load(&mq, smem + i * L::q, DK, hk, t, &sh.q_full[i]);
-          loads[0] = n + 1;
+        if (keys) {
+          const int i = place<L::nk>(n);
+          if (L::nk == 1 && t + kC < seg.t1 && lane == 0) {
+            tma_prefetch_3d(&mk, 0, hk, t + kC);
+            if (DK > 64) tma_prefetch_3d(&mk, 64, hk, t + kC);
+          }
+          if (n >= L::nk && !(good = wait(sh, &sh.k_empty[i], turn<L::nk>(n) ^ 1))) break;
+          load(&mk, smem + L::at_k + i * L::k, DK, hk, t, &sh.k_full[i]);
+          loads = n + 1;
+        } else {
+          const int i = place<L::nv>(n);
+          if (n >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(n) ^ 1))) break;
+          load(&mv, smem + L::at_v + i * L::v, DV, h, t, &sh.v_full[i]);
+          v_loads = n + 1;
+          if (!STATE_ONLY) {
+            const int iq = place<2>(n);
+            if (n >= 2 && !(good = wait(sh, &sh.q_empty[iq], turn<2>(n) ^ 1))) break;
+            load(&mq, smem + iq * L::q, DK, hk, t, &sh.q_full[iq]);
+            loads = n + 1;
+          }
         }
-        const int iv = place<L::nv>(n), ik = place<L::nk>(n);
-        if (n >= L::nv && !(good = wait(sh, &sh.v_empty[iv], turn<L::nv>(n) ^ 1))) break;
-        load(&mv, smem + L::at_v + iv * L::v, DV, h, t, &sh.v_full[iv]);
-        loads[2] = n + 1;
-        if (n >= L::nk && !(good = wait(sh, &sh.k_empty[ik], turn<L::nk>(n) ^ 1))) break;
-        load(&mk, smem + L::at_k + ik * L::k, DK, hk, t, &sh.k_full[ik]);
-        loads[1] = n + 1;
       }
     }
-    if (!good) {  // leave no copy in flight behind: the last ones of each kind
-      if (!STATE_ONLY && loads[0] > 0) wait_out(&sh.q_full[place<2>(loads[0] - 1)], turn<2>(loads[0] - 1));
-      if (!STATE_ONLY && loads[0] > 1) wait_out(&sh.q_full[place<2>(loads[0] - 2)], turn<2>(loads[0] - 2));
+    if (!good)  // leave no copy in flight behind: the last ones of each kind
 #pragma unroll 1
       for (int i = 1; i <= 3; ++i) {
-        if (i <= L::nk && loads[1] >= i) wait_out(&sh.k_full[place<L::nk>(loads[1] - i)], turn<L::nk>(loads[1] - i));
-        if (i <= L::nv && loads[2] >= i) wait_out(&sh.v_full[place<L::nv>(loads[2] - i)], turn<L::nv>(loads[2] - i));
+        if (keys && i <= L::nk && loads >= i) wait_out(&sh.k_full[place<L::nk>(loads - i)], turn<L::nk>(loads - i));
+        if (!keys && i <= L::nq && loads >= i) wait_out(&sh.q_full[place<2>(loads - i)], turn<2>(loads - i));
+        if (!keys && i <= L::nv && v_loads >= i) wait_out(&sh.v_full[place<L::nv>(v_loads - i)], turn<L::nv>(v_loads - i));
       }
-    }
   } else if (warp == 17) {
     // ------------------------------------------------ MMAs
     // The next unit that has tokens, from u on; its number, and its chunks in `chunks`.
@@ -681,50 +688,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       chunks = later;
     }
   } else {
-    // ------------------------------------------------ decays: 32 tokens at a time
+    // ------------------------------------------------ decays: four sums of 32 tokens side by side
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const float* al = a.alpha + seg.h;
-      auto fetch = [&](int t) { return t + lane < seg.t1 ? __ldg(al + (t + lane) * a.alpha_stride) : 1.f; };
-      float now[4], next[4];  // this chunk's decays, and the next one's on their way
+      float next[4];  // the next chunk's decays, on their way
+      auto fetch = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) next[i] = fetch(seg.t0 + 32 * i);
-      float2 before = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int t = seg.t0; t < seg.t1; t += 32) {
-        const int part = (t - seg.t0) % kC;
-        if (part == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) now[i] = next[i];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) next[i] = fetch(t + kC + 32 * i);
+        for (int i = 0; i < 4; ++i) {
+          const int tok = t + 32 * i + lane;  // past the prompt's end nothing decays
+          next[i] = tok < seg.t1 ? __ldg(al + tok * a.alpha_stride) : 1.f;
         }
-        const float x = part == 0 ? now[0] : part == 32 ? now[1] : part == 64 ? now[2] : now[3];
+      };
+      fetch(seg.t0);
+#pragma unroll 1
+      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+        float2 sum[4];
         // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
-        float2 sum = make_float2(x == 0.f ? -1000.f : log2f(x), 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = make_float2(next[i] == 0.f ? -1000.f : log2f(next[i]), 0.f);
+        if (t + kC < seg.t1) fetch(t + kC);
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-          const float2 below = make_float2(__shfl_up_sync(0xffffffffu, sum.x, o), __shfl_up_sync(0xffffffffu, sum.y, o));
-          if (lane >= o) sum = add2(below, sum);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 below =
+                make_float2(__shfl_up_sync(0xffffffffu, sum[i].x, o), __shfl_up_sync(0xffffffffu, sum[i].y, o));
+            if (lane >= o) sum[i] = add2(below, sum[i]);
+          }
         }
-        if (part == 0) {
-          if (n >= 2 && !(good = wait(sh, &sh.g_empty[n & 1], ((n >> 1) - 1) & 1))) break;
-          before = make_float2(0.f, 0.f);
+        if (n >= 2 && !(good = wait(sh, &sh.g_empty[n & 1], ((n >> 1) - 1) & 1))) break;
+        float2 before = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i > 0) sum[i] = add2(before, sum[i]);
+          sh.g[n & 1][32 * i + lane] = sum[i];
+          before = make_float2(__shfl_sync(0xffffffffu, sum[i].x, 31), __shfl_sync(0xffffffffu, sum[i].y, 31));
         }
-        sum = add2(before, sum);
-        sh.g[n & 1][part + lane] = sum;
-        before = make_float2(__shfl_sync(0xffffffffu, sum.x, 31), __shfl_sync(0xffffffffu, sum.y, 31));
-        if (part + 32 == kC || t + 32 >= seg.t1) {
-          // past the prompt's end nothing decays
-#pragma unroll 1
-          for (int i = part + 32; i < kC; i += 32) sh.g[n & 1][i + lane] = before;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
-          ++n;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
       }
     }
   }
