@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kC = 128;          // tokens per chunk
 constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two TMA warps
+constexpr int kAhead = kC;       // tokens by which tiles are brought to L2 before they are loaded
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
@@ -98,8 +99,8 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 // Waits for the phase of that parity; false once this or another warp has given up.  Executed by a
-// whole warp, one answer for all of it.
-__device__ __noinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+// whole warp, one answer for all of it.  The first look is inline, the rest is not.
+__device__ __noinline__ bool wait_more(Shared& sh, uint64_t* bar, uint32_t parity) {
   bool ok = false;
 #pragma unroll 1
   for (uint32_t it = 0; it < kPolls && !ok; ++it) {
@@ -108,6 +109,10 @@ __device__ __noinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
   }
   if (!ok) *reinterpret_cast<volatile int*>(&sh.fail) = 1;
   return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+  return wait_more(sh, bar, parity);
 }
 // The library's wait, out of line: for the paths after a wait gave up.
 __device__ __noinline__ void wait_out(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity); }
@@ -557,19 +562,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const int h = seg.h, hk = h / (a.H / a.Hk);
+      auto ahead = [&](const CUtensorMap* map, int columns, int h, int t) {
+        if (t < seg.t1 && lane == 0) {
+          tma_prefetch_3d(map, 0, h, t);
+          if (columns > 64) tma_prefetch_3d(map, 64, h, t);
+        }
+      };
 #pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
         if (keys) {
           const int i = place<L::nk>(n);
-          if (L::nk == 1 && t + kC < seg.t1 && lane == 0) {
-            tma_prefetch_3d(&mk, 0, hk, t + kC);
-            if (DK > 64) tma_prefetch_3d(&mk, 64, hk, t + kC);
-          }
+          ahead(&mk, DK, hk, t + kAhead);
           if (n >= L::nk && !(good = wait(sh, &sh.k_empty[i], turn<L::nk>(n) ^ 1))) break;
           load(&mk, smem + L::at_k + i * L::k, DK, hk, t, &sh.k_full[i]);
           loads = n + 1;
         } else {
           const int i = place<L::nv>(n);
+          ahead(&mv, DV, h, t + kAhead);
+          if (!STATE_ONLY) ahead(&mq, DK, hk, t + kAhead);
           if (n >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(n) ^ 1))) break;
           load(&mv, smem + L::at_v + i * L::v, DV, h, t, &sh.v_full[i]);
           v_loads = n + 1;
@@ -607,27 +617,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Descriptors count 16 bytes; only their start differs, so the others are these plus an offset.
     const uint64_t by_rows = sw128_desc(0), by_columns = sw128_mn_desc(0, kHalf), state = sw128_mn_desc(st, DK * 128);
     auto start = [&](int offset) { return __shfl_sync(0xffffffffu, (base + offset) >> 4, 0); };
-    // Scores of chunk n, once its tiles have landed.
-    auto scores = [&](int n) {
-      const int iq = place<2>(n), ik = place<L::nk>(n);
-      if (!wait(sh, &sh.q_full[iq], turn<2>(n)) || !wait(sh, &sh.k_full[ik], turn<L::nk>(n))) return false;
-      tc_fence_after();
-      constexpr uint32_t id = idesc_bf16_f32(kC, kC);
-      const uint64_t dq = by_rows + start(iq * L::q), dk = by_rows + start(L::at_k + ik * L::k);
-      if (elect_one()) {
-#pragma unroll
-        for (int c = 0; c < DK; c += 16) {
-          const int off = (c / 64 * kHalf + c % 64 * 2) >> 4;
-          mma_bf16(tmem + kColQK, dq + off, dk + off, id, c > 0);
-        }
-        mma_commit(&sh.qk_done);
-      }
-      __syncwarp();
-      return true;
+    // Scores of chunk n, whose tiles have landed.
+    auto landed = [&](int n) {
+      return wait(sh, &sh.q_full[place<2>(n)], turn<2>(n)) && wait(sh, &sh.k_full[place<L::nk>(n)], turn<L::nk>(n));
     };
+    auto scores = [&](uint64_t dq, uint64_t dk) {
+      constexpr uint32_t id = idesc_bf16_f32(kC, kC);
+#pragma unroll
+      for (int c = 0; c < DK; c += 16) {
+        const int off = (c / 64 * kHalf + c % 64 * 2) >> 4;
+        mma_bf16(tmem + kColQK, dq + off, dk + off, id, c > 0);
+      }
+      mma_commit(&sh.qk_done);
+    };
+    auto q_rows = [&](int n) { return by_rows + start(place<2>(n) * L::q); };
+    auto k_rows = [&](int n) { return by_rows + start(L::at_k + place<L::nk>(n) * L::k); };
     int chunks, later;
     int u = find(blockIdx.x, chunks);
-    if (!STATE_ONLY && u < units) good = scores(0);
+    if (!STATE_ONLY && u < units && (good = landed(0))) {
+      tc_fence_after();
+      const uint64_t dq = q_rows(0), dk = k_rows(0);
+      if (elect_one()) scores(dq, dk);
+      __syncwarp();
+    }
 #pragma unroll 1
     while (u < units && good) {
       const int next = find(u + gridDim.x, later);
@@ -639,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
           tc_fence_after();
           constexpr uint32_t ids = idesc_bf16_f32(kC, DV, true);
-          const uint64_t dq = by_rows + start(place<2>(n) * L::q);
+          const uint64_t dq = q_rows(n);
           if (elect_one()) {
 #pragma unroll 1
             for (int part = 0; part < 2; ++part)
@@ -669,9 +681,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (STATE_ONLY) continue;
+        const bool more = i + 1 < chunks || next < units;
+        if (more && !(good = landed(n + 1))) break;
         if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
         if (!(good = wait(sh, &sh.o_ready, n & 1))) break;
         tc_fence_after();
+        const uint64_t dq = q_rows(n + 1), dk = k_rows(n + 1);
         if (elect_one()) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
@@ -679,10 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColO, tmem + kColQK + c + 8 * part, dv + c * 8, idv, 1);
           mma_commit(&sh.o_done);
+          if (more) scores(dq, dk);
           mma_commit(&sh.v_empty[iv]);
         }
         __syncwarp();
-        if ((i + 1 < chunks || next < units) && !(good = scores(n + 1))) break;
       }
       u = next;
       chunks = later;
