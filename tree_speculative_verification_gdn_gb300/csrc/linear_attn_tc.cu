@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
         if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
+        if (!STATE_ONLY && n > 0 && !(good = wait(sh, &sh.qs_done, (n - 1) & 1))) break;  // it has read the last S
         tc_fence_after();
         if (mine) {
           uint32_t s[16];
@@ -647,25 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < chunks; ++i, ++n) {
         const int iv = place<L::nv>(n);
         if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
-        if (!STATE_ONLY) {
-          if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
-          tc_fence_after();
-          constexpr uint32_t ids = idesc_bf16_f32(kC, DV, true);
-          const uint64_t dq = q_rows(n);
-          if (elect_one()) {
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int c = 0; c < DK; c += 16)
-                mma_bf16(tmem + kColO, dq + ((c / 64 * kHalf + c % 64 * 2) >> 4), state + ((part * L::s + c * 128) >> 4),
-                         ids, part + c > 0);
-            mma_commit(&sh.qs_done);
-          }
-          __syncwarp();
-        }
         if (!(good = wait(sh, &sh.k_ready, n & 1))) break;
         if (!(good = wait(sh, &sh.v_full[iv], turn<L::nv>(n)))) break;
         tc_fence_after();
+        // ST first, so that the next K' is made while QS and PV run.
         // M = 128 key columns; with dk = 64 the upper 64 are whatever those lanes hold, and nobody reads
         // them.
         constexpr uint32_t idv = idesc_bf16_f32(kC, DV, true);
@@ -681,12 +667,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (STATE_ONLY) continue;
+        if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
+        tc_fence_after();
+        constexpr uint32_t ids = idesc_bf16_f32(kC, DV, true);
+        const uint64_t this_q = q_rows(n);
+        if (elect_one()) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int c = 0; c < DK; c += 16)
+              mma_bf16(tmem + kColO, this_q + ((c / 64 * kHalf + c % 64 * 2) >> 4), state + ((part * L::s + c * 128) >> 4),
+                       ids, part + c > 0);
+          mma_commit(&sh.qs_done);
+        }
+        __syncwarp();
         const bool more = i + 1 < chunks || next < units;
         if (more && !(good = landed(n + 1))) break;
         if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
         if (!(good = wait(sh, &sh.o_ready, n & 1))) break;
         tc_fence_after();
-        const uint64_t dq = q_rows(n + 1), dk = k_rows(n + 1);
+        const uint64_t next_q = q_rows(n + 1), next_k = k_rows(n + 1);
         if (elect_one()) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColO, tmem + kColQK + c + 8 * part, dv + c * 8, idv, 1);
           mma_commit(&sh.o_done);
-          if (more) scores(dq, dk);
+          if (more) scores(next_q, next_k);
           mma_commit(&sh.v_empty[iv]);
         }
         __syncwarp();
