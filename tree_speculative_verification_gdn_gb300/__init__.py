@@ -130,28 +130,49 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _rows(t):
-    """Pointer and row stride (elements) of a tensor whose rows -- everything past the first
-    dimension -- are dense; the rows themselves may lie apart, as in a slice of a projection."""
+def _refuse(name: str, t, shape, dtype):
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the library must be CUDA tensors")
+    raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _whole(name: str, t, shape, dtype):
+    """Pointer of a dense tensor.  The library sees pointers and sizes only: a tensor of another
+    shape or type is caught here."""
     if t is None:
-        return None, 0
+        return None
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        _refuse(name, t, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous CUDA tensors")
+    return t.data_ptr()
+
+
+def _rows(name: str, t, shape, dtype, row: int):
+    """Pointer and row stride (elements) of a tensor whose rows -- everything past the first
+    dimension, ``row`` elements -- are dense; the rows themselves may lie apart, as in a slice of a
+    projection."""
+    if t is None:
+        return None, row
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        _refuse(name, t, shape, dtype)
+    if t.is_contiguous():
+        return t.data_ptr(), row
     dense = 1
     for n, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if n != 1 and stride != dense:
             raise ValueError("the rows of tensors passed to the library must be dense")
         dense *= n
-    if not t.is_cuda:
-        raise ValueError("tensors passed to the library must be CUDA tensors")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else dense
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else row
 
 
-def _same(what: str, t, shape, dtype=None) -> None:
-    """The library sees pointers and sizes only: a tensor of another shape or type is caught here."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
-        raise ValueError(f"{what}: expected {tuple(shape)} {dtype or ''}, got {tuple(t.shape)} {t.dtype}")
+# The current stream's handle without building a Stream object (3 us of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -375,8 +396,9 @@ def tv_linear_attn_workspace_size(B, T, max_len, H, dk, dv, io_dtype=torch.bfloa
 
 def _alpha(alpha, n, H):
     """One decay per head, [H], or per token and head, [n, H]."""
-    _same("alpha", alpha, (H,) if alpha.dim() == 1 else (n, H), torch.float32)
-    return (_ptr(alpha), 0) if alpha.dim() == 1 else _rows(alpha)
+    if alpha.dim() == 1:
+        return _whole("alpha", alpha, (H,), torch.float32), 0
+    return _rows("alpha", alpha, (n, H), torch.float32, H)
 
 
 def tv_linear_attn_prompt(q, k, v, alpha, cu_seqlens, out, S, err, S0=None, max_len: int | None = None,
@@ -388,24 +410,29 @@ def tv_linear_attn_prompt(q, k, v, alpha, cu_seqlens, out, S, err, S0=None, max_
     T, H, dv = v.shape
     Hk, dk = q.shape[1:]
     B = cu_seqlens.shape[0] - 1
-    for name, t, shape, dtype in (("q", q, (T, Hk, dk), v.dtype), ("k", k, (T, Hk, dk), v.dtype),
-                                  ("out", out, (T, H, dv), v.dtype), ("S", S, (B, H, dv, dk), None),
-                                  ("S0", S0, (B, H, dv, dk), S.dtype), ("cu_seqlens", cu_seqlens, (B + 1,), torch.int32),
-                                  ("err", err, (B,), torch.int32)):
-        _same(name, t, shape, dtype)
-    (pq, sq), (pk, sk), (pv, sv), (po, so), (pa, sa) = _rows(q), _rows(k), _rows(v), _rows(out), _alpha(alpha, T, H)
+    io, state, keys, values, states = v.dtype, S.dtype, (T, Hk, dk), (T, H, dv), (B, H, dv, dk)
+    pq, sq = _rows("q", q, keys, io, Hk * dk)
+    pk, sk = _rows("k", k, keys, io, Hk * dk)
+    pv, sv = _rows("v", v, values, io, H * dv)
+    po, so = _rows("out", out, values, io, H * dv)
+    pa, sa = _alpha(alpha, T, H)
     max_len = T if max_len is None else int(max_len)
+    size = 0
     if workspace is None:
-        need = lib.tv_linear_attn_workspace_size(B, T, min(max_len, T), H, dk, dv, _DTYPES[v.dtype])
-        if need:
-            on = torch.cuda.current_stream() if stream is None else stream
-            with torch.cuda.stream(on):
-                workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        size = lib.tv_linear_attn_workspace_size(B, T, max_len, H, dk, dv, _DTYPES[io])
+        if size:
+            if stream is None:
+                workspace = torch.empty(size, dtype=torch.uint8, device=v.device)
+            else:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(size, dtype=torch.uint8, device=v.device)
+    else:
+        size = workspace.numel() * workspace.element_size()
     _check(lib.tv_linear_attn_prompt(
-        pq, sq, pk, sk, pv, sv, pa, sa, _ptr(S0), _ptr(cu_seqlens), B, T, max_len, Hk, H, dk, dv, _DTYPES[v.dtype],
-        _DTYPES[S.dtype], float(q_scale), po, so, _ptr(S), _ptr(workspace), size, _ptr(err), _stream(stream)),
-        "tv_linear_attn_prompt")
+        pq, sq, pk, sk, pv, sv, pa, sa, _whole("S0", S0, states, state),
+        _whole("cu_seqlens", cu_seqlens, (B + 1,), torch.int32), B, T, max_len, Hk, H, dk, dv, _DTYPES[io],
+        _DTYPES[state], q_scale, po, so, _whole("S", S, states, state), _ptr(workspace), size,
+        _whole("err", err, (B,), torch.int32), _stream(stream)), "tv_linear_attn_prompt")
 
 
 def tv_linear_attn_step(q, k, v, alpha, S, out, live=None, q_scale: float = 1.0, stream=None) -> None:
@@ -413,44 +440,44 @@ def tv_linear_attn_step(q, k, v, alpha, S, out, live=None, q_scale: float = 1.0,
     alpha [B, H] or [H]; sequences with live[b] = 0 are left alone."""
     B, H, dv = v.shape
     Hk, dk = q.shape[1:]
-    for name, t, shape, dtype in (("q", q, (B, Hk, dk), v.dtype), ("k", k, (B, Hk, dk), v.dtype),
-                                  ("out", out, (B, H, dv), v.dtype), ("S", S, (B, H, dv, dk), None),
-                                  ("live", live, (B,), torch.int32)):
-        _same(name, t, shape, dtype)
-    (pq, sq), (pk, sk), (pv, sv), (po, so), (pa, sa) = _rows(q), _rows(k), _rows(v), _rows(out), _alpha(alpha, B, H)
+    io, state, keys, values = v.dtype, S.dtype, (B, Hk, dk), (B, H, dv)
+    pq, sq = _rows("q", q, keys, io, Hk * dk)
+    pk, sk = _rows("k", k, keys, io, Hk * dk)
+    pv, sv = _rows("v", v, values, io, H * dv)
+    po, so = _rows("out", out, values, io, H * dv)
+    pa, sa = _alpha(alpha, B, H)
     _check(lib.tv_linear_attn_step(
-        pq, sq, pk, sk, pv, sv, pa, sa, _ptr(live), B, Hk, H, dk, dv, _DTYPES[v.dtype], _DTYPES[S.dtype],
-        float(q_scale), po, so, _ptr(S), _stream(stream)), "tv_linear_attn_step")
+        pq, sq, pk, sk, pv, sv, pa, sa, _whole("live", live, (B,), torch.int32), B, Hk, H, dk, dv, _DTYPES[io],
+        _DTYPES[state], q_scale, po, so, _whole("S", S, (B, H, dv, dk), state), _stream(stream)), "tv_linear_attn_step")
 
 
 def tv_gated_rmsnorm(x, gate, weight, out, eps: float, gate_first: bool = False, weight_offset: float = 0.0,
                      stream=None) -> None:
     """x, gate, out [rows, H, d] (row stride free): rmsnorm over d, times silu(gate); with
     ``gate_first`` the norm is taken of x * silu(gate).  gate and weight [d] may be None."""
-    rows, H, d = x.shape
-    for name, t, shape in (("gate", gate, x.shape), ("out", out, x.shape), ("weight", weight, (d,))):
-        _same(name, t, shape, x.dtype)
-    (px, sx), (pg, sg), (po, so) = _rows(x), _rows(gate), _rows(out)
-    _check(lib.tv_gated_rmsnorm(px, sx, pg, sg, _ptr(weight), rows, H, d, _DTYPES[x.dtype], float(eps),
-                                float(weight_offset), int(bool(gate_first)), po, so, _stream(stream)),
-           "tv_gated_rmsnorm")
+    shape, io = x.shape, x.dtype
+    rows, H, d = shape
+    px, sx = _rows("x", x, shape, io, H * d)
+    pg, sg = _rows("gate", gate, shape, io, H * d)
+    po, so = _rows("out", out, shape, io, H * d)
+    _check(lib.tv_gated_rmsnorm(px, sx, pg, sg, _whole("weight", weight, (d,), io), rows, H, d, _DTYPES[io], eps,
+                                weight_offset, int(gate_first), po, so, _stream(stream)), "tv_gated_rmsnorm")
 
 
 def tv_residual_rmsnorm(y, residual, residual_out, eps: float, out=None, weight=None, post_weight=None, gate=None,
                         scale: float = 1.0, weight_offset: float = 0.0, stream=None) -> None:
     """residual_out = residual + scale * gate * (y, or rmsnorm(y) with post_weight); out (optional) =
     rmsnorm(residual_out) with weight.  All [rows, D] (row stride free), weights [D]."""
-    rows, D = y.shape
-    for name, t, shape, dtype in (("residual", residual, (rows, D), None), ("out", out, (rows, D), y.dtype),
-                                  ("residual_out", residual_out, (rows, D), residual.dtype),
-                                  ("gate", gate, (rows, D), y.dtype), ("weight", weight, (D,), y.dtype),
-                                  ("post_weight", post_weight, (D,), y.dtype)):
-        _same(name, t, shape, dtype)
-    (py, sy), (pr, sr), (pg, sg), (pro, sro), (po, so) = (_rows(y), _rows(residual), _rows(gate), _rows(residual_out),
-                                                          _rows(out))
-    _check(lib.tv_residual_rmsnorm(py, sy, pr, sr, _ptr(post_weight), pg, sg, float(scale), _ptr(weight), rows, D,
-                                   _DTYPES[y.dtype], _DTYPES[residual.dtype], float(eps), float(weight_offset), pro,
-                                   sro, po, so, _stream(stream)), "tv_residual_rmsnorm")
+    shape, io, res = y.shape, y.dtype, residual.dtype
+    rows, D = shape
+    py, sy = _rows("y", y, shape, io, D)
+    pr, sr = _rows("residual", residual, shape, res, D)
+    pg, sg = _rows("gate", gate, shape, io, D)
+    pro, sro = _rows("residual_out", residual_out, shape, res, D)
+    po, so = _rows("out", out, shape, io, D)
+    _check(lib.tv_residual_rmsnorm(py, sy, pr, sr, _whole("post_weight", post_weight, (D,), io), pg, sg, scale,
+                                   _whole("weight", weight, (D,), io), rows, D, _DTYPES[io], _DTYPES[res], eps,
+                                   weight_offset, pro, sro, po, so, _stream(stream)), "tv_residual_rmsnorm")
 
 
 def tv_test_bounded_wait(max_polls: int, arrive: bool, status, elapsed_ns, stream=None) -> None:
