@@ -524,7 +524,10 @@ TV_API int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, c
  *                                           decay for each head
  *   S0          [B, H, dv, dk] state_dtype  in   state before the prompt; NULL: zero
  *   cu_seqlens  [B + 1] int32          in
- *   max_len     an upper bound of the prompts' lengths (T serves; closer is faster)
+ *   max_len     an upper bound of the prompts' lengths (T serves; closer is faster).  Long prompts
+ *               are cut into segments that run side by side; where depends on the sizes and max_len,
+ *               and with it the order of some sums: results of calls that agree in those are equal
+ *               bit for bit
  *   out         [T, H, dv]  io_dtype   out  rows of no prompt are not written
  *   S           [B, H, dv, dk] state_dtype  out  state after the prompt; may be S0 itself
  *   workspace   device scratch of at least tv_linear_attn_workspace_size(...) bytes, 16-byte

@@ -102,7 +102,7 @@ def test_prompt_lengths(io, state, lens):
 def test_long_prompt_on_few_heads(io, state):
     # far more tokens than heads: the prompt is cut into segments; the shorter ones are not
     c = make([5003, 70, 0, 1200], 1, 2, 128, 128, io, state, seed=5)
-    out, S, err = prompt(c)
+    out, S, err = prompt(c, max_len=5003)
     check_prompt(c, out, S, err)
     again, S2, _ = prompt(c, in_place=True, max_len=5003)
     assert torch.equal(out, again) and torch.equal(S, S2)      # S may be S0 itself, cut or not

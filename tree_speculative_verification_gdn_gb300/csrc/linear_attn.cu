@@ -7,6 +7,9 @@
 //
 // Row r of S needs k_t, q_t, alpha_t and v_t[r] only, so rows are independent: a CTA of the prompt
 // kernel keeps kRows rows in registers, eight lanes a row, and walks the tokens.
+#include <algorithm>
+#include <type_traits>
+
 #include "linear_attn.cuh"
 
 namespace tv {
@@ -149,18 +152,19 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
     if (tid < kBlock) s_a[tid] = ra;
     __syncthreads();
     if (t + kBlock < seg.t1) fetch(t + kBlock);
-#pragma unroll
-    for (int u = 0; u < kBlock; u += 8) {
+    // Eight tokens; with SOME only those of the segment.
+    auto walk = [&](int u, auto some) {
+      constexpr bool SOME = decltype(some)::value;
       float dot[kRPL][8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int r = 0; r < kRPL; ++r) dot[r][i] = 0.f;
+        if (SOME && t + u + i >= seg.t1) continue;  // the same for the whole CTA
         const float al = s_a[u + i];
         float v[kRPL];
 #pragma unroll
-        for (int r = 0; r < kRPL; ++r) {
-          v[r] = s_v[u + i][row0 + r];
-          dot[r][i] = 0.f;
-        }
+        for (int r = 0; r < kRPL; ++r) v[r] = s_v[u + i][row0 + r];
         if (STATE_ONLY) total *= al;
 #pragma unroll
         for (int j = 0; j < CPL / 4; ++j) {
@@ -182,6 +186,11 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
       if (!STATE_ONLY)
 #pragma unroll
         for (int r = 0; r < kRPL; ++r) s_o[u + l][row0 + r] = sum8(dot[r], l) * a.q_scale;
+    };
+#pragma unroll 1
+    for (int u = 0; u < kBlock && t + u < seg.t1; u += 8) {
+      if (t + u + 8 <= seg.t1) walk(u, std::false_type());
+      else walk(u, std::true_type());
     }
     if (!STATE_ONLY) {
       __syncthreads();
@@ -309,15 +318,27 @@ cudaError_t step_dims(const LinStepArgs& a, cudaStream_t s) {
 }  // namespace
 
 int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io) {
-  (void)B; (void)dk;
+  (void)dk;
   const int sms = device_sm_count();
   if (io == TV_BF16) {
-    // One CTA per SM walks whole (segment, head) units: cut when the longest prompt alone takes over
-    // twice the balanced time, into as many pieces as make two rounds of units.
-    if ((long long)max_len * sms <= 2LL * T * H) return 0;
-    const int pieces = 2 * sms / H > 1 ? 2 * sms / H : 1;
-    const int seg = ((T + pieces - 1) / pieces + 127) / 128 * 128;
-    return max_len > seg ? seg : 0;
+    // One CTA per SM walks whole (segment, head) units.  Measured on a GB300, in us: a unit costs 5 and
+    // 3.6 a chunk of 128 tokens, in the pass over states alone 5 and 1.8; a launch 4, the scan 3 and
+    // 0.5 a segment.  The cheapest cut of the longest prompt into equal pieces, or none.  (16 heads, one
+    // prompt: 768 tokens 27 uncut and 30 in pieces of 256; 4096 tokens 109 uncut, 50 in pieces of 512.)
+    const int longest = (max_len + 127) / 128;
+    auto cost = [&](int chunks) {
+      const long long units = (long long)H * std::max<long long>(B, (T / 128 + chunks - 1) / chunks);
+      const long long rounds = (units + sms - 1) / sms;
+      const double whole = 4 + rounds * (5 + 3.6 * chunks);
+      if (chunks >= longest) return whole;
+      return whole + 4 + rounds * (5 + 1.8 * chunks) + 3 + 0.5 * ((longest + chunks - 1) / chunks);
+    };
+    int best = longest;
+    for (int pieces = 2; pieces <= 64 && longest / pieces > 1; ++pieces) {
+      const int chunks = (longest + pieces - 1) / pieces;
+      if (cost(chunks) < 0.9 * cost(best)) best = chunks;
+    }
+    return best < longest ? best * 128 : 0;
   }
   long long seg = ((long long)T * H * (dv / kRows) + 4 * sms - 1) / (4 * sms);
   seg = (seg + 127) / 128 * 128;

@@ -59,16 +59,38 @@ __device__ __forceinline__ float row_sum(float x, float* s_part) {
   }
 }
 
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
+// The exponential to the precision that the element type can show: bf16 keeps 2^-8 of a value, the
+// hardware's 2^x is good to 2^-21 of it where the gate is not yet 0 or 1.
+__device__ __forceinline__ float exp_for(float x, bf16) { return __expf(x); }
+__device__ __forceinline__ float exp_for(float x, float) { return expf(x); }
+template <typename T>
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + exp_for(-g, T())); }
 
+// id / H for ids below 2^31, by a multiplication: the quotient of every thread's row cost as much as
+// half its arithmetic.
+struct Divide {
+  unsigned mul, shift;
+};
+Divide divide_by(int H) {
+  unsigned s = 0;
+  while ((1u << s) < (unsigned)H) ++s;  // 2^s >= H
+  return {s == 0 ? 0u : (unsigned)((1ull << (31 + s)) / H + 1), s};
+}
+__device__ __forceinline__ int quotient(int id, Divide by) {
+  return by.shift == 0 ? id : (int)(__umulhi((unsigned)id, by.mul) >> (by.shift - 1));
+}
+
+// G > 0: G lanes a row, one vector each, eight blocks on an SM to keep 64 KB of loads in flight
+// (40001 x 32 rows of 128 bf16: 220 us without the bound on registers; two rows a thread 205 us).
+// G = 0: a block a row, VPT vectors a thread.
 template <typename T, int G, int VPT, bool FULL>
-__global__ void __launch_bounds__(G == 0 ? 1024 : 256) gated_rmsnorm_kernel(GatedNormArgs a) {
+__global__ void __launch_bounds__(G == 0 ? 1024 : 256, G == 0 ? 1 : 8) gated_rmsnorm_kernel(GatedNormArgs a, Divide by) {
   __shared__ float s_part[32];
   const int per = G > 0 ? G : blockDim.x;
   const int id = G > 0 ? blockIdx.x * (256 / (G > 0 ? G : 1)) + threadIdx.x / per : blockIdx.x;
   const int l = G > 0 ? threadIdx.x % per : threadIdx.x;
   const bool in = id < a.rows * a.H;  // every lane stays for the sums
-  const int r = in ? id / a.H : 0, h = in ? id % a.H : 0;
+  const int r = in ? quotient(id, by) : 0, h = in ? id - r * a.H : 0;
   const int n = in ? a.d : 0;
   const T* x = static_cast<const T*>(a.x) + r * a.x_stride + (long long)h * a.d;
   const T* gate = a.gate != nullptr ? static_cast<const T*>(a.gate) + r * a.gate_stride + (long long)h * a.d : nullptr;
@@ -88,7 +110,7 @@ __global__ void __launch_bounds__(G == 0 ? 1024 : 256) gated_rmsnorm_kernel(Gate
     if ((l + j * per) * 8 - phase >= n) continue;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      g[j][i] = gate != nullptr ? silu(g[j][i]) : 1.f;
+      g[j][i] = gate != nullptr ? silu<T>(g[j][i]) : 1.f;
       if (a.gate_first) v[j][i] *= g[j][i];
       sum = fmaf(v[j][i], v[j][i], sum);
     }
@@ -185,10 +207,11 @@ bool rows16(const void* p, long long stride, int dtype) {
 
 template <typename T, int G, int VPT>
 cudaError_t gated_go(const GatedNormArgs& a, bool full, int block, cudaStream_t s) {
-  const long long n = (long long)a.rows * a.H;
-  const unsigned grid = (unsigned)(G > 0 ? (n + 256 / (G > 0 ? G : 1) - 1) / (256 / (G > 0 ? G : 1)) : n);
-  if (full) gated_rmsnorm_kernel<T, G, VPT, true><<<grid, block, 0, s>>>(a);
-  else gated_rmsnorm_kernel<T, G, VPT, false><<<grid, block, 0, s>>>(a);
+  constexpr int per = G > 0 ? 256 / (G > 0 ? G : 1) : 1;
+  const unsigned grid = (unsigned)(((long long)a.rows * a.H + per - 1) / per);
+  const Divide by = divide_by(a.H);
+  if (full) gated_rmsnorm_kernel<T, G, VPT, true><<<grid, block, 0, s>>>(a, by);
+  else gated_rmsnorm_kernel<T, G, VPT, false><<<grid, block, 0, s>>>(a, by);
   return cudaGetLastError();
 }
 
