@@ -492,14 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (rows < kC) {
           if (!(good = wait(sh, &sh.v_full[place<L::nv>(n)], turn<L::nv>(n)))) break;
-          uint4* kt = reinterpret_cast<uint4*>(k_tile);
-          uint4* vt = reinterpret_cast<uint4*>(smem + L::at_v + place<L::nv>(n) * L::v);
+          auto clear = [&](unsigned char* tile, int columns) {  // eight 16-byte pieces a row and 64 columns
 #pragma unroll 1
-          for (int i = r; i < kC * DK / 8; i += 128)
-            if (i / 8 % kC >= rows) kt[i] = make_uint4(0, 0, 0, 0);
+            for (int half = 0; half < columns / 64; ++half)
 #pragma unroll 1
-          for (int i = r; i < kC * DV / 8; i += 128)
-            if (i / 8 % kC >= rows) vt[i] = make_uint4(0, 0, 0, 0);
+              for (int i = rows * 8 + r; i < kC * 8; i += 128)
+                reinterpret_cast<uint4*>(tile + half * kHalf)[i] = make_uint4(0, 0, 0, 0);
+          };
+          clear(k_tile, DK);
+          clear(smem + L::at_v + place<L::nv>(n) * L::v, DV);
           fence_proxy_async();
           asm volatile("bar.sync 1, 128;" ::: "memory");
         }
