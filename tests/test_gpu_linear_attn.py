@@ -110,6 +110,13 @@ def test_long_prompt_on_few_heads(io, state):
     check_prompt(c, *prompt(c, S0=None), S0=False)
 
 
+@pytest.mark.parametrize("lens,H", [([4096], 16), ([1500, 900, 0, 600], 12)])
+def test_fewer_segments_than_the_host_can_bound(lens, H):
+    # the launch is sized by B + T / segment; the CTAs past the real segments find nothing to do
+    c = make(lens, H, H, 64, 64, "bf16", "f32", seed=sum(lens))
+    check_prompt(c, *prompt(c, S0=None), S0=False)
+
+
 def test_prompt_in_place_many_heads():
     c = make([300, 41], 16, 32, 128, 128, seed=8)
     out, S, err = prompt(c)

@@ -20,7 +20,7 @@ __device__ __forceinline__ bool check_seqlens(const LinAttnArgs& a) {
 }
 
 struct Segment {
-  int b;        // prompt; -1: no such segment
+  int b;        // prompt; -1: no such segment (empty, the other fields set)
   int h;        // value head
   int index;    // segment of the prompt
   int count;    // segments of the prompt
@@ -35,9 +35,7 @@ __device__ __forceinline__ int segments_of(int len, int seg_len) {
 // the same answer in every lane; cu_seqlens has passed check_seqlens.
 static __device__ __noinline__ Segment find_segment(const LinAttnArgs& a, int u) {
   const int g = u / a.H;
-  Segment s;
-  s.b = -1;
-  s.h = u - g * a.H;
+  Segment s{-1, u - g * a.H, 0, 1, 0, 0};
   if (a.seg_len == 0) {
     if (g < a.B) {
       s.b = g;

@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kC = 128;          // tokens per chunk
 constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two TMA warps
+constexpr int kAhead = kC;       // tokens by which tiles are brought to L2 before they are loaded
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
@@ -556,43 +557,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     const bool keys = warp == 19;
-    // Tiles go to L2 a chunk before they are loaded, those of the next unit too.
-    auto ahead = [&](const CUtensorMap* map, int columns, int h, int t) {
-      if (lane == 0) {
-        tma_prefetch_3d(map, 0, h, t);
-        if (columns > 64) tma_prefetch_3d(map, 64, h, t);
-      }
-    };
-    auto ahead_of = [&](const Segment& seg, int t) {
-      if (seg.b < 0 || t >= seg.t1) return;
-      const int hk = seg.h / (a.H / a.Hk);
-      if (keys) {
-        ahead(&mk, DK, hk, t);
-      } else {
-        ahead(&mv, DV, seg.h, t);
-        if (!STATE_ONLY) ahead(&mq, DK, hk, t);
-      }
-    };
     int loads = 0, v_loads = 0;  // of K or Q, of V
-    int u = blockIdx.x;
-    Segment seg = find_segment(a, u);
 #pragma unroll 1
-    while (seg.b >= 0 && good) {
-      u += gridDim.x;
-      const Segment after = u < units ? find_segment(a, u) : Segment{-1, 0, 0, 0, 0, 0};
+    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+      const Segment seg = find_segment(a, u);
+      if (seg.b < 0) break;
+      if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const int h = seg.h, hk = h / (a.H / a.Hk);
-      const int end = STATE_ONLY && seg.index + 1 == seg.count ? seg.t0 : seg.t1;
+      auto ahead = [&](const CUtensorMap* map, int columns, int h, int t) {
+        if (t < seg.t1 && lane == 0) {
+          tma_prefetch_3d(map, 0, h, t);
+          if (columns > 64) tma_prefetch_3d(map, 64, h, t);
+        }
+      };
 #pragma unroll 1
-      for (int t = seg.t0; t < end; t += kC, ++n) {
-        const bool more = t + kC < end;
-        ahead_of(more ? seg : after, more ? t + kC : after.t0);
+      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
         if (keys) {
           const int i = place<L::nk>(n);
+          ahead(&mk, DK, hk, t + kAhead);
           if (n >= L::nk && !(good = wait(sh, &sh.k_empty[i], turn<L::nk>(n) ^ 1))) break;
           load(&mk, smem + L::at_k + i * L::k, DK, hk, t, &sh.k_full[i]);
           loads = n + 1;
         } else {
           const int i = place<L::nv>(n);
+          ahead(&mv, DV, h, t + kAhead);
+          if (!STATE_ONLY) ahead(&mq, DK, hk, t + kAhead);
           if (n >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(n) ^ 1))) break;
           load(&mv, smem + L::at_v + i * L::v, DV, h, t, &sh.v_full[i]);
           v_loads = n + 1;
@@ -604,7 +593,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      seg = after;
     }
     if (!good)  // leave no copy in flight behind: the last ones of each kind
 #pragma unroll 1
@@ -717,31 +705,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------ decays: four sums of 32 tokens side by side
-    float next[4];  // the next chunk's decays, on their way
-    auto fetch = [&](const Segment& seg, int t) {
+#pragma unroll 1
+    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+      const Segment seg = find_segment(a, u);
+      if (seg.b < 0) break;
+      if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const float* al = a.alpha + seg.h;
+      float next[4];  // the next chunk's decays, on their way
+      auto fetch = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = t + 32 * i + lane;  // past the prompt's end nothing decays
-        next[i] = seg.b >= 0 && tok < seg.t1 ? __ldg(al + tok * a.alpha_stride) : 1.f;
-      }
-    };
-    int u = blockIdx.x;
-    Segment seg = find_segment(a, u);
-    fetch(seg, seg.t0);
+        for (int i = 0; i < 4; ++i) {
+          const int tok = t + 32 * i + lane;  // past the prompt's end nothing decays
+          next[i] = tok < seg.t1 ? __ldg(al + tok * a.alpha_stride) : 1.f;
+        }
+      };
+      fetch(seg.t0);
 #pragma unroll 1
-    while (seg.b >= 0 && good) {
-      u += gridDim.x;
-      const Segment after = u < units ? find_segment(a, u) : Segment{-1, 0, 0, 0, 0, 0};
-      const int end = STATE_ONLY && seg.index + 1 == seg.count ? seg.t0 : seg.t1;
-      if (end == seg.t0) fetch(after, after.t0);
-#pragma unroll 1
-      for (int t = seg.t0; t < end; t += kC, ++n) {
+      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
         float2 sum[4];
         // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = make_float2(next[i] == 0.f ? -1000.f : log2f(next[i]), 0.f);
-        fetch(t + kC < end ? seg : after, t + kC < end ? t + kC : after.t0);
+        if (t + kC < seg.t1) fetch(t + kC);
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
@@ -762,7 +747,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
       }
-      seg = after;
     }
   }
   __syncwarp();
