@@ -13,7 +13,9 @@
 //     PV: O, added to                    A = P,    B = V       (bf16 pair, tensor memory, over the scores)
 // P, K' and S are fp32 results and enter as value + remainder, two bf16 each (2^-16 left out): one
 // bf16 alone would put an error as large as the output's own rounding on every output, and 2^-9 on
-// an fp32 state.  Exponents only ever go down: within 32 x 32 diagonal blocks each 2^(g_i - g_j) is
+// an fp32 state.  (A third part of K' was tried for fp32 states and left out: their error stayed near
+// 3e-6, since the matrix units cut what they add to an accumulator instead of rounding it, and the third
+// part's products add to that; it cost a quarter of the time.)  Exponents only ever go down: within 32 x 32 diagonal blocks each 2^(g_i - g_j) is
 // taken directly, elsewhere as 2^(g_i - g_r) 2^(g_r - g_j) with r the first row of i's block, so no
 // factor exceeds 1 however fast the decay.  g is summed and kept as two floats: after a reset (alpha
 // near 0) small differences of large sums remain.
@@ -51,10 +53,11 @@ constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 struct Shared {
   float2 g[2][kC];  // g_i as two floats, by chunk parity
   float f[192];     // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
-  uint64_t q_full[2], q_empty[2], k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t g_full[2], g_empty[2];
   uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
   uint64_t s_ready, k_ready, p_ready, o_ready, o_free;  // operands written, outputs read
+  uint64_t o_meet, k_meet;                              // the warps of a role among themselves
   uint64_t drain;
   uint32_t tmem;
   int fail;
@@ -64,7 +67,7 @@ template <int DK, int DV, bool STATE_ONLY>
 struct Plan {
   static constexpr int k = kC * 2 * DK, v = kC * 2 * DV;  // bytes of a tile
   static constexpr int q = k > v ? k : v;                 // outputs leave through it
-  static constexpr int nq = STATE_ONLY ? 0 : 2, nk = STATE_ONLY ? 3 : DK + DV == 256 ? 1 : 2, nv = STATE_ONLY ? 3 : 2;
+  static constexpr int nq = STATE_ONLY ? 0 : 2, nk = !STATE_ONLY && DK + DV == 256 ? 1 : 2, nv = 2;
   static constexpr int at_k = nq * q, at_v = at_k + nk * k, at_s = at_v + nv * v;
   static constexpr int s = STATE_ONLY ? 0 : DV * DK * 2;  // the state's bf16 values; as much for its remainders
   static constexpr int bytes = at_s + 2 * s + (int)sizeof(Shared);
@@ -113,6 +116,12 @@ __device__ __noinline__ bool wait_more(Shared& sh, uint64_t* bar, uint32_t parit
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
   if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
   return wait_more(sh, bar, parity);
+}
+// All 128 threads of a role, by a wait that ends as the others do (a named barrier would wait for ever
+// for a warp that gave up).
+__device__ __forceinline__ bool meet(Shared& sh, uint64_t* bar, uint32_t& times) {
+  mbar_arrive(bar);
+  return wait(sh, bar, times++ & 1);
 }
 // The library's wait, out of line: for the paths after a wait gave up.
 __device__ __noinline__ void wait_out(uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity); }
@@ -197,8 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok) return;
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) {
-      if (i < 2) mbar_init(&sh.q_full[i], 1), mbar_init(&sh.q_empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], 4);
       mbar_init(&sh.v_full[i], 1);
@@ -217,6 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.p_ready, 128);
     mbar_init(&sh.o_ready, 128);
     mbar_init(&sh.o_free, 128);
+    mbar_init(&sh.o_meet, 128);
+    mbar_init(&sh.k_meet, 128);
     mbar_init(&sh.drain, 1);
     sh.fail = 0;
     mbar_fence_init();
@@ -230,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Every role walks the same units and chunks; n counts chunks over all units.
   int n = 0;
+  uint32_t met = 0;  // times the role's warps have met
   bool good = true;
   if (warp < 4) {
     // ------------------------------------------------ scores to P (thread = token)
@@ -355,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(o + c / 8 * kHalf + r * 128 + ((c % 8) ^ (r & 7)) * 16) =
                   make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             fence_proxy_async();
-            asm volatile("bar.sync 2, 128;" ::: "memory");
+            if (!(good = meet(sh, &sh.o_meet, met))) break;
             if (r == 0) {
 #pragma unroll
               for (int c = 0; c < DV; c += 64) tma_store_3d(&mo, c, seg.h, t, o + c / 64 * kHalf);
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           clear(k_tile, DK);
           clear(smem + L::at_v + place<L::nv>(n) * L::v, DV);
           fence_proxy_async();
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (!(good = meet(sh, &sh.k_meet, met))) break;
         }
         if (mine) {
           const float2 gc = g[kC - 1];
@@ -596,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!good)  // leave no copy in flight behind: the last ones of each kind
 #pragma unroll 1
-      for (int i = 1; i <= 3; ++i) {
+      for (int i = 1; i <= 2; ++i) {
         if (keys && i <= L::nk && loads >= i) wait_out(&sh.k_full[place<L::nk>(loads - i)], turn<L::nk>(loads - i));
         if (!keys && i <= L::nq && loads >= i) wait_out(&sh.q_full[place<2>(loads - i)], turn<2>(loads - i));
         if (!keys && i <= L::nv && v_loads >= i) wait_out(&sh.v_full[place<L::nv>(v_loads - i)], turn<L::nv>(v_loads - i));
