@@ -26,12 +26,13 @@
 // memory.
 //
 // Twenty warps: four turn scores into P (thread = token), four scale and write outputs (thread =
-// token), four own the state (thread = key column), four scale the keys; one loads Q and V, one K, one
-// issues the MMAs, one sums the decays.  Two tiles of Q, one of K (free again as soon as the scores and K'
-// have read it; the next one waits for it in L2) and two of V are in flight; a chunk's outputs leave through its Q tile by a TMA store
-// (stores of a row by each thread held up every other shared-memory access of the SM).  One CTA per SM,
-// since five 32 KB tiles and the state's bf16 pair fill shared memory.  A chunk runs every role's code once, and together it has to stay in the
-// instruction cache: hence loops that are not unrolled and waits that are not inlined.
+// token), four own the state (thread = key column), four scale the keys; one loads K and Q, one V, one
+// issues the MMAs, one sums the decays.  K and Q tiles take turns in a ring of three (K goes back when
+// the scores and K' have read it, Q when QS has), V has two; a chunk's outputs leave through its V tile
+// by a TMA store (stores of a row by each thread held up every other shared-memory access of the SM).
+// (Bringing tiles to L2 a chunk ahead made no difference with this ring.)  One CTA per SM, since five 32 KB tiles and the state's bf16
+// pair fill shared memory.  A chunk runs every role's code once, and together it has to stay near the
+// instruction cache: hence loops that are not unrolled, and only the first look of a wait inline.
 #include "linear_attn.cuh"
 #include "tv_async.cuh"
 #include "tv_tc.cuh"
@@ -42,7 +43,6 @@ namespace {
 
 constexpr int kC = 128;          // tokens per chunk
 constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two TMA warps
-constexpr int kAhead = kC;       // tokens by which tiles are brought to L2 before they are loaded
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
@@ -53,7 +53,7 @@ constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 struct Shared {
   float2 g[2][kC];  // g_i as two floats, by chunk parity
   float f[192];     // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
-  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t kq_full[3], kq_empty[3], v_full[2], v_empty[2];
   uint64_t g_full[2], g_empty[2];
   uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
   uint64_t s_ready, k_ready, p_ready, o_ready, o_free;  // operands written, outputs read
@@ -65,20 +65,20 @@ struct Shared {
 
 template <int DK, int DV, bool STATE_ONLY>
 struct Plan {
-  static constexpr int k = kC * 2 * DK, v = kC * 2 * DV;  // bytes of a tile
-  static constexpr int q = k > v ? k : v;                 // outputs leave through it
-  static constexpr int nq = STATE_ONLY ? 0 : 2, nk = !STATE_ONLY && DK + DV == 256 ? 1 : 2, nv = 2;
-  static constexpr int at_k = nq * q, at_v = at_k + nk * k, at_s = at_v + nv * v;
+  static constexpr int k = kC * 2 * DK, v = kC * 2 * DV;  // bytes of a tile of K or Q, of V
+  static constexpr int nk = 3, nv = 2;                    // tiles in flight
+  static constexpr int step = STATE_ONLY ? 1 : 2;         // a chunk's tiles in the ring: K, Q
+  static constexpr int at_v = nk * k, at_s = at_v + nv * v;
   static constexpr int s = STATE_ONLY ? 0 : DV * DK * 2;  // the state's bf16 values; as much for its remainders
   static constexpr int bytes = at_s + 2 * s + (int)sizeof(Shared);
   static_assert(bytes <= kSmemMax, "fits an SM");
 };
 
-// A chunk's place among N tiles, and the parity of that place's use.
+// Place of tile i in a ring of N, and the parity of that place's use.
 template <int N>
-__device__ __forceinline__ int place(int n) { return N > 1 ? n % N : 0; }
+__device__ __forceinline__ int place(int i) { return i % N; }
 template <int N>
-__device__ __forceinline__ uint32_t turn(int n) { return (n / (N > 0 ? N : 1)) & 1; }
+__device__ __forceinline__ uint32_t turn(int i) { return (i / N) & 1; }
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -206,13 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok) return;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 4);
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sh.kq_full[i], 1);
+      mbar_init(&sh.kq_empty[i], 1);
+      if (i < L::nv) mbar_init(&sh.v_full[i], 1), mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.g_full[i], 1);
@@ -359,10 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           mbar_arrive(&sh.o_free);
-          // PV has run, so QK and QS of this chunk have read its Q tile.
-          const int slot = place<2>(n);
+          // PV has run, and ST before it: nobody reads this chunk's V tile any more.
+          const int slot = place<L::nv>(n);
           if (t + kC <= seg.t1) {
-            unsigned char* o = smem + slot * L::q;
+            unsigned char* o = smem + L::at_v + slot * L::v;
 #pragma unroll
             for (int c = 0; c < DV / 8; ++c)
               *reinterpret_cast<uint4*>(o + c / 8 * kHalf + r * 128 + ((c % 8) ^ (r & 7)) * 16) =
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < DV; c += 64) tma_store_3d(&mo, c, seg.h, t, o + c / 64 * kHalf);
               bulk_commit();
               bulk_wait_read<0>();
-              mbar_arrive(&sh.q_empty[slot]);
+              mbar_arrive(&sh.v_empty[slot]);
             }
             __syncwarp();
           } else {  // a whole tile would write into the next prompt's rows
@@ -383,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < DV / 8; ++c) o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             }
-            if (r == 0) mbar_arrive(&sh.q_empty[slot]);
+            if (r == 0) mbar_arrive(&sh.v_empty[slot]);
             __syncwarp();
           }
         }
@@ -498,10 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
         const int rows = seg.t1 - t;
-        unsigned char* k_tile = smem + L::at_k + place<L::nk>(n) * L::k;
+        const int ik = n * L::step;
+        unsigned char* k_tile = smem + place<L::nk>(ik) * L::k;
         const float2* g = sh.g[n & 1];
         if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
-        if (!(good = wait(sh, &sh.k_full[place<L::nk>(n)], turn<L::nk>(n)))) break;
+        if (!(good = wait(sh, &sh.kq_full[place<L::nk>(ik)], turn<L::nk>(ik)))) break;
         if (n > 0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;  // it has read the last K'
         tc_fence_after();
         if (rows < kC) {
@@ -554,9 +552,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.k_ready);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
-        // K is free as soon as the scores have read it too, for the next one to land in time.
-        if (!STATE_ONLY && !(good = wait(sh, &sh.qk_done, n & 1))) break;
-        if (lane == 0) mbar_arrive(&sh.k_empty[place<L::nk>(n)]);
       }
     }
   } else if (warp == 16 || warp == 19) {
@@ -569,50 +564,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    const bool keys = warp == 19;
-    int loads = 0, v_loads = 0;  // of K or Q, of V
+    const bool keys = warp == 19;  // K and Q, else V
+    int loads = 0;                 // tiles asked for
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const int h = seg.h, hk = h / (a.H / a.Hk);
-      auto ahead = [&](const CUtensorMap* map, int columns, int h, int t) {
-        if (t < seg.t1 && lane == 0) {
-          tma_prefetch_3d(map, 0, h, t);
-          if (columns > 64) tma_prefetch_3d(map, 64, h, t);
-        }
-      };
 #pragma unroll 1
-      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+      for (int t = seg.t0; t < seg.t1 && good; t += kC) {
         if (keys) {
-          const int i = place<L::nk>(n);
-          ahead(&mk, DK, hk, t + kAhead);
-          if (n >= L::nk && !(good = wait(sh, &sh.k_empty[i], turn<L::nk>(n) ^ 1))) break;
-          load(&mk, smem + L::at_k + i * L::k, DK, hk, t, &sh.k_full[i]);
-          loads = n + 1;
-        } else {
-          const int i = place<L::nv>(n);
-          ahead(&mv, DV, h, t + kAhead);
-          if (!STATE_ONLY) ahead(&mq, DK, hk, t + kAhead);
-          if (n >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(n) ^ 1))) break;
-          load(&mv, smem + L::at_v + i * L::v, DV, h, t, &sh.v_full[i]);
-          v_loads = n + 1;
-          if (!STATE_ONLY) {
-            const int iq = place<2>(n);
-            if (n >= 2 && !(good = wait(sh, &sh.q_empty[iq], turn<2>(n) ^ 1))) break;
-            load(&mq, smem + iq * L::q, DK, hk, t, &sh.q_full[iq]);
-            loads = n + 1;
+#pragma unroll 1
+          for (int tile = 0; tile < L::step; ++tile, ++loads) {
+            const int i = place<L::nk>(loads);
+            if (loads >= L::nk && !(good = wait(sh, &sh.kq_empty[i], turn<L::nk>(loads) ^ 1))) break;
+            load(tile == 0 ? &mk : &mq, smem + i * L::k, DK, hk, t, &sh.kq_full[i]);
           }
+        } else {
+          const int i = place<L::nv>(loads);
+          if (loads >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(loads) ^ 1))) break;
+          load(&mv, smem + L::at_v + i * L::v, DV, h, t, &sh.v_full[i]);
+          ++loads;
         }
       }
     }
-    if (!good)  // leave no copy in flight behind: the last ones of each kind
+    if (!good)  // leave no copy in flight behind: the last ones
 #pragma unroll 1
-      for (int i = 1; i <= 2; ++i) {
-        if (keys && i <= L::nk && loads >= i) wait_out(&sh.k_full[place<L::nk>(loads - i)], turn<L::nk>(loads - i));
-        if (!keys && i <= L::nq && loads >= i) wait_out(&sh.q_full[place<2>(loads - i)], turn<2>(loads - i));
-        if (!keys && i <= L::nv && v_loads >= i) wait_out(&sh.v_full[place<L::nv>(v_loads - i)], turn<L::nv>(v_loads - i));
+      for (int i = 1; i <= (keys ? L::nk : L::nv) && i <= loads; ++i) {
+        if (keys) wait_out(&sh.kq_full[place<L::nk>(loads - i)], turn<L::nk>(loads - i));
+        else wait_out(&sh.v_full[place<L::nv>(loads - i)], turn<L::nv>(loads - i));
       }
   } else if (warp == 17) {
     // ------------------------------------------------ MMAs
@@ -634,7 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto start = [&](int offset) { return __shfl_sync(0xffffffffu, (base + offset) >> 4, 0); };
     // Scores of chunk n, whose tiles have landed.
     auto landed = [&](int n) {
-      return wait(sh, &sh.q_full[place<2>(n)], turn<2>(n)) && wait(sh, &sh.k_full[place<L::nk>(n)], turn<L::nk>(n));
+      const int i = n * L::step;
+      return wait(sh, &sh.kq_full[place<L::nk>(i)], turn<L::nk>(i)) &&
+             wait(sh, &sh.kq_full[place<L::nk>(i + 1)], turn<L::nk>(i + 1));
     };
     auto scores = [&](uint64_t dq, uint64_t dk) {
       constexpr uint32_t id = idesc_bf16_f32(kC, kC);
@@ -645,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(&sh.qk_done);
     };
-    auto q_rows = [&](int n) { return by_rows + start(place<2>(n) * L::q); };
-    auto k_rows = [&](int n) { return by_rows + start(L::at_k + place<L::nk>(n) * L::k); };
+    auto q_rows = [&](int n) { return by_rows + start(place<L::nk>(n * L::step + 1) * L::k); };
+    auto k_rows = [&](int n) { return by_rows + start(place<L::nk>(n * L::step) * L::k); };
     int chunks, later;
     int u = find(blockIdx.x, chunks);
     if (!STATE_ONLY && u < units && (good = landed(0))) {
@@ -671,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idv = idesc_bf16_f32(kC, DV, true);
         const uint64_t dv = by_columns + start(L::at_v + iv * L::v);
         if (elect_one()) {
+          mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);  // the scores have read K, and K' is made
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -693,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_bf16(tmem + kColO, this_q + ((c / 64 * kHalf + c % 64 * 2) >> 4), state + ((part * L::s + c * 128) >> 4),
                        ids, part + c > 0);
           mma_commit(&sh.qs_done);
+          mma_commit(&sh.kq_empty[place<L::nk>(n * L::step + 1)]);
         }
         __syncwarp();
         const bool more = i + 1 < chunks || next < units;
@@ -709,7 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_bf16_tmem_a(tmem + kColO, tmem + kColQK + c + 8 * part, dv + c * 8, idv, 1);
           mma_commit(&sh.o_done);
           if (more) scores(next_q, next_k);
-          mma_commit(&sh.v_empty[iv]);
         }
         __syncwarp();
       }
