@@ -340,49 +340,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.o_ready);
           if (!(good = wait(sh, &sh.o_done, n & 1))) break;
           tc_fence_after();
-          // Read and round everything first: the next chunk's products wait for the accumulator.
-          uint32_t w[DV / 2];
-#pragma unroll
+          // PV has run, and ST before it: nobody reads this chunk's V tile any more, and it takes the
+          // outputs.  A chunk cut short goes out row by row: a whole tile would write into the next
+          // prompt's rows.
+          const int slot = place<L::nv>(n);
+          unsigned char* tile = smem + L::at_v + slot * L::v;
+          const bool whole = t + kC <= seg.t1;
+          bf16* o = out + (t + r) * a.out_stride;
+#pragma unroll 1
           for (int c = 0; c < DV; c += 32) {
             uint32_t x[32];
             tmem_ld32(acc + c, x);
             tmem_wait_ld();
             tmem_join<32>(x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 y = pair_of(x + 2 * i);
-              w[c / 2 + i] = pack_bf16x2(y.x, y.y);
+            for (int i = 0; i < 4; ++i) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(x[8 * i]), __uint_as_float(x[8 * i + 1]));
+              w.y = pack_bf16x2(__uint_as_float(x[8 * i + 2]), __uint_as_float(x[8 * i + 3]));
+              w.z = pack_bf16x2(__uint_as_float(x[8 * i + 4]), __uint_as_float(x[8 * i + 5]));
+              w.w = pack_bf16x2(__uint_as_float(x[8 * i + 6]), __uint_as_float(x[8 * i + 7]));
+              if (whole)
+                *reinterpret_cast<uint4*>(tile + c / 64 * kHalf + r * 128 + ((c % 64 / 8 + i) ^ (r & 7)) * 16) = w;
+              else if (t + r < seg.t1)
+                *reinterpret_cast<uint4*>(o + c + 8 * i) = w;
             }
           }
           tc_fence_before();
           mbar_arrive(&sh.o_free);
-          // PV has run, and ST before it: nobody reads this chunk's V tile any more.
-          const int slot = place<L::nv>(n);
-          if (t + kC <= seg.t1) {
-            unsigned char* o = smem + L::at_v + slot * L::v;
-#pragma unroll
-            for (int c = 0; c < DV / 8; ++c)
-              *reinterpret_cast<uint4*>(o + c / 8 * kHalf + r * 128 + ((c % 8) ^ (r & 7)) * 16) =
-                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          if (whole) {
             fence_proxy_async();
             if (!(good = meet(sh, &sh.o_meet, met))) break;
             if (r == 0) {
 #pragma unroll
-              for (int c = 0; c < DV; c += 64) tma_store_3d(&mo, c, seg.h, t, o + c / 64 * kHalf);
+              for (int c = 0; c < DV; c += 64) tma_store_3d(&mo, c, seg.h, t, tile + c / 64 * kHalf);
               bulk_commit();
               bulk_wait_read<0>();
-              mbar_arrive(&sh.v_empty[slot]);
             }
-            __syncwarp();
-          } else {  // a whole tile would write into the next prompt's rows
-            if (t + r < seg.t1) {
-              uint4* o = reinterpret_cast<uint4*>(out + (t + r) * a.out_stride);
-#pragma unroll
-              for (int c = 0; c < DV / 8; ++c) o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-            }
-            if (r == 0) mbar_arrive(&sh.v_empty[slot]);
-            __syncwarp();
           }
+          if (r == 0) mbar_arrive(&sh.v_empty[slot]);
+          __syncwarp();
         }
       }
     }
