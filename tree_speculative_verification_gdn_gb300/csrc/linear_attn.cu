@@ -230,17 +230,27 @@ __global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, in
   if (at >= size) return;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   if (a.S0 != nullptr) load_vec_rw<4>(static_cast<const TST*>(a.S0) + ((size_t)b * a.H + h) * size + at, x);
-  for (int s = 0; s < n; ++s) {
-    const size_t slot = (size_t)(first + s) * a.H + h;
-    float* p = a.slots + slot * size + at;
-    float d[4];
-    if (s + 1 < n) load_vec_rw<4>(p, d);
-    store_vec<4>(p, x);
-    if (s + 1 < n) {
-      const float f = a.decay[slot];
+  // Four segments' values are asked for before the first is needed (one by one, a segment took 4 us).
+  constexpr int kAhead = 4;
+  const size_t stride = (size_t)a.H * size;
+  float* p = a.slots + ((size_t)first * a.H + h) * size + at;
+  const float* f = a.decay + (size_t)first * a.H + h;
+  for (int s = 0; s < n; s += kAhead, p += kAhead * stride, f += kAhead * a.H) {
+    float d[kAhead][4], g[kAhead];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = fmaf(f, x[c], d[c]);
-    }
+    for (int i = 0; i < kAhead; ++i)
+      if (s + i + 1 < n) {
+        load_vec_rw<4>(p + i * stride, d[i]);
+        g[i] = f[i * a.H];
+      }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (s + i < n) {
+        store_vec<4>(p + i * stride, x);
+        if (s + i + 1 < n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = fmaf(g[i], x[c], d[i][c]);
+      }
   }
 }
 

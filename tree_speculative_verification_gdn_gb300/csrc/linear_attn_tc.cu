@@ -33,6 +33,10 @@
 // (Bringing tiles to L2 a chunk ahead made no difference with this ring.)  One CTA per SM, since five 32 KB tiles and the state's bf16
 // pair fill shared memory.  A chunk runs every role's code once, and together it has to stay near the
 // instruction cache: hence loops that are not unrolled, and only the first look of a wait inline.
+//
+// In the pass over states alone (STATE_ONLY: the contributions of a cut prompt's segments) chunks come
+// last to first: with the decay from a chunk's end to the segment's folded into K', the state only adds
+// up, tensor memory holds two K', and nobody touches S until the end.
 #include "linear_attn.cuh"
 #include "tv_async.cuh"
 #include "tv_tc.cuh"
@@ -47,7 +51,7 @@ constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
 
-// TMEM columns
+// TMEM columns; K' of even and odd chunks in the pass over states: from 256 and from 384
 constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 
 struct Shared {
@@ -117,6 +121,16 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
   if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
   return wait_more(sh, bar, parity);
 }
+// The pass over states alone keeps two chunks going: its barriers take turns.
+__device__ __forceinline__ uint64_t* state_done(Shared& sh, int n) { return n & 1 ? &sh.qs_done : &sh.st_done; }
+__device__ __forceinline__ uint64_t* state_keys(Shared& sh, int n) { return n & 1 ? &sh.p_ready : &sh.k_ready; }
+// Chunk number i of a segment, in the order of the pass: where it starts.
+template <bool STATE_ONLY>
+__device__ __forceinline__ int chunk_at(const Segment& seg, int i) {
+  return seg.t0 + (STATE_ONLY ? (seg.t1 - seg.t0 - 1) / kC - i : i) * kC;
+}
+__device__ __forceinline__ int chunks_of(const Segment& seg) { return (seg.t1 - seg.t0 + kC - 1) / kC; }
+
 // All 128 threads of a role, by a wait that ends as the others do (a named barrier would wait for ever
 // for a warp that gave up).
 __device__ __forceinline__ bool meet(Shared& sh, uint64_t* bar, uint32_t& times) {
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.g_full[i], 1);
-      mbar_init(&sh.g_empty[i], STATE_ONLY ? 8 : 16);
+      mbar_init(&sh.g_empty[i], STATE_ONLY ? 4 : 16);
     }
     mbar_init(&sh.qk_done, 1);
     mbar_init(&sh.qs_done, 1);
@@ -388,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = tid - 256;
     const uint32_t row = quad + kColS;
     const bool mine = 32 * (warp - 8) < DK;  // warp-uniform
+    uint32_t unit = 0;                       // units begun
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -395,44 +410,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool last = seg.index + 1 == seg.count;
       if (STATE_ONLY && last) continue;
       const size_t head = ((size_t)seg.b * a.H + seg.h) * DV * DK + r, slot = (size_t)u * DV * DK + r;
-      float total = 1.f;
-      if (mine) {
-#pragma unroll 1
-        for (int c = 0; c < DV; c += 16) {
-          float x[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (!STATE_ONLY && seg.count > 1) x[i] = a.slots[slot + (c + i) * DK];
-            else if (!STATE_ONLY && a.S0 != nullptr) x[i] = to_f32(static_cast<const TST*>(a.S0)[head + (c + i) * DK]);
-            else x[i] = 0.f;
-          }
-          tmem_st16_nowait(row + c, reinterpret_cast<const uint32_t*>(x));
-        }
-        tmem_wait_st();
-      }
-#pragma unroll 1
-      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-        if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
-        const float2 gc = sh.g[n & 1][kC - 1];
-        const float keep = ex2_approx(gc.x + gc.y);
-        if (STATE_ONLY) total *= keep;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
-        if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
-        if (!STATE_ONLY && n > 0 && !(good = wait(sh, &sh.qs_done, (n - 1) & 1))) break;  // it has read the last S
+      if (STATE_ONLY) {
+        mbar_arrive(&sh.s_ready);  // the last unit's state has been read
+        if (!(good = wait(sh, &sh.o_done, unit++ & 1))) break;
         tc_fence_after();
+      } else {
         if (mine) {
-          uint32_t s[16];
-          tmem_ld16_nowait(row, s);
 #pragma unroll 1
           for (int c = 0; c < DV; c += 16) {
-            uint32_t x[16];
-            tmem_wait_ld();
-            tmem_join<16>(s);
+            float x[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = s[i];
-            if (c + 16 < DV) tmem_ld16_nowait(row + c + 16, s);
-            if (!STATE_ONLY) {
+            for (int i = 0; i < 16; ++i) {
+              if (seg.count > 1) x[i] = a.slots[slot + (c + i) * DK];
+              else if (a.S0 != nullptr) x[i] = to_f32(static_cast<const TST*>(a.S0)[head + (c + i) * DK]);
+              else x[i] = 0.f;
+            }
+            tmem_st16_nowait(row + c, reinterpret_cast<const uint32_t*>(x));
+          }
+          tmem_wait_st();
+        }
+#pragma unroll 1
+        for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+          if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+          const float2 gc = sh.g[n & 1][kC - 1];
+          const float keep = ex2_approx(gc.x + gc.y);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+          if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
+          if (n > 0 && !(good = wait(sh, &sh.qs_done, (n - 1) & 1))) break;  // it has read the last S
+          tc_fence_after();
+          if (mine) {
+            uint32_t s[16];
+            tmem_ld16_nowait(row, s);
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 16) {
+              uint32_t x[16];
+              tmem_wait_ld();
+              tmem_join<16>(s);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = s[i];
+              if (c + 16 < DV) tmem_ld16_nowait(row + c + 16, s);
               unsigned char* to = s_hi + (c / 64) * (DK * 128) + r * 128;
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
@@ -445,19 +462,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(to + off) = hi;
                 *reinterpret_cast<uint4*>(to + L::s + off) = lo;
               }
-            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
-            tmem_st16_nowait(row + c, x);
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
+              tmem_st16_nowait(row + c, x);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
+          fence_proxy_async();
+          tc_fence_before();
+          mbar_arrive(&sh.s_ready);
         }
-        fence_proxy_async();
-        tc_fence_before();
-        mbar_arrive(&sh.s_ready);
       }
       if (!good) break;
-      if (seg.t1 > seg.t0) {
+      if (!STATE_ONLY && seg.t1 > seg.t0) {
         if (!(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
         tc_fence_after();
       }
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (STATE_ONLY && r == 0) a.decay[u] = total;
+      tc_fence_before();
     }
   } else if (warp < 16) {
     // ------------------------------------------------ K', transposed into tensor memory
@@ -489,15 +506,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
+      float2 later = make_float2(0.f, 0.f);  // log2 of the decay from the chunk's end to the segment's
+      const int chunks = chunks_of(seg);
 #pragma unroll 1
-      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+      for (int at = 0; at < chunks; ++at, ++n) {
+        const int t = chunk_at<STATE_ONLY>(seg, at);
         const int rows = seg.t1 - t;
         const int ik = n * L::step;
         unsigned char* k_tile = smem + place<L::nk>(ik) * L::k;
         const float2* g = sh.g[n & 1];
         if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
         if (!(good = wait(sh, &sh.kq_full[place<L::nk>(ik)], turn<L::nk>(ik)))) break;
-        if (n > 0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;  // it has read the last K'
+        // the update has read the last K' of this place
+        if (STATE_ONLY ? n > 1 && !(good = wait(sh, state_done(sh, n), (n - 2) >> 1 & 1))
+                       : n > 0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1)))
+          break;
         tc_fence_after();
         if (rows < kC) {
           if (!(good = wait(sh, &sh.v_full[place<L::nv>(n)], turn<L::nv>(n)))) break;
@@ -513,8 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async();
           if (!(good = meet(sh, &sh.k_meet, met))) break;
         }
+        float2 gc = g[kC - 1];
+        if (STATE_ONLY) gc = later = add2(later, gc);
         if (mine) {
-          const float2 gc = g[kC - 1];
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {  // 64 tokens
             float2 scale[8];                      // of tokens 8 i + 2 (lane % 4) and + 1
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   split2(__fmul2_rn(make_float2(bf16lo(w[x]), bf16hi(w[x])), scale[2 * i + x / 2]), hi[4 * i + x],
                          lo[4 * i + x]);
               }
-              const uint32_t to = keys + ((uint32_t)(16 * half) << 16) + 32 * part;
+              const uint32_t to = keys - (STATE_ONLY && !(n & 1) ? 128 : 0) + ((uint32_t)(16 * half) << 16) + 32 * part;
               tmem_st_16x32(to, hi);
               tmem_st_16x32(to + 64, lo);
             }
@@ -546,10 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&sh.k_ready);
+        mbar_arrive(STATE_ONLY ? state_keys(sh, n) : &sh.k_ready);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
       }
+      if (STATE_ONLY && r == 0) a.decay[u] = ex2_approx(later.x + later.y);
     }
   } else if (warp == 16 || warp == 19) {
     // ------------------------------------------------ TMA loads
@@ -569,8 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const int h = seg.h, hk = h / (a.H / a.Hk);
+      const int chunks = chunks_of(seg);
 #pragma unroll 1
-      for (int t = seg.t0; t < seg.t1 && good; t += kC) {
+      for (int at = 0; at < chunks && good; ++at) {
+        const int t = chunk_at<STATE_ONLY>(seg, at);
         if (keys) {
 #pragma unroll 1
           for (int tile = 0; tile < L::step; ++tile, ++loads) {
@@ -628,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto q_rows = [&](int n) { return by_rows + start(place<L::nk>(n * L::step + 1) * L::k); };
     auto k_rows = [&](int n) { return by_rows + start(place<L::nk>(n * L::step) * L::k); };
     int chunks, later;
+    uint32_t unit = 0;  // units begun
     int u = find(blockIdx.x, chunks);
     if (!STATE_ONLY && u < units && (good = landed(0))) {
       tc_fence_after();
@@ -641,8 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < chunks; ++i, ++n) {
         const int iv = place<L::nv>(n);
-        if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
-        if (!(good = wait(sh, &sh.k_ready, n & 1))) break;
+        if (STATE_ONLY) {
+          if (i == 0 && !(good = wait(sh, &sh.s_ready, unit++ & 1))) break;
+          if (!(good = wait(sh, state_keys(sh, n), n >> 1 & 1))) break;
+        } else {
+          if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
+          if (!(good = wait(sh, &sh.k_ready, n & 1))) break;
+        }
         if (!(good = wait(sh, &sh.v_full[iv], turn<L::nv>(n)))) break;
         tc_fence_after();
         // ST first, so that the next K' is made while QS and PV run.
@@ -656,9 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int c = 0; c < kC; c += 16)
-              mma_bf16_tmem_a(tmem + kColS, tmem + kColK + 64 * part + c / 2, dv + c * 8, idv, 1);
-          mma_commit(&sh.st_done);
+              mma_bf16_tmem_a(tmem + kColS, tmem + kColK - (STATE_ONLY && !(n & 1) ? 128 : 0) + 64 * part + c / 2,
+                              dv + c * 8, idv, !STATE_ONLY || i + part + c > 0);
+          mma_commit(STATE_ONLY ? state_done(sh, n) : &sh.st_done);
           if (STATE_ONLY) mma_commit(&sh.v_empty[iv]);
+          if (STATE_ONLY && i + 1 == chunks) mma_commit(&sh.o_done);
         }
         __syncwarp();
         if (STATE_ONLY) continue;
@@ -713,14 +748,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           next[i] = tok < seg.t1 ? __ldg(al + tok * a.alpha_stride) : 1.f;
         }
       };
-      fetch(seg.t0);
+      const int chunks = chunks_of(seg);
+      if (chunks > 0) fetch(chunk_at<STATE_ONLY>(seg, 0));
 #pragma unroll 1
-      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+      for (int at = 0; at < chunks; ++at, ++n) {
         float2 sum[4];
         // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = make_float2(next[i] == 0.f ? -1000.f : log2f(next[i]), 0.f);
-        if (t + kC < seg.t1) fetch(t + kC);
+        if (at + 1 < chunks) fetch(chunk_at<STATE_ONLY>(seg, at + 1));
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
