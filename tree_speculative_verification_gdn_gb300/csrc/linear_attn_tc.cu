@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       chunks = later;
     }
   } else {
-    // ------------------------------------------------ decays: four sums of 32 tokens side by side
+    // ------------------------------------------------ decays: four tokens a lane
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tok = t + 32 * i + lane;  // past the prompt's end nothing decays
+          const int tok = t + 4 * lane + i;  // past the prompt's end nothing decays
           next[i] = tok < seg.t1 ? __ldg(al + tok * a.alpha_stride) : 1.f;
         }
       };
@@ -757,23 +757,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = make_float2(next[i] == 0.f ? -1000.f : log2f(next[i]), 0.f);
         if (at + 1 < chunks) fetch(chunk_at<STATE_ONLY>(seg, at + 1));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) sum[i] = add2(sum[i - 1], sum[i]);
+        float2 up = sum[3];
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 below =
-                make_float2(__shfl_up_sync(0xffffffffu, sum[i].x, o), __shfl_up_sync(0xffffffffu, sum[i].y, o));
-            if (lane >= o) sum[i] = add2(below, sum[i]);
-          }
+          const float2 below = make_float2(__shfl_up_sync(0xffffffffu, up.x, o), __shfl_up_sync(0xffffffffu, up.y, o));
+          if (lane >= o) up = add2(below, up);
         }
+        up = make_float2(__shfl_up_sync(0xffffffffu, up.x, 1), __shfl_up_sync(0xffffffffu, up.y, 1));
         if (n >= 2 && !(good = wait(sh, &sh.g_empty[n & 1], ((n >> 1) - 1) & 1))) break;
-        float2 before = make_float2(0.f, 0.f);
+        float4* g = reinterpret_cast<float4*>(sh.g[n & 1] + 4 * lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i > 0) sum[i] = add2(before, sum[i]);
-          sh.g[n & 1][32 * i + lane] = sum[i];
-          before = make_float2(__shfl_sync(0xffffffffu, sum[i].x, 31), __shfl_sync(0xffffffffu, sum[i].y, 31));
-        }
+        for (int i = 0; i < 4; ++i)
+          if (lane > 0) sum[i] = add2(up, sum[i]);
+        g[0] = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
+        g[1] = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
       }
