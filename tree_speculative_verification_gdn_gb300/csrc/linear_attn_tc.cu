@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int n = 0;
   uint32_t met = 0;  // times the role's warps have met
   bool good = true;
-  if (warp < 4) {
+  if (!STATE_ONLY && warp < 4) {
     // ------------------------------------------------ scores to P (thread = token)
     if constexpr (!STATE_ONLY) {
       const uint32_t qk = quad + kColQK;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------ outputs (thread = token)
     if constexpr (!STATE_ONLY) {
       const uint32_t acc = quad + kColO;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 12) {
+  } else if (warp >= 8 && warp < 12) {
     // ------------------------------------------------ the state (thread = key column)
     const int r = tid - 256;
     const uint32_t row = quad + kColS;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
-  } else if (warp < 16) {
+  } else if (warp >= 12 && warp < 16) {
     // ------------------------------------------------ K', transposed into tensor memory
     // Lane l of a transposing load holds tokens 2 (l % 4) and + 1 of an 8 x 8 tile, key column l / 4.
     // Rows past the segment's end hold another prompt's tokens, or none: K and V rows there become zero.
@@ -732,8 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       u = next;
       chunks = later;
     }
-  } else {
+  } else if (warp == 18 || warp == 0) {
     // ------------------------------------------------ decays: four tokens a lane
+    // In the pass over states, whose other steps are short, two warps take turns.
+    constexpr int kTurns = STATE_ONLY ? 2 : 1;
+    const int turn = STATE_ONLY && warp == 0;
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -749,14 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       const int chunks = chunks_of(seg);
-      if (chunks > 0) fetch(chunk_at<STATE_ONLY>(seg, 0));
+      const int first = (n ^ turn) & (kTurns - 1), past = n + chunks;
+      n += first;
+      if (first < chunks) fetch(chunk_at<STATE_ONLY>(seg, first));
 #pragma unroll 1
-      for (int at = 0; at < chunks; ++at, ++n) {
+      for (int at = first; at < chunks; at += kTurns, n += kTurns) {
         float2 sum[4];
         // alpha = 0 forgets everything: 2^-1000 times any state is 0 in fp32
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = make_float2(next[i] == 0.f ? -1000.f : log2f(next[i]), 0.f);
-        if (at + 1 < chunks) fetch(chunk_at<STATE_ONLY>(seg, at + 1));
+        if (at + kTurns < chunks) fetch(chunk_at<STATE_ONLY>(seg, at + kTurns));
 #pragma unroll
         for (int i = 1; i < 4; ++i) sum[i] = add2(sum[i - 1], sum[i]);
         float2 up = sum[3];
@@ -776,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full[n & 1]);
       }
+      n = past;
     }
   }
   __syncwarp();
