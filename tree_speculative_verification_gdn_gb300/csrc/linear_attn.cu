@@ -8,6 +8,7 @@
 // Row r of S needs k_t, q_t, alpha_t and v_t[r] only, so rows are independent: a CTA of the prompt
 // kernel keeps kRows rows in registers, eight lanes a row, and walks the tokens.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "linear_attn.cuh"
@@ -332,16 +333,20 @@ int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io
   const int sms = device_sm_count();
   if (io == TV_BF16) {
     // One CTA per SM walks whole (segment, head) units.  Measured on a GB300, in us: a unit costs 5 and
-    // 3.6 a chunk of 128 tokens, in the pass over states alone 5 and 1.8; a launch 4, the scan 3 and
-    // 0.5 a segment.  The cheapest cut of the longest prompt into equal pieces, or none.  (16 heads, one
-    // prompt: 768 tokens 27 uncut and 30 in pieces of 256; 4096 tokens 109 uncut, 50 in pieces of 512.)
+    // 3.2 a chunk of 128 tokens, in the pass over states alone 5 and 1.2; a launch 4, the scan 3 and
+    // 0.4 a segment.  The cheapest cut of the longest prompt into equal pieces, or none.  (16 heads, one
+    // prompt: 768 tokens 26 uncut and 24 in six pieces; 4096 tokens 108 uncut, 38 in eight pieces.  32
+    // heads, 32768 tokens: 816 uncut, 304 in four pieces, 315 in nine.)
     const int longest = (max_len + 127) / 128;
+    // Prompts of one length run in rounds; of ragged ones the longest, which start first, or the sum counts.
+    auto pass = [&](int chunks, double each) {
+      const double units = (double)H * std::max(B, (T / 128 + chunks - 1) / chunks), alone = 5 + each * chunks;
+      if ((long long)B * max_len == T) return 4 + std::ceil(units / sms) * alone;
+      return 4 + std::max(1.25 * alone, 1.15 * (units * 5 + each * H * (T / 128.0)) / sms);
+    };
     auto cost = [&](int chunks) {
-      const long long units = (long long)H * std::max<long long>(B, (T / 128 + chunks - 1) / chunks);
-      const long long rounds = (units + sms - 1) / sms;
-      const double whole = 4 + rounds * (5 + 3.6 * chunks);
-      if (chunks >= longest) return whole;
-      return whole + 4 + rounds * (5 + 1.8 * chunks) + 3 + 0.5 * ((longest + chunks - 1) / chunks);
+      if (chunks >= longest) return pass(chunks, 3.2);
+      return pass(chunks, 3.2) + pass(chunks, 1.2) + 3 + 0.4 * ((longest + chunks - 1) / chunks);
     };
     int best = longest;
     for (int pieces = 2; pieces <= 64 && longest / pieces > 1; ++pieces) {
