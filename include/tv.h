@@ -539,12 +539,14 @@ TV_API int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, c
  *                                           TV_ERR_TIMEOUT (a bounded device wait gave up; that
  *                                           prompt's outputs are then unspecified)
  * Rounding: products accumulate in fp32; bf16 operands that are themselves sums or scaled
- * (scores, decayed keys, states) enter the matrix units as a bf16 pair, value and remainder.
+ * (scores, decayed keys, states) enter the matrix units as a bf16 pair, value and remainder.  An
+ * fp32 state of bf16 inputs is off by about 3e-6 of its norm after a thousand tokens (the matrix
+ * units cut what they add to an accumulator), of fp32 inputs by 3e-7.
  * A non-finite input makes later tokens of its prompt and head non-finite, and may make earlier
  * ones of the same 128-token chunk so; other prompts are not touched.
  * Supported: dk, dv in {64, 128}; H a multiple of Hk; (io, state) as tv_gdn_tree_verify_fork.
  * Strides: at least the dense row (Hk * dk or H * dv; alpha H or 0) and whole multiples of 16
- * bytes (alpha: any), else TV_ERR_INVALID_ARG.
+ * bytes (alpha: any), else TV_ERR_INVALID_ARG.  B * H <= 2^24.
  * ---------------------------------------------------------------------------------------- */
 TV_API size_t tv_linear_attn_workspace_size(int B, int T, int max_len, int H, int dk, int dv, int io_dtype);
 TV_API int tv_linear_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -37,6 +37,13 @@
 // In the pass over states alone (STATE_ONLY: the contributions of a cut prompt's segments) chunks come
 // last to first: with the decay from a chunk's end to the segment's folded into K', the state only adds
 // up, tensor memory holds two K', and nobody touches S until the end.
+//
+// Measured on a GB300: 32 prompts of 2048 tokens, 32 heads of 128, 395 us = 5.5 TB/s, 0.82 of a plain copy's
+// rate; the tensor pipe is busy half of the time, issue slots too.  What bounds it is the chain a chunk
+// hangs on, about 6000 clocks: the state's conversion 2300, ST 1300, QS 1500, scaling 600 (P alongside, 3400
+// from its scores), then PV and the next scores.  Alone an MMA takes 70 clocks, here about 100, beside the
+// other roles' traffic.  Other orders of the four products, more warps on the state (768 threads leave 80
+// registers, and K' spills) and copying the state in bulk were slower.
 #include "linear_attn.cuh"
 #include "tv_async.cuh"
 #include "tv_tc.cuh"
