@@ -585,7 +585,7 @@ TV_API int tv_linear_attn_step(const void* q, int64_t q_stride, const void* k, i
  *                 NULL (factor 1); out may be x itself
  *   weight        [d] io_dtype, or NULL (out is not scaled by a weight, and weight_offset is not used)
  * Arithmetic is fp32, rounded once on store.  Any d from 1 to 32768 and any stride of at least H * d;
- * base addresses need only their element's alignment.  rows * H < 2^31.
+ * base addresses need only their element's alignment.  rows * H <= 2^31 - 256.
  * ---------------------------------------------------------------------------------------- */
 TV_API int tv_gated_rmsnorm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
                             const void* weight, int rows, int H, int d, int io_dtype, float eps, float weight_offset,

@@ -80,7 +80,7 @@ GATED_OK = dict(x=P, xs=256, gate=P, gs=256, weight=P, rows=3, H=2, d=128, io=tv
     (BAD, dict(xs=255)), (BAD, dict(gs=255)), (BAD, dict(os=255)), (BAD, dict(rows=-1)), (BAD, dict(H=0)), (BAD, dict(d=0)),
     (NONE, dict(d=32769, xs=1 << 20, gs=1 << 20, os=1 << 20)), (BAD, dict(io=2)), (BAD, dict(eps=-1.0)),
     (BAD, dict(eps=float("nan"))), (BAD, dict(offset=float("inf"))), (BAD, dict(first=2)),
-    (NONE, dict(rows=1 << 30, H=2)), (tv.TV_OK, dict(rows=0, x=None)),
+    (NONE, dict(rows=1 << 30, H=2)), (NONE, dict(rows=(1 << 31) - 1, H=1, xs=1 << 20)), (tv.TV_OK, dict(rows=0, x=None)),
 ])
 def test_gated_norm_refusals(want, changes):
     assert call("tv_gated_rmsnorm", GATED, GATED_OK, **changes) == want

@@ -454,7 +454,8 @@ int tv_gated_rmsnorm(const void* x, int64_t x_stride, const void* gate, int64_t 
   if (rows < 0 || H < 1 || d < 1 || !(eps >= 0.f) || !isfinite(eps) || !isfinite(weight_offset) || gate_first < 0 ||
       gate_first > 1)
     return TV_ERR_INVALID_ARG;
-  if (d > kNormMax || (long long)rows * H > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  // Row numbers are ints, and the last block counts up to 31 past the last one.
+  if (d > kNormMax || (long long)rows * H > 0x7fffff00LL) return TV_ERR_UNSUPPORTED;
   if (rows == 0) return TV_OK;
   const int64_t row = (int64_t)H * d;
   if (!el(x, io_dtype) || !el(out, io_dtype) || (gate != nullptr && !el(gate, io_dtype)) ||
