@@ -145,6 +145,31 @@ def test_prompt_reset_then_slow_decay_keeps_its_precision():
     check_prompt(c, *prompt(c))
 
 
+@pytest.mark.parametrize("io,state", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+def test_tokens_masked_by_a_zero_key_leave_the_state(io, state):
+    c = make([700, 5000], 2, 4, 128, 128, io, state, seed=8, alpha=torch.ones(5700, 4))
+    c["k"].zero_()
+    _, S, err = prompt(c)
+    assert not any(err)
+    assert torch.equal(S, c["S0"])
+
+
+def test_long_prompt_with_a_slow_decay_keeps_an_fp32_state():
+    """Every head walks its 64 chunks by itself.  The keys' pair leaves half of 2^-16; a chunk's sixteen
+    cuts are half a unit of 2^-23 / 1.39 each, of which four units are given back: at most 1.8 units
+    remain for each chunk that the state has come through."""
+    T, H, d = 8192, 152, 64
+    c = make([T], 8, H, d, d, "bf16", "f32", seed=9, alpha=torch.full((T, H), 0.9999))
+    _, S, err = prompt(c)
+    assert not any(err)
+    a = float(torch.tensor(0.9999).double())  # the decay the kernel gets
+    w = a ** torch.arange(T - 1, -1, -1, dtype=torch.float64, device=DEV)
+    for h in (0, 77, 151):
+        want = (c["v"][:, h].double() * w[:, None]).T @ c["k"][:, h // 19].double() + c["S0"][0, h].double() * a ** T
+        off = float((S[0, h].double() - want).norm() / want.norm())
+        assert off <= 2.0 ** -17 + 64 * 1.8 * 2.0 ** -23, (h, off)
+
+
 def test_other_prompts_rows_and_gaps_are_not_touched():
     # NaN and infinity in the next prompt's first tokens, in the rows before the first prompt and
     # behind the last one, reach nobody else
