@@ -729,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         const bool more = i + 1 < chunks || next < units;
-        if (more && !(good = landed(n + 1))) break;
         if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
         if (!(good = wait(sh, &sh.o_ready, n & 1))) break;
         tc_fence_after();
@@ -741,9 +740,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColO, tmem + kColQK + c + 8 * part, dv + c * 8, idv, 1);
           mma_commit(&sh.o_done);
-          if (more) scores(next_q, next_k);
         }
         __syncwarp();
+        if (more) {
+          if (!(good = landed(n + 1))) break;
+          if (elect_one()) scores(next_q, next_k);
+          __syncwarp();
+        }
       }
       u = next;
       chunks = later;
