@@ -10,13 +10,14 @@
 //     QK: scores [token i, token j]      A = Q,    B = K
 //     QS: O [token i, value]             A = Q,    B = S^T     (bf16 pair); its rows then scaled in place
 //     ST: S^T [key column, value]        A = K'^T, B = V       (bf16 pair, tensor memory), added to the state
+//         fp32 states: a third part as well (shared memory, in K's place), after QS
 //     PV: O, added to                    A = P,    B = V       (bf16 pair, tensor memory, over the scores)
 // P, K' and S are fp32 results and enter as value + remainder, two bf16 each (2^-16 left out): one
 // bf16 alone would put an error as large as the output's own rounding on every output, and 2^-9 on
-// an fp32 state.  (A third part of K' was tried for fp32 states and left out: their error stayed near
-// 3e-6, since the matrix units cut what they add to an accumulator instead of rounding it, and the third
-// part's products add to that; it cost a quarter of the time.)  Exponents only ever go down: within
-// 32 x 32 diagonal blocks each 2^(g_i - g_j) is taken directly, elsewhere as
+// an fp32 state.  For an fp32 state K' has a third part, written over K once the scores have read it:
+// without it the state is off by 2.5e-6 of its norm, with it by 5e-7 to 1e-6 (32 prompts of 2048 tokens
+// 398 -> 463 us; a bf16 state's own rounding is a thousand times either).  Exponents only ever go down:
+// within 32 x 32 diagonal blocks each 2^(g_i - g_j) is taken directly, elsewhere as
 // 2^(g_i - g_r) 2^(g_r - g_j) with r the first row of i's block, so no factor exceeds 1 however fast
 // the decay.  g is summed and kept as two floats: after a reset (alpha
 // near 0) small differences of large sums remain.
@@ -45,6 +46,8 @@
 // from its scores), then PV and the next scores.  Alone an MMA takes 70 clocks, here about 100, beside the
 // other roles' traffic.  Other orders of the four products, more warps on the state (768 threads leave 80
 // registers, and K' spills) and copying the state in bulk were slower.
+#include <type_traits>
+
 #include "linear_attn.cuh"
 #include "tv_async.cuh"
 #include "tv_tc.cuh"
@@ -58,13 +61,16 @@ constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
-// A chunk reaches the state by sixteen accumulations (eight steps of 16 tokens, value and remainder),
-// each of which cuts the sum towards zero: half a unit of its last place on average, 0.36 * 2^-23 of it.
-// What survives into the next chunk is scaled by the decay anyway, and there gets back 4 * 2^-23 of the
-// 4.7 * 2^-23 measured: 8 prompts of 8192 tokens 7.8e-6 -> 2.8e-6 of the state's norm, one of 32768
-// 9.0e-6 -> 3.6e-6, at no cost.  A chunk without decay gets nothing back: it may hold tokens masked by
-// a zero key and a decay of 1, which leave the state exactly as it was.
-constexpr float kUncut = 1.f + 4.f / (1 << 23);
+// A chunk reaches the state by 8 accumulations (16 tokens each) of every part of K', and each cuts the
+// sum towards zero: half a unit of its last place on average, 0.36 * 2^-23 of it.  What survives into
+// the next chunk is scaled by the decay anyway, and there gets back the 4 * 2^-23 (two parts) or
+// 7 * 2^-23 (three) that measured best of whole numbers: without it the state lost 1e-6 of itself per
+// thousand tokens (8 prompts of 8192 tokens, two parts: off by 7.8e-6, with it 2.8e-6; three parts
+// 1.0e-6).  A chunk without decay gets nothing back: it may hold tokens masked by a zero key and a decay
+// of 1, which leave the state exactly as it was.
+template <typename TST>
+constexpr float kUncut = 1.f + (std::is_same<TST, float>::value ? 7.f : 4.f) / (1 << 23);
+constexpr uint32_t kTransposedA = 1u << 15;  // instruction descriptor: A is MN-major
 
 // TMEM columns; K' of even and odd chunks in the pass over states: from 256 and from 384
 constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
@@ -76,6 +82,7 @@ struct Shared {
   uint64_t g_full[2], g_empty[2];
   uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
   uint64_t s_ready, k_ready, p_ready, o_ready, o_free;  // operands written, outputs read
+  uint64_t k_third, st_part;  // fp32 states: third part of K' written, the first two added
   uint64_t o_meet, k_meet;                              // the warps of a role among themselves
   uint64_t drain;
   uint32_t tmem;
@@ -199,11 +206,22 @@ __device__ __forceinline__ void ldsm4t(uint32_t at, uint32_t* v) {
 __device__ __forceinline__ float2 pair_of(const uint32_t* s) {
   return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
-// x as value and remainder, two columns a word.
-__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+// What bf16 leaves of x; two columns a word.
+__device__ __forceinline__ float2 rest_of(float2 x, uint32_t rounded) {
+  return __ffma2_rn(make_float2(bf16lo(rounded), bf16hi(rounded)), make_float2(-1.f, -1.f), x);
+}
+// x as value and remainder; what they leave.
+__device__ __forceinline__ float2 split2(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x.x, x.y);
-  const float2 rest = __ffma2_rn(make_float2(bf16lo(hi), bf16hi(hi)), make_float2(-1.f, -1.f), x);
+  const float2 rest = rest_of(x, hi);
   lo = pack_bf16x2(rest.x, rest.y);
+  return rest_of(rest, lo);
+}
+// That rest of a key times its decay, instead of the key.
+__device__ __forceinline__ uint32_t third_part(uint32_t keys, float scale) {
+  uint32_t hi, lo;
+  const float2 rest = split2(__fmul2_rn(make_float2(bf16lo(keys), bf16hi(keys)), make_float2(scale, scale)), hi, lo);
+  return pack_bf16x2(rest.x, rest.y);
 }
 
 // Sums of two floats: hi + lo with |lo| at most half a step of hi.
@@ -224,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                           const __grid_constant__ CUtensorMap mo) {
   using L = Plan<DK, DV, STATE_ONLY>;
+  constexpr bool THIRD = std::is_same<TST, float>::value;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* s_hi = smem + L::at_s;  // the state's values, then their remainders
   Shared& sh = *reinterpret_cast<Shared*>(s_hi + 2 * L::s);
@@ -253,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.p_ready, 128);
     mbar_init(&sh.o_ready, 128);
     mbar_init(&sh.o_free, 128);
+    mbar_init(&sh.k_third, 128);
+    mbar_init(&sh.st_part, 1);
     mbar_init(&sh.o_meet, 128);
     mbar_init(&sh.k_meet, 128);
     mbar_init(&sh.drain, 1);
@@ -449,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
           const float2 gc = sh.g[n & 1][kC - 1];
           float keep = ex2_approx(gc.x + gc.y);
-          if (keep != 1.f) keep *= kUncut;
+          if (keep != 1.f) keep *= kUncut<TST>;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
           if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
@@ -535,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(good = wait(sh, &sh.kq_full[place<L::nk>(ik)], turn<L::nk>(ik)))) break;
         // the update has read the last K' of this place
         if (STATE_ONLY ? n > 1 && !(good = wait(sh, state_done(sh, n), (n - 2) >> 1 & 1))
-                       : n > 0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1)))
+                       : n > 0 && !(good = wait(sh, THIRD ? &sh.st_part : &sh.st_done, (n - 1) & 1)))
           break;
         tc_fence_after();
         if (rows < kC) {
@@ -554,6 +575,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float2 gc = g[kC - 1];
         if (STATE_ONLY) gc = later = add2(later, gc);
+        // The third part of K' takes the place of K (thread = token; pieces in an order without conflicts).
+        auto third = [&] {
+          const float scale = exp2_gap(gc, g[r]);
+#pragma unroll 2
+          for (int i = 0; i < DK / 8; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(k_tile + i / 8 * kHalf + r * 128 + ((i ^ r) & 7) * 16);
+            const uint4 w = *at;
+            *at = make_uint4(third_part(w.x, scale), third_part(w.y, scale), third_part(w.z, scale),
+                             third_part(w.w, scale));
+          }
+          fence_proxy_async();
+        };
         if (mine) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {  // 64 tokens
@@ -585,8 +618,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
+        if (THIRD && STATE_ONLY) {
+          if (!(good = meet(sh, &sh.k_meet, met))) break;  // all have read the keys
+          third();
+        }
         tc_fence_before();
         mbar_arrive(STATE_ONLY ? state_keys(sh, n) : &sh.k_ready);
+        if (THIRD && !STATE_ONLY) {
+          if (!(good = wait(sh, &sh.k_ready, n & 1))) break;  // all have read the keys,
+          if (!(good = wait(sh, &sh.qk_done, n & 1))) break;  // and the scores too
+          third();
+          mbar_arrive(&sh.k_third);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
       }
@@ -699,15 +742,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // them.
         constexpr uint32_t idv = idesc_bf16_f32(kC, DV, true);
         const uint64_t dv = by_columns + start(L::at_v + iv * L::v);
+        const uint64_t rest = by_columns + start(place<L::nk>(n * L::step) * L::k);
+        auto add_third = [&] {
+#pragma unroll
+          for (int c = 0; c < kC; c += 16) mma_bf16(tmem + kColS, rest + c * 8, dv + c * 8, idv | kTransposedA, 1);
+        };
         if (elect_one()) {
-          mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);  // the scores have read K, and K' is made
+          if (!THIRD) mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);  // the scores have read K, and K' is made
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColS, tmem + kColK - (STATE_ONLY && !(n & 1) ? 128 : 0) + 64 * part + c / 2,
                               dv + c * 8, idv, !STATE_ONLY || i + part + c > 0);
-          mma_commit(STATE_ONLY ? state_done(sh, n) : &sh.st_done);
+          if (THIRD && STATE_ONLY) {
+            add_third();
+            mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);
+          }
+          mma_commit(STATE_ONLY ? state_done(sh, n) : THIRD ? &sh.st_part : &sh.st_done);
           if (STATE_ONLY) mma_commit(&sh.v_empty[iv]);
           if (STATE_ONLY && i + 1 == chunks) mma_commit(&sh.o_done);
         }
@@ -728,6 +780,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&sh.kq_empty[place<L::nk>(n * L::step + 1)]);
         }
         __syncwarp();
+        if (THIRD) {
+          if (!(good = wait(sh, &sh.k_third, n & 1))) break;
+          if (elect_one()) {
+            add_third();
+            mma_commit(&sh.st_done);
+            mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);
+          }
+          __syncwarp();
+        }
         const bool more = i + 1 < chunks || next < units;
         if (!(good = wait(sh, &sh.p_ready, n & 1))) break;
         if (!(good = wait(sh, &sh.o_ready, n & 1))) break;
