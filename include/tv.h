@@ -540,7 +540,7 @@ TV_API int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, c
  *                                           prompt's outputs are then unspecified)
  * Rounding: products accumulate in fp32; bf16 operands that are themselves sums or scaled
  * (scores, decayed keys, states) enter the matrix units as a bf16 pair, value and remainder.  An
- * fp32 state of bf16 inputs is off by 5e-7 to 1e-6 of its norm (three parts of a key), of fp32
+ * fp32 state of bf16 inputs is off by 5e-7 to 2e-6 of its norm (three parts of a key), of fp32
  * inputs by 3e-7.  The matrix units cut what they add to an accumulator; a decaying state gets that
  * back on average, one whose decays are exactly 1 does not and loses 1e-6 of itself per thousand
  * tokens.

@@ -40,7 +40,7 @@
 // last to first: with the decay from a chunk's end to the segment's folded into K', the state only adds
 // up, tensor memory holds two K', and nobody touches S until the end.
 //
-// Measured on a GB300: 32 prompts of 2048 tokens, 32 heads of 128, 395 us = 5.5 TB/s, 0.82 of a plain copy's
+// Measured on a GB300: 32 prompts of 2048 tokens, 32 heads of 128, 392 us = 5.6 TB/s, 0.82 of a plain copy's
 // rate; the tensor pipe is busy half of the time, issue slots too.  What bounds it is the chain a chunk
 // hangs on, about 6000 clocks: the state's conversion 2300, ST 1300, QS 1500, scaling 600 (P alongside, 3400
 // from its scores), then PV and the next scores.  Alone an MMA takes 70 clocks, here about 100, beside the
@@ -70,6 +70,11 @@ constexpr int kSmemMax = 232448;  // per block
 // of 1, which leave the state exactly as it was.
 template <typename TST>
 constexpr float kUncut = 1.f + (std::is_same<TST, float>::value ? 7.f : 4.f) / (1 << 23);
+// A segment's sum meets nothing on its way and gets back at the end what its chunks lost, by the same
+// reckoning with 3 and 5 (one of 13107 tokens: 3.9e-6 -> 1.8e-6; 8 ragged prompts of up to 3001 1.3e-6 ->
+// 8e-7, times equal).
+template <typename TST>
+constexpr float kUncutSum = (std::is_same<TST, float>::value ? 5.f : 3.f) / (1 << 23);
 constexpr uint32_t kTransposedA = 1u << 15;  // instruction descriptor: A is MN-major
 
 // TMEM columns; K' of even and odd chunks in the pass over states: from 256 and from 384
@@ -78,6 +83,7 @@ constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 struct Shared {
   float2 g[2][kC];  // g_i as two floats, by chunk parity
   float f[192];     // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
+  float uncut[4];   // pass over states: what a unit's sum is multiplied by, by unit
   uint64_t kq_full[3], kq_empty[3], v_full[2], v_empty[2];
   uint64_t g_full[2], g_empty[2];
   uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
@@ -446,10 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool last = seg.index + 1 == seg.count;
       if (STATE_ONLY && last) continue;
       const size_t head = ((size_t)seg.b * a.H + seg.h) * DV * DK + r, slot = (size_t)u * DV * DK + r;
+      float uncut = 1.f;
       if (STATE_ONLY) {
         mbar_arrive(&sh.s_ready);  // the last unit's state has been read
         if (!(good = wait(sh, &sh.o_done, unit++ & 1))) break;
         tc_fence_after();
+        uncut = sh.uncut[(unit - 1) & 3];
       } else {
         if (mine) {
 #pragma unroll 1
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_join<16>(s);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (STATE_ONLY) a.slots[slot + (c + i) * DK] = __uint_as_float(s[i]);
+            if (STATE_ONLY) a.slots[slot + (c + i) * DK] = __uint_as_float(s[i]) * uncut;
             else static_cast<TST*>(a.S)[head + (c + i) * DK] = from_f32<TST>(__uint_as_float(s[i]));
           }
         }
@@ -537,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Rows past the segment's end hold another prompt's tokens, or none: K and V rows there become zero.
     const int r = tid - 384;
     const uint32_t keys = quad + kColK;
+    int units_done = 0;
     const bool mine = 32 * (warp - 12) < DK;  // warp-uniform
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
@@ -544,6 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       float2 later = make_float2(0.f, 0.f);  // log2 of the decay from the chunk's end to the segment's
+      // Chunks weighed by their share of the sum's square, and how often they are cut: by every chunk
+      // from their own on that decays and is not yet below the sum's last place.
+      float sum = 0.f, cuts = 0.f;
       const int chunks = chunks_of(seg);
 #pragma unroll 1
       for (int at = 0; at < chunks; ++at, ++n) {
@@ -574,7 +586,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(good = meet(sh, &sh.k_meet, met))) break;
         }
         float2 gc = g[kC - 1];
-        if (STATE_ONLY) gc = later = add2(later, gc);
+        if (STATE_ONLY) {
+          sum += ex2_approx(2.f * fminf(later.x, 0.f));
+          if (gc.x != 0.f && later.x > -24.f) cuts += sum;
+          if (r == 0) sh.uncut[units_done & 3] = 1.f + kUncutSum<TST> * (cuts / sum);
+          gc = later = add2(later, gc);
+        }
         // The third part of K' takes the place of K (thread = token; pieces in an order without conflicts).
         auto third = [&] {
           const float scale = exp2_gap(gc, g[r]);
@@ -633,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
       }
+      ++units_done;
       if (STATE_ONLY && r == 0) a.decay[u] = ex2_approx(later.x + later.y);
     }
   } else if (warp == 16 || warp == 19) {
