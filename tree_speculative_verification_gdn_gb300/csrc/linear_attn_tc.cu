@@ -38,7 +38,8 @@
 //
 // In the pass over states alone (STATE_ONLY: the contributions of a cut prompt's segments) chunks come
 // last to first: with the decay from a chunk's end to the segment's folded into K', the state only adds
-// up, tensor memory holds two K', and nobody touches S until the end.
+// up, tensor memory holds two K', and nobody touches S until the end.  The warps without outputs to write
+// make the third part there (one prompt of 32768 tokens, fp32 states, 429 -> 386 us).
 //
 // Measured on a GB300: 32 prompts of 2048 tokens, 32 heads of 128, 392 us = 5.6 TB/s, 0.82 of a plain copy's
 // rate; the tensor pipe is busy half of the time, issue slots too.  What bounds it is the chain a chunk
@@ -152,6 +153,7 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
 // The pass over states alone keeps two chunks going: its barriers take turns.
 __device__ __forceinline__ uint64_t* state_done(Shared& sh, int n) { return n & 1 ? &sh.qs_done : &sh.st_done; }
 __device__ __forceinline__ uint64_t* state_keys(Shared& sh, int n) { return n & 1 ? &sh.p_ready : &sh.k_ready; }
+__device__ __forceinline__ uint64_t* state_third(Shared& sh, int n) { return n & 1 ? &sh.st_part : &sh.k_third; }
 // Chunk number i of a segment, in the order of the pass: where it starts.
 template <bool STATE_ONLY>
 __device__ __forceinline__ int chunk_at(const Segment& seg, int i) {
@@ -242,6 +244,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float exp2_gap(float2 a, float2 b) { return ex2_approx((a.x - b.x) + (a.y - b.y)); }
 
+// The third part of row r of K' takes the place of K's (pieces in an order without conflicts).
+template <int DK>
+__device__ __forceinline__ void third_parts(unsigned char* k_tile, int r, float scale) {
+#pragma unroll 2
+  for (int i = 0; i < DK / 8; ++i) {
+    uint4* at = reinterpret_cast<uint4*>(k_tile + i / 8 * kHalf + r * 128 + ((i ^ r) & 7) * 16);
+    const uint4 w = *at;
+    *at = make_uint4(third_part(w.x, scale), third_part(w.y, scale), third_part(w.z, scale),
+                     third_part(w.w, scale));
+  }
+  fence_proxy_async();
+}
+
 template <int DK, int DV, typename TST, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ LinAttnArgs a, int units, const __grid_constant__ CUtensorMap mq,
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.g_full[i], 1);
-      mbar_init(&sh.g_empty[i], STATE_ONLY ? 4 : 16);
+      mbar_init(&sh.g_empty[i], !STATE_ONLY ? 16 : THIRD ? 8 : 4);
     }
     mbar_init(&sh.qk_done, 1);
     mbar_init(&sh.qs_done, 1);
@@ -279,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.o_ready, 128);
     mbar_init(&sh.o_free, 128);
     mbar_init(&sh.k_third, 128);
-    mbar_init(&sh.st_part, 1);
+    mbar_init(&sh.st_part, STATE_ONLY ? 128 : 1);
     mbar_init(&sh.o_meet, 128);
     mbar_init(&sh.k_meet, 128);
     mbar_init(&sh.drain, 1);
@@ -359,6 +374,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
         }
+      }
+    }
+  } else if (STATE_ONLY && THIRD && warp >= 4 && warp < 8) {
+    // ------------------------------------------------ third part of K' (thread = token)
+    const int r = tid - 128;
+#pragma unroll 1
+    for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+      const Segment seg = find_segment(a, u);
+      if (seg.b < 0) break;
+      if (seg.index + 1 == seg.count) continue;
+      float2 later = make_float2(0.f, 0.f);
+      const int chunks = chunks_of(seg);
+#pragma unroll 1
+      for (int at = 0; at < chunks; ++at, ++n) {
+        if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+        later = add2(later, sh.g[n & 1][kC - 1]);
+        const float scale = exp2_gap(later, sh.g[n & 1][r]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+        if (!(good = wait(sh, state_keys(sh, n), n >> 1 & 1))) break;  // K has been read
+        third_parts<DK>(smem + place<L::nk>(n) * L::k, r, scale);
+        mbar_arrive(state_third(sh, n));
       }
     }
   } else if (warp >= 4 && warp < 8) {
@@ -592,18 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r == 0) sh.uncut[units_done & 3] = 1.f + kUncutSum<TST> * (cuts / sum);
           gc = later = add2(later, gc);
         }
-        // The third part of K' takes the place of K (thread = token; pieces in an order without conflicts).
-        auto third = [&] {
-          const float scale = exp2_gap(gc, g[r]);
-#pragma unroll 2
-          for (int i = 0; i < DK / 8; ++i) {
-            uint4* at = reinterpret_cast<uint4*>(k_tile + i / 8 * kHalf + r * 128 + ((i ^ r) & 7) * 16);
-            const uint4 w = *at;
-            *at = make_uint4(third_part(w.x, scale), third_part(w.y, scale), third_part(w.z, scale),
-                             third_part(w.w, scale));
-          }
-          fence_proxy_async();
-        };
         if (mine) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {  // 64 tokens
@@ -635,16 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        if (THIRD && STATE_ONLY) {
-          if (!(good = meet(sh, &sh.k_meet, met))) break;  // all have read the keys
-          third();
-        }
         tc_fence_before();
         mbar_arrive(STATE_ONLY ? state_keys(sh, n) : &sh.k_ready);
         if (THIRD && !STATE_ONLY) {
           if (!(good = wait(sh, &sh.k_ready, n & 1))) break;  // all have read the keys,
           if (!(good = wait(sh, &sh.qk_done, n & 1))) break;  // and the scores too
-          third();
+          third_parts<DK>(k_tile, r, exp2_gap(gc, g[r]));
           mbar_arrive(&sh.k_third);
         }
         __syncwarp();
@@ -773,16 +794,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColS, tmem + kColK - (STATE_ONLY && !(n & 1) ? 128 : 0) + 64 * part + c / 2,
                               dv + c * 8, idv, !STATE_ONLY || i + part + c > 0);
-          if (THIRD && STATE_ONLY) {
-            add_third();
-            mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);
-          }
-          mma_commit(STATE_ONLY ? state_done(sh, n) : THIRD ? &sh.st_part : &sh.st_done);
-          if (STATE_ONLY) mma_commit(&sh.v_empty[iv]);
-          if (STATE_ONLY && i + 1 == chunks) mma_commit(&sh.o_done);
+          if (!STATE_ONLY) mma_commit(THIRD ? &sh.st_part : &sh.st_done);
         }
         __syncwarp();
-        if (STATE_ONLY) continue;
+        if (STATE_ONLY) {
+          if (THIRD && !(good = wait(sh, state_third(sh, n), n >> 1 & 1))) break;
+          if (elect_one()) {
+            if (THIRD) {
+              add_third();
+              mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);
+            }
+            mma_commit(state_done(sh, n));
+            mma_commit(&sh.v_empty[iv]);
+            if (i + 1 == chunks) mma_commit(&sh.o_done);
+          }
+          __syncwarp();
+          continue;
+        }
         if (n > 0 && !(good = wait(sh, &sh.o_free, (n - 1) & 1))) break;
         tc_fence_after();
         constexpr uint32_t ids = idesc_bf16_f32(kC, DV, true);
