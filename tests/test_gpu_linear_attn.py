@@ -155,9 +155,9 @@ def test_tokens_masked_by_a_zero_key_leave_the_state(io, state):
 
 
 def test_long_prompt_with_a_slow_decay_keeps_an_fp32_state():
-    """Every head walks its 64 chunks by itself.  The keys' pair leaves half of 2^-16; a chunk's sixteen
-    cuts are half a unit of 2^-23 / 1.39 each, of which four units are given back: at most 1.8 units
-    remain for each chunk that the state has come through."""
+    """Every head walks its 64 chunks by itself.  A pair of bf16 leaves half of 2^-16 of a key; the sixteen
+    cuts of a pair's products are half a unit of 2^-23 / 1.39 each, and with four units given back at most
+    1.8 remain for each chunk that the state has come through.  (A third part leaves less of either.)"""
     T, H, d = 8192, 152, 64
     c = make([T], 8, H, d, d, "bf16", "f32", seed=9, alpha=torch.full((T, H), 0.9999))
     _, S, err = prompt(c)
