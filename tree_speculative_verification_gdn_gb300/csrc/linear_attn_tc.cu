@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float scale = exp2_gap(later, sh.g[n & 1][r]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+        if (!(good = wait(sh, &sh.kq_full[place<L::nk>(n)], turn<L::nk>(n)))) break;
         if (!(good = wait(sh, state_keys(sh, n), n >> 1 & 1))) break;  // K has been read
         third_parts<DK>(smem + place<L::nk>(n) * L::k, r, scale);
         mbar_arrive(state_third(sh, n));
