@@ -350,6 +350,7 @@ int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io
     // 0.4 a segment.  The cheapest cut of the longest prompt into equal pieces, or none.  (16 heads, one
     // prompt: 768 tokens 26 uncut and 24 in six pieces; 4096 tokens 108 uncut, 38 in eight pieces.  32
     // heads, 32768 tokens: 816 uncut, 304 in four pieces, 315 in nine.)
+    // fp32 states take 1.2 to 1.3 times as long in both passes (third part of the keys) and are cut alike.
     const int longest = (max_len + 127) / 128;
     // Prompts of one length run in rounds; of ragged ones the longest, which start first, or the sum counts.
     auto pass = [&](int chunks, double each) {
