@@ -852,6 +852,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (more) {
           if (!(good = landed(n + 1))) break;
+          // The scores go over P, which PV reads: MMAs are kept in order on one accumulator, and these have two.
+          if (!(good = wait(sh, &sh.o_done, n & 1))) break;
+          tc_fence_after();
           if (elect_one()) scores(next_q, next_k);
           __syncwarp();
         }
