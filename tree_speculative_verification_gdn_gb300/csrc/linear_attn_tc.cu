@@ -62,18 +62,8 @@ constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
-// A chunk reaches the state by 8 accumulations (16 tokens each) of every part of K', and each cuts the
-// sum towards zero: half a unit of its last place on average, 0.36 * 2^-23 of it.  What survives into
-// the next chunk is scaled by the decay anyway, and there gets back the 4 * 2^-23 (two parts) or
-// 7 * 2^-23 (three) that measured best of whole numbers: without it the state lost 1e-6 of itself per
-// thousand tokens (8 prompts of 8192 tokens, two parts: off by 7.8e-6, with it 2.8e-6; three parts
-// 1.0e-6).  A chunk without decay gets nothing back: it may hold tokens masked by a zero key and a decay
-// of 1, which leave the state exactly as it was.
-template <typename TST>
-constexpr float kUncut = 1.f + (std::is_same<TST, float>::value ? 7.f : 4.f) / (1 << 23);
-// A segment's sum meets nothing on its way and gets back at the end what its chunks lost, by the same
-// reckoning with 3 and 5 (one of 13107 tokens: 3.9e-6 -> 1.8e-6; 8 ragged prompts of up to 3001 1.3e-6 ->
-// 8e-7, times equal).
+// A segment's sum gets back at the end what its chunks lost, by their weight and their cuts (one of 13107
+// tokens: 3.9e-6 -> 1.8e-6; 8 ragged prompts of up to 3001 1.3e-6 -> 8e-7, times equal).
 template <typename TST>
 constexpr float kUncutSum = (std::is_same<TST, float>::value ? 5.f : 3.f) / (1 << 23);
 constexpr uint32_t kTransposedA = 1u << 15;  // instruction descriptor: A is MN-major
@@ -214,9 +204,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t at, uint32_t* v) {
 __device__ __forceinline__ float2 pair_of(const uint32_t* s) {
   return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
+__device__ __forceinline__ float2 rest_of(float2 x, float2 part) { return __ffma2_rn(part, make_float2(-1.f, -1.f), x); }
 // What bf16 leaves of x; two columns a word.
 __device__ __forceinline__ float2 rest_of(float2 x, uint32_t rounded) {
-  return __ffma2_rn(make_float2(bf16lo(rounded), bf16hi(rounded)), make_float2(-1.f, -1.f), x);
+  return rest_of(x, make_float2(bf16lo(rounded), bf16hi(rounded)));
 }
 // x as value and remainder; what they leave.
 __device__ __forceinline__ float2 split2(float2 x, uint32_t& hi, uint32_t& lo) {
@@ -241,6 +232,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   const float2 s = two_sum(a.x, b.x);
   const float e = s.y + (a.y + b.y), hi = s.x + e;
   return make_float2(hi, e - (hi - s.x));
+}
+// 2^g as value and remainder.  A state goes through it once a chunk, often the same one for thousands of
+// tokens: a value alone, off by 2^-22, would be off 256 times as far after 32768 tokens.  Below 1/2 little
+// is left after a few chunks.
+__device__ __forceinline__ float2 decay_of(float2 g) {
+  const float x = g.x + g.y;
+  if (!(x > -1.f)) return make_float2(ex2_approx(x), 0.f);
+  const float less = expm1f(x * 0.69314718f), value = 1.f + less;
+  return make_float2(value, less - (value - 1.f));
 }
 __device__ __forceinline__ float exp2_gap(float2 a, float2 b) { return ex2_approx((a.x - b.x) + (a.y - b.y)); }
 
@@ -483,6 +483,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t row = quad + kColS;
     const bool mine = 32 * (warp - 8) < DK;  // warp-uniform
     uint32_t unit = 0;                       // units begun
+    // The matrix units cut every sum that they add to towards zero, so they are not given the state: a chunk
+    // adds to the decayed remainder of it (2^-9 of the state, what bf16 leaves), and the value, which lies in
+    // shared memory for QS, joins it here.  Value and remainder together hold more than a float, so a state
+    // that thousands of chunks decay by a little is not rounded by each.
+    float kept = 0.f;  // decay of the value in shared memory; 0: none there yet
+    float owed = 0.f;  // what rounding has left out of the decays so far, as a fraction
+    auto place_of = [&](int c) { return s_hi + c / 64 * (DK * 128) + r * 128 + ((c / 8 % 8) ^ (r & 7)) * 16; };
+    // The values of columns c .. c + 15, two a word.
+    auto load_values = [&](int c, uint32_t* w) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint4 x = kept != 0.f ? *reinterpret_cast<const uint4*>(place_of(c + 8 * v)) : make_uint4(0, 0, 0, 0);
+        w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+      }
+    };
+    auto unpack = [](uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); };
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -497,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uncut = sh.uncut[(unit - 1) & 3];
       } else {
+        kept = owed = 0.f;
         if (mine) {
 #pragma unroll 1
           for (int c = 0; c < DV; c += 16) {
@@ -515,42 +532,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
           if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
           const float2 gc = sh.g[n & 1][kC - 1];
-          float keep = ex2_approx(gc.x + gc.y);
-          if (keep != 1.f) keep *= kUncut<TST>;
+          const float2 decay = decay_of(gc);
+          const float more = fmaf(decay.x, owed, decay.y), keep = decay.x + more;
+          owed = keep > 0.5f ? __fdividef(more - (keep - decay.x), keep) : 0.f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
           if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
           if (n > 0 && !(good = wait(sh, &sh.qs_done, (n - 1) & 1))) break;  // it has read the last S
           tc_fence_after();
           if (mine) {
-            uint32_t s[16];
+            uint32_t s[16], w[8];
             tmem_ld16_nowait(row, s);
+            load_values(0, w);
+            const float2 keep2 = make_float2(keep, keep), kept2 = make_float2(kept, kept), drop2 = make_float2(-kept, -kept);
 #pragma unroll 1
             for (int c = 0; c < DV; c += 16) {
-              uint32_t x[16];
+              uint32_t x[16], old[8], hi[8], lo[8];
               tmem_wait_ld();
               tmem_join<16>(s);
 #pragma unroll
               for (int i = 0; i < 16; ++i) x[i] = s[i];
-              if (c + 16 < DV) tmem_ld16_nowait(row + c + 16, s);
-              unsigned char* to = s_hi + (c / 64) * (DK * 128) + r * 128;
 #pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                uint4 hi, lo;
-                split2(pair_of(x + 8 * v), hi.x, lo.x);
-                split2(pair_of(x + 8 * v + 2), hi.y, lo.y);
-                split2(pair_of(x + 8 * v + 4), hi.z, lo.z);
-                split2(pair_of(x + 8 * v + 6), hi.w, lo.w);
-                const int off = ((c % 64 / 8 + v) ^ (r & 7)) * 16;
-                *reinterpret_cast<uint4*>(to + off) = hi;
-                *reinterpret_cast<uint4*>(to + L::s + off) = lo;
+              for (int i = 0; i < 8; ++i) old[i] = w[i];
+              if (c + 16 < DV) {
+                tmem_ld16_nowait(row + c + 16, s);
+                load_values(c + 16, w);
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
+              for (int i = 0; i < 8; ++i) {
+                const float2 value = unpack(old[i]), rest = pair_of(x + 2 * i), sum = __ffma2_rn(value, kept2, rest);
+                hi[i] = pack_bf16x2(sum.x, sum.y);
+                const float2 left = rest_of(rest, __ffma2_rn(value, drop2, unpack(hi[i])));
+                lo[i] = pack_bf16x2(left.x, left.y);
+                const float2 y = __fmul2_rn(left, keep2);
+                x[2 * i] = __float_as_uint(y.x);
+                x[2 * i + 1] = __float_as_uint(y.y);
+              }
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                unsigned char* to = place_of(c + 8 * v);
+                *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
+                *reinterpret_cast<uint4*>(to + L::s) = make_uint4(lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+              }
               tmem_st16_nowait(row + c, x);
             }
             tmem_wait_st();
           }
+          kept = keep;
           fence_proxy_async();
           tc_fence_before();
           mbar_arrive(&sh.s_ready);
@@ -568,10 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16_nowait(row + c, s);
           tmem_wait_ld();
           tmem_join<16>(s);
+          uint32_t w[8];
+          if (!STATE_ONLY) load_values(c, w);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (STATE_ONLY) a.slots[slot + (c + i) * DK] = __uint_as_float(s[i]) * uncut;
-            else static_cast<TST*>(a.S)[head + (c + i) * DK] = from_f32<TST>(__uint_as_float(s[i]));
+            if (STATE_ONLY) {
+              a.slots[slot + (c + i) * DK] = __uint_as_float(s[i]) * uncut;
+            } else {
+              const float value = i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+              static_cast<TST*>(a.S)[head + (c + i) * DK] = from_f32<TST>(fmaf(value, kept, __uint_as_float(s[i])));
+            }
           }
         }
       }
@@ -790,11 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           if (!THIRD) mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);  // the scores have read K, and K' is made
 #pragma unroll 1
-          for (int part = 0; part < 2; ++part)
+          for (int part = 1; part >= 0; --part)  // remainders first: their sum is small, and cut by little
 #pragma unroll
             for (int c = 0; c < kC; c += 16)
               mma_bf16_tmem_a(tmem + kColS, tmem + kColK - (STATE_ONLY && !(n & 1) ? 128 : 0) + 64 * part + c / 2,
-                              dv + c * 8, idv, !STATE_ONLY || i + part + c > 0);
+                              dv + c * 8, idv, !STATE_ONLY || i + (1 - part) + c > 0);
           if (!STATE_ONLY) mma_commit(THIRD ? &sh.st_part : &sh.st_done);
         }
         __syncwarp();
