@@ -11,6 +11,7 @@ The bound, for C chunks of 128 tokens and u = 2^-24:
   * a decay e^-x is off by the last places of the logarithm, its product and its sum, 2^-22 x, or by 2^-22
     for a chunk that decays below a half, where x >= 0.69: 1.45 * 2^-22 x.  Tokens that keep coming are
     about x = 1 old in the norm; a state that is all old is as old as the prompt (looked at up to e^-20).
+A cut prompt's segments are sums of their chunks' sums, added in fp32: the third again, not more often.
 A state to which nothing is added has the last two only.  No part of it depends on how large the state is
 beside what is added, or on which tokens add anything.
 """
@@ -76,6 +77,30 @@ def test_state_of_a_long_prompt_in_one_piece(kind, dk, dv):
     _, S, err = L.prompt(c)
     assert not any(err)
     check(c, S, kind, list(range(7)) + [150])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,dk,dv", [(12000, 128, 128), (32768, 128, 128), (9001, 64, 128), (9001, 128, 64), (9001, 64, 64)])
+def test_state_of_a_long_prompt_in_segments(kind, T, dk, dv):
+    H = 7
+    assert tv.tv_linear_attn_workspace_size(1, T, T, H, dk, dv) > 0
+    c = make(T, H, dk, dv, kind)
+    _, S, err = L.prompt(c)
+    assert not any(err)
+    check(c, S, kind, range(H))
+
+
+def test_states_of_ragged_prompts_in_segments():
+    lens = [3001, 6, 7, 849, 0, 666, 10, 3]
+    c = L.make(lens, 4, 8, 128, 128, "bf16", "f32", seed=4)
+    assert tv.tv_linear_attn_workspace_size(8, sum(lens), 3001, 8, 128, 128) > 0
+    out, S, err = L.prompt(c, max_len=3001)
+    want = torch.from_numpy(recurrence(c)[1]).to(DEV)
+    assert not any(err)
+    for b, n in enumerate(lens):
+        assert float((S[b].double() - want[b]).norm() / want[b].norm()) <= bound(-(-n // 128), adds=n > 0), b
+    again, S2, _ = L.prompt(c, max_len=3001)
+    assert torch.equal(out, again) and torch.equal(S, S2)
 
 
 def test_states_of_many_prompts_with_decays_per_token():

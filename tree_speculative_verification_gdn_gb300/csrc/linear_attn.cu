@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
       }
     }
   }
-  float total = 1.f;
+  float2 total = make_float2(1.f, 0.f);  // the segment's decay, as two floats
 
   Raw8<TIO> rk[kVec], rq[kVec];
   TIO rv[kVPT];
@@ -175,7 +175,10 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
           d[r] = make_float2(0.f, 0.f);
         }
         const float2 al2 = make_float2(al, al);
-        if (STATE_ONLY) total *= al;
+        if (STATE_ONLY) {
+          const float x = total.x * al;
+          total = make_float2(x, fmaf(total.y, al, fmaf(total.x, al, -x)));
+        }
 #pragma unroll
         for (int j = 0; j < CPL / 4; ++j) {
           const float4 k4 = *reinterpret_cast<const float4*>(&s_k[u + i][4 * l + 32 * j]);
@@ -246,9 +249,10 @@ __global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, in
   constexpr int kAhead = 4;
   const size_t stride = (size_t)a.H * size;
   float* p = a.slots + ((size_t)first * a.H + h) * size + at;
-  const float* f = a.decay + (size_t)first * a.H + h;
+  const float2* f = a.decay + (size_t)first * a.H + h;
   for (int s = 0; s < n; s += kAhead, p += kAhead * stride, f += kAhead * a.H) {
-    float d[kAhead][4], g[kAhead];
+    float d[kAhead][4];
+    float2 g[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (s + i + 1 < n) {
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, in
         store_vec<4>(p + i * stride, x);
         if (s + i + 1 < n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = fmaf(g[i], x[c], d[i][c]);
+          for (int c = 0; c < 4; ++c) x[c] = fmaf(g[i].x, x[c], fmaf(g[i].y, x[c], d[i][c]));
       }
   }
 }

@@ -62,19 +62,15 @@ constexpr int kThreads = 640;    // four roles of four warps; MMA, decay and two
 constexpr int kHalf = kC * 128;  // bytes of 64 columns of a 128-token tile
 constexpr uint32_t kPolls = 1u << 18;
 constexpr int kSmemMax = 232448;  // per block
-// A segment's sum gets back at the end what its chunks lost, by their weight and their cuts (one of 13107
-// tokens: 3.9e-6 -> 1.8e-6; 8 ragged prompts of up to 3001 1.3e-6 -> 8e-7, times equal).
-template <typename TST>
-constexpr float kUncutSum = (std::is_same<TST, float>::value ? 5.f : 3.f) / (1 << 23);
 constexpr uint32_t kTransposedA = 1u << 15;  // instruction descriptor: A is MN-major
 
-// TMEM columns; K' of even and odd chunks in the pass over states: from 256 and from 384
+// TMEM columns; in the pass over states K' of even and odd chunks: from 256 and from 384, their sums from 0 and
+// from 128
 constexpr uint32_t kColS = 0, kColO = 128, kColQK = 256, kColK = 384;
 
 struct Shared {
   float2 g[2][kC];  // g_i as two floats, by chunk parity
   float f[192];     // 2^(g_r - g_j) of row blocks 1, 2, 3: 32, 64, 96 entries
-  float uncut[4];   // pass over states: what a unit's sum is multiplied by, by unit
   uint64_t kq_full[3], kq_empty[3], v_full[2], v_empty[2];
   uint64_t g_full[2], g_empty[2];
   uint64_t qk_done, qs_done, st_done, o_done;           // MMAs complete
@@ -143,6 +139,7 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
 // The pass over states alone keeps two chunks going: its barriers take turns.
 __device__ __forceinline__ uint64_t* state_done(Shared& sh, int n) { return n & 1 ? &sh.qs_done : &sh.st_done; }
 __device__ __forceinline__ uint64_t* state_keys(Shared& sh, int n) { return n & 1 ? &sh.p_ready : &sh.k_ready; }
+__device__ __forceinline__ uint64_t* state_read(Shared& sh, int n) { return n & 1 ? &sh.o_ready : &sh.s_ready; }
 __device__ __forceinline__ uint64_t* state_third(Shared& sh, int n) { return n & 1 ? &sh.st_part : &sh.k_third; }
 // Chunk number i of a segment, in the order of the pass: where it starts.
 template <bool STATE_ONLY>
@@ -288,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.qs_done, 1);
     mbar_init(&sh.st_done, 1);
     mbar_init(&sh.o_done, 1);
-    mbar_init(&sh.s_ready, 128);
+    mbar_init(&sh.s_ready, STATE_ONLY ? 2 * DV : 128);
     mbar_init(&sh.k_ready, 128);
     mbar_init(&sh.p_ready, 128);
-    mbar_init(&sh.o_ready, 128);
+    mbar_init(&sh.o_ready, STATE_ONLY ? 2 * DV : 128);
     mbar_init(&sh.o_free, 128);
     mbar_init(&sh.k_third, 128);
     mbar_init(&sh.st_part, STATE_ONLY ? 128 : 1);
@@ -477,12 +474,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp >= 8 && warp < 12) {
+  } else if (STATE_ONLY && ((warp >= 8 && warp < 12) || (DV == 128 && warp < 4))) {
+    // ------------------------------------------------ the segments' sums (thread = key column, 64 values)
+    // A chunk's sum starts from zero in the matrix units, which cut every sum that they add to, and joins the
+    // segment's here.
+    if constexpr (STATE_ONLY) {
+      const int r = 32 * (warp & 3) + lane, c0 = warp < 4 ? 64 : 0;
+      const bool mine = 32 * (warp & 3) < DK;  // warp-uniform
+#pragma unroll 1
+      for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
+        const Segment seg = find_segment(a, u);
+        if (seg.b < 0) break;
+        if (seg.index + 1 == seg.count) continue;
+        float2 sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = make_float2(0.f, 0.f);
+        const int chunks = chunks_of(seg);
+#pragma unroll 1
+        for (int at = 0; at < chunks; ++at, ++n) {
+          if (!(good = wait(sh, state_done(sh, n), n >> 1 & 1))) break;
+          tc_fence_after();
+          if (mine) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+              uint32_t x[16];
+              tmem_ld16_nowait(quad + (n & 1 ? kColO : kColS) + c0 + c, x);
+              tmem_wait_ld();
+              tmem_join<16>(x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[c / 2 + i] = __fadd2_rn(sum[c / 2 + i], pair_of(x + 2 * i));
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(state_read(sh, n));
+        }
+        if (good && mine) {
+          float* to = a.slots + ((size_t)u * DV + c0) * DK + r;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            to[2 * i * DK] = sum[i].x;
+            to[(2 * i + 1) * DK] = sum[i].y;
+          }
+        }
+      }
+    }
+  } else if (!STATE_ONLY && warp >= 8 && warp < 12) {
     // ------------------------------------------------ the state (thread = key column)
     const int r = tid - 256;
     const uint32_t row = quad + kColS;
     const bool mine = 32 * (warp - 8) < DK;  // warp-uniform
-    uint32_t unit = 0;                       // units begun
     // The matrix units cut every sum that they add to towards zero, so they are not given the state: a chunk
     // adds to the decayed remainder of it (2^-9 of the state, what bf16 leaves), and the value, which lies in
     // shared memory for QS, joins it here.  Value and remainder together hold more than a float, so a state
@@ -504,92 +544,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment seg = find_segment(a, u);
       if (seg.b < 0) break;
       const bool last = seg.index + 1 == seg.count;
-      if (STATE_ONLY && last) continue;
       const size_t head = ((size_t)seg.b * a.H + seg.h) * DV * DK + r, slot = (size_t)u * DV * DK + r;
-      float uncut = 1.f;
-      if (STATE_ONLY) {
-        mbar_arrive(&sh.s_ready);  // the last unit's state has been read
-        if (!(good = wait(sh, &sh.o_done, unit++ & 1))) break;
+      kept = owed = 0.f;
+      if (mine) {
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 16) {
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (seg.count > 1) x[i] = a.slots[slot + (c + i) * DK];
+            else if (a.S0 != nullptr) x[i] = to_f32(static_cast<const TST*>(a.S0)[head + (c + i) * DK]);
+            else x[i] = 0.f;
+          }
+          tmem_st16_nowait(row + c, reinterpret_cast<const uint32_t*>(x));
+        }
+        tmem_wait_st();
+      }
+#pragma unroll 1
+      for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
+        if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
+        const float2 gc = sh.g[n & 1][kC - 1];
+        const float2 decay = decay_of(gc);
+        const float more = fmaf(decay.x, owed, decay.y), keep = decay.x + more;
+        owed = keep > 0.5f ? __fdividef(more - (keep - decay.x), keep) : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
+        if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
+        if (n > 0 && !(good = wait(sh, &sh.qs_done, (n - 1) & 1))) break;  // it has read the last S
         tc_fence_after();
-        uncut = sh.uncut[(unit - 1) & 3];
-      } else {
-        kept = owed = 0.f;
         if (mine) {
+          uint32_t s[16], w[8];
+          tmem_ld16_nowait(row, s);
+          load_values(0, w);
+          const float2 keep2 = make_float2(keep, keep), kept2 = make_float2(kept, kept), drop2 = make_float2(-kept, -kept);
 #pragma unroll 1
           for (int c = 0; c < DV; c += 16) {
-            float x[16];
+            uint32_t x[16], old[8], hi[8], lo[8];
+            tmem_wait_ld();
+            tmem_join<16>(s);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (seg.count > 1) x[i] = a.slots[slot + (c + i) * DK];
-              else if (a.S0 != nullptr) x[i] = to_f32(static_cast<const TST*>(a.S0)[head + (c + i) * DK]);
-              else x[i] = 0.f;
+            for (int i = 0; i < 16; ++i) x[i] = s[i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) old[i] = w[i];
+            if (c + 16 < DV) {
+              tmem_ld16_nowait(row + c + 16, s);
+              load_values(c + 16, w);
             }
-            tmem_st16_nowait(row + c, reinterpret_cast<const uint32_t*>(x));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 value = unpack(old[i]), rest = pair_of(x + 2 * i), sum = __ffma2_rn(value, kept2, rest);
+              hi[i] = pack_bf16x2(sum.x, sum.y);
+              const float2 left = rest_of(rest, __ffma2_rn(value, drop2, unpack(hi[i])));
+              lo[i] = pack_bf16x2(left.x, left.y);
+              const float2 y = __fmul2_rn(left, keep2);
+              x[2 * i] = __float_as_uint(y.x);
+              x[2 * i + 1] = __float_as_uint(y.y);
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              unsigned char* to = place_of(c + 8 * v);
+              *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
+              *reinterpret_cast<uint4*>(to + L::s) = make_uint4(lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
+            }
+            tmem_st16_nowait(row + c, x);
           }
           tmem_wait_st();
         }
-#pragma unroll 1
-        for (int t = seg.t0; t < seg.t1; t += kC, ++n) {
-          if (!(good = wait(sh, &sh.g_full[n & 1], (n >> 1) & 1))) break;
-          const float2 gc = sh.g[n & 1][kC - 1];
-          const float2 decay = decay_of(gc);
-          const float more = fmaf(decay.x, owed, decay.y), keep = decay.x + more;
-          owed = keep > 0.5f ? __fdividef(more - (keep - decay.x), keep) : 0.f;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
-          if (t > seg.t0 && !(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
-          if (n > 0 && !(good = wait(sh, &sh.qs_done, (n - 1) & 1))) break;  // it has read the last S
-          tc_fence_after();
-          if (mine) {
-            uint32_t s[16], w[8];
-            tmem_ld16_nowait(row, s);
-            load_values(0, w);
-            const float2 keep2 = make_float2(keep, keep), kept2 = make_float2(kept, kept), drop2 = make_float2(-kept, -kept);
-#pragma unroll 1
-            for (int c = 0; c < DV; c += 16) {
-              uint32_t x[16], old[8], hi[8], lo[8];
-              tmem_wait_ld();
-              tmem_join<16>(s);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = s[i];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) old[i] = w[i];
-              if (c + 16 < DV) {
-                tmem_ld16_nowait(row + c + 16, s);
-                load_values(c + 16, w);
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 value = unpack(old[i]), rest = pair_of(x + 2 * i), sum = __ffma2_rn(value, kept2, rest);
-                hi[i] = pack_bf16x2(sum.x, sum.y);
-                const float2 left = rest_of(rest, __ffma2_rn(value, drop2, unpack(hi[i])));
-                lo[i] = pack_bf16x2(left.x, left.y);
-                const float2 y = __fmul2_rn(left, keep2);
-                x[2 * i] = __float_as_uint(y.x);
-                x[2 * i + 1] = __float_as_uint(y.y);
-              }
-#pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                unsigned char* to = place_of(c + 8 * v);
-                *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
-                *reinterpret_cast<uint4*>(to + L::s) = make_uint4(lo[4 * v], lo[4 * v + 1], lo[4 * v + 2], lo[4 * v + 3]);
-              }
-              tmem_st16_nowait(row + c, x);
-            }
-            tmem_wait_st();
-          }
-          kept = keep;
-          fence_proxy_async();
-          tc_fence_before();
-          mbar_arrive(&sh.s_ready);
-        }
+        kept = keep;
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&sh.s_ready);
       }
       if (!good) break;
-      if (!STATE_ONLY && seg.t1 > seg.t0) {
+      if (seg.t1 > seg.t0) {
         if (!(good = wait(sh, &sh.st_done, (n - 1) & 1))) break;
         tc_fence_after();
       }
-      if (mine && (STATE_ONLY || last)) {
+      if (mine && last) {
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
           uint32_t s[16];
@@ -597,15 +628,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           tmem_join<16>(s);
           uint32_t w[8];
-          if (!STATE_ONLY) load_values(c, w);
+          load_values(c, w);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (STATE_ONLY) {
-              a.slots[slot + (c + i) * DK] = __uint_as_float(s[i]) * uncut;
-            } else {
-              const float value = i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
-              static_cast<TST*>(a.S)[head + (c + i) * DK] = from_f32<TST>(fmaf(value, kept, __uint_as_float(s[i])));
-            }
+            const float value = i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+            static_cast<TST*>(a.S)[head + (c + i) * DK] = from_f32<TST>(fmaf(value, kept, __uint_as_float(s[i])));
           }
         }
       }
@@ -617,7 +644,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Rows past the segment's end hold another prompt's tokens, or none: K and V rows there become zero.
     const int r = tid - 384;
     const uint32_t keys = quad + kColK;
-    int units_done = 0;
     const bool mine = 32 * (warp - 12) < DK;  // warp-uniform
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
@@ -625,9 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seg.b < 0) break;
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       float2 later = make_float2(0.f, 0.f);  // log2 of the decay from the chunk's end to the segment's
-      // Chunks weighed by their share of the sum's square, and how often they are cut: by every chunk
-      // from their own on that decays and is not yet below the sum's last place.
-      float sum = 0.f, cuts = 0.f;
       const int chunks = chunks_of(seg);
 #pragma unroll 1
       for (int at = 0; at < chunks; ++at, ++n) {
@@ -658,12 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(good = meet(sh, &sh.k_meet, met))) break;
         }
         float2 gc = g[kC - 1];
-        if (STATE_ONLY) {
-          sum += ex2_approx(2.f * fminf(later.x, 0.f));
-          if (gc.x != 0.f && later.x > -24.f) cuts += sum;
-          if (r == 0) sh.uncut[units_done & 3] = 1.f + kUncutSum<TST> * (cuts / sum);
-          gc = later = add2(later, gc);
-        }
+        if (STATE_ONLY) gc = later = add2(later, gc);
         if (mine) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {  // 64 tokens
@@ -706,10 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_empty[n & 1]);
       }
-      ++units_done;
-      if (STATE_ONLY && r == 0) a.decay[u] = ex2_approx(later.x + later.y);
+      if (STATE_ONLY && r == 0) a.decay[u] = decay_of(later);
     }
-  } else if (warp == 16 || warp == 19) {
+  } else if (warp == 19 || (!STATE_ONLY && warp == 16)) {
     // ------------------------------------------------ TMA loads
     auto load = [&](const CUtensorMap* map, unsigned char* to, int columns, int h, int t, uint64_t* full) {
       if (lane == 0) {
@@ -719,8 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    const bool keys = warp == 19;  // K and Q, else V
-    int loads = 0;                 // tiles asked for
+    // One warp K and Q, one V; in the pass over states one both.
+    const bool keys = warp == 19, values = STATE_ONLY || !keys;
+    int nk = 0, nv = 0;  // tiles asked for
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);
@@ -728,30 +746,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (STATE_ONLY && seg.index + 1 == seg.count) continue;
       const int h = seg.h, hk = h / (a.H / a.Hk);
       const int chunks = chunks_of(seg);
+      int tile = 0;  // of the segment's K and Q tiles, the next
 #pragma unroll 1
       for (int at = 0; at < chunks && good; ++at) {
-        const int t = chunk_at<STATE_ONLY>(seg, at);
         if (keys) {
+          // K's place is free before V's: a chunk ahead where one warp loads both
+          const int to = L::step * min(at + (STATE_ONLY ? 2 : 1), chunks);
 #pragma unroll 1
-          for (int tile = 0; tile < L::step; ++tile, ++loads) {
-            const int i = place<L::nk>(loads);
-            if (loads >= L::nk && !(good = wait(sh, &sh.kq_empty[i], turn<L::nk>(loads) ^ 1))) break;
-            load(tile == 0 ? &mk : &mq, smem + i * L::k, DK, hk, t, &sh.kq_full[i]);
+          for (; tile < to; ++tile, ++nk) {
+            const int i = place<L::nk>(nk);
+            if (nk >= L::nk && !(good = wait(sh, &sh.kq_empty[i], turn<L::nk>(nk) ^ 1))) break;
+            load(tile % L::step == 0 ? &mk : &mq, smem + i * L::k, DK, hk, chunk_at<STATE_ONLY>(seg, tile / L::step),
+                 &sh.kq_full[i]);
           }
-        } else {
-          const int i = place<L::nv>(loads);
-          if (loads >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(loads) ^ 1))) break;
-          load(&mv, smem + L::at_v + i * L::v, DV, h, t, &sh.v_full[i]);
-          ++loads;
+        }
+        if (values && good) {
+          const int i = place<L::nv>(nv);
+          if (nv >= L::nv && !(good = wait(sh, &sh.v_empty[i], turn<L::nv>(nv) ^ 1))) break;
+          load(&mv, smem + L::at_v + i * L::v, DV, h, chunk_at<STATE_ONLY>(seg, at), &sh.v_full[i]);
+          ++nv;
         }
       }
     }
-    if (!good)  // leave no copy in flight behind: the last ones
+    if (!good) {  // leave no copy in flight behind: the last ones
 #pragma unroll 1
-      for (int i = 1; i <= (keys ? L::nk : L::nv) && i <= loads; ++i) {
-        if (keys) wait_out(&sh.kq_full[place<L::nk>(loads - i)], turn<L::nk>(loads - i));
-        else wait_out(&sh.v_full[place<L::nv>(loads - i)], turn<L::nv>(loads - i));
-      }
+      for (int i = 1; i <= L::nk && i <= nk; ++i) wait_out(&sh.kq_full[place<L::nk>(nk - i)], turn<L::nk>(nk - i));
+#pragma unroll 1
+      for (int i = 1; i <= L::nv && i <= nv; ++i) wait_out(&sh.v_full[place<L::nv>(nv - i)], turn<L::nv>(nv - i));
+    }
   } else if (warp == 17) {
     // ------------------------------------------------ MMAs
     // The next unit that has tokens, from u on; its number, and its chunks in `chunks`.
@@ -788,7 +810,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto q_rows = [&](int n) { return by_rows + start(place<L::nk>(n * L::step + 1) * L::k); };
     auto k_rows = [&](int n) { return by_rows + start(place<L::nk>(n * L::step) * L::k); };
     int chunks, later;
-    uint32_t unit = 0;  // units begun
     int u = find(blockIdx.x, chunks);
     if (!STATE_ONLY && u < units && (good = landed(0))) {
       tc_fence_after();
@@ -803,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < chunks; ++i, ++n) {
         const int iv = place<L::nv>(n);
         if (STATE_ONLY) {
-          if (i == 0 && !(good = wait(sh, &sh.s_ready, unit++ & 1))) break;
+          if (n > 1 && !(good = wait(sh, state_read(sh, n), (n - 2) >> 1 & 1))) break;
           if (!(good = wait(sh, state_keys(sh, n), n >> 1 & 1))) break;
         } else {
           if (!(good = wait(sh, &sh.s_ready, n & 1))) break;
@@ -817,9 +838,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idv = idesc_bf16_f32(kC, DV, true);
         const uint64_t dv = by_columns + start(L::at_v + iv * L::v);
         const uint64_t rest = by_columns + start(place<L::nk>(n * L::step) * L::k);
+        const uint32_t to = tmem + (STATE_ONLY && n & 1 ? kColO : kColS);
         auto add_third = [&] {
 #pragma unroll
-          for (int c = 0; c < kC; c += 16) mma_bf16(tmem + kColS, rest + c * 8, dv + c * 8, idv | kTransposedA, 1);
+          for (int c = 0; c < kC; c += 16) mma_bf16(to, rest + c * 8, dv + c * 8, idv | kTransposedA, 1);
         };
         if (elect_one()) {
           if (!THIRD) mma_commit(&sh.kq_empty[place<L::nk>(n * L::step)]);  // the scores have read K, and K' is made
@@ -827,8 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 1; part >= 0; --part)  // remainders first: their sum is small, and cut by little
 #pragma unroll
             for (int c = 0; c < kC; c += 16)
-              mma_bf16_tmem_a(tmem + kColS, tmem + kColK - (STATE_ONLY && !(n & 1) ? 128 : 0) + 64 * part + c / 2,
-                              dv + c * 8, idv, !STATE_ONLY || i + (1 - part) + c > 0);
+              mma_bf16_tmem_a(to, tmem + kColK - (STATE_ONLY && !(n & 1) ? 128 : 0) + 64 * part + c / 2,
+                              dv + c * 8, idv, !STATE_ONLY || (1 - part) + c > 0);
           if (!STATE_ONLY) mma_commit(THIRD ? &sh.st_part : &sh.st_done);
         }
         __syncwarp();
@@ -841,7 +863,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_commit(state_done(sh, n));
             mma_commit(&sh.v_empty[iv]);
-            if (i + 1 == chunks) mma_commit(&sh.o_done);
           }
           __syncwarp();
           continue;
@@ -896,11 +917,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       u = next;
       chunks = later;
     }
-  } else if (warp == 18 || warp == 0) {
+  } else if (warp == 18 || (STATE_ONLY && warp == 16)) {
     // ------------------------------------------------ decays: four tokens a lane
     // In the pass over states, whose other steps are short, two warps take turns.
     constexpr int kTurns = STATE_ONLY ? 2 : 1;
-    const int turn = STATE_ONLY && warp == 0;
+    const int turn = warp == 16;
 #pragma unroll 1
     for (int u = blockIdx.x; u < units && good; u += gridDim.x) {
       const Segment seg = find_segment(a, u);

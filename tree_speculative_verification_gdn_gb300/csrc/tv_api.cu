@@ -413,7 +413,7 @@ int tv_linear_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_
     a.seg_len = tv::linear_attn_segment(B, T, max_len, H, dk, dv, io_dtype);
     const size_t segments = (size_t)B + T / a.seg_len;
     a.slots = static_cast<float*>(workspace);
-    a.decay = a.slots + segments * H * dv * dk;
+    a.decay = reinterpret_cast<float2*>(a.slots + segments * H * dv * dk);
   }
   return cuda_status(tv::launch_linear_attn_prompt(a, stream));
 }

@@ -186,10 +186,10 @@ struct LinAttnArgs {
   int32_t* err;
   // Prompts longer than seg_len are cut into segments of that many tokens that run side by side
   // (0: no prompt is cut).  slots [segments, H, dv, dk] fp32 holds each segment's own contribution
-  // to the state, then the state it starts from; decay [segments, H] its total decay.
+  // to the state, then the state it starts from; decay [segments, H] its total decay as two floats.
   int seg_len;
   float* slots;
-  float* decay;
+  float2* decay;
 };
 // Segment length for these sizes, 0 for none; host-only.
 int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io);
