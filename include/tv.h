@@ -539,11 +539,17 @@ TV_API int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, c
  *                                           TV_ERR_TIMEOUT (a bounded device wait gave up; that
  *                                           prompt's outputs are then unspecified)
  * Rounding: products accumulate in fp32; bf16 operands that are themselves sums or scaled
- * (scores, decayed keys, states) enter the matrix units as a bf16 pair, value and remainder.  An
- * fp32 state of bf16 inputs is off by 5e-7 to 2e-6 of its norm (three parts of a key), of fp32
- * inputs by 3e-7.  The matrix units cut what they add to an accumulator; a decaying state gets that
- * back on average, one whose decays are exactly 1 does not and loses 1e-6 of itself per thousand
- * tokens.
+ * (scores, decayed keys, states) enter the matrix units as a bf16 pair, value and remainder, the
+ * keys of an fp32 state in three parts.  From chunk to chunk a state is carried in 32 bits, and the
+ * matrix units, which cut what they add to an accumulator, add to its small remainder only.  An
+ * fp32 state of bf16 inputs is off by at most 1e-6 of its norm, whatever its length, its decays and
+ * the share of tokens that add to it (measured: 5e-7 after 32768 tokens); what is left of an S0 to
+ * which nothing was added, decayed to e^-x of itself, by x * 1e-7 more.
+ * fp32 inputs (and bf16 prompts too short for a chunk) are walked token by token, as by
+ * tv_linear_attn_step, and round an fp32 state once a token: off by 3e-7 where decays forget within
+ * thousands of tokens, by 6e-6 after 32768 tokens of decays 1 or 1 - 1e-5; decays within 1e-6 of 1
+ * round an element the same way again and again, 2e-4 after 32768 tokens at the worst (1 - 2^-24).
+ * The states are not a gated delta rule's: no tv_gdn_* call takes them.
  * A non-finite input makes later tokens of its prompt and head non-finite, and may make earlier
  * ones of the same 128-token chunk so; other prompts are not touched.
  * Supported: dk, dv in {64, 128}; H a multiple of Hk; (io, state) as tv_gdn_tree_verify_fork.
@@ -586,7 +592,7 @@ TV_API int tv_linear_attn_step(const void* q, int64_t q_stride, const void* k, i
  *   x, gate, out  [rows, H, d] io_dtype   row r starts at x + r * x_stride (elements); gate may be
  *                 NULL (factor 1); out may be x itself
  *   weight        [d] io_dtype, or NULL (out is not scaled by a weight, and weight_offset is not used)
- * Arithmetic is fp32, rounded once on store.  Any d from 1 to 32768 and any stride of at least H * d;
+ * Arithmetic is fp32, rounded once on store.  silu(g) of gates below -87.3, at most 1e-36, is 0.  Any d from 1 to 32768 and any stride of at least H * d;
  * base addresses need only their element's alignment.  rows * H <= 2^31 - 256.
  * ---------------------------------------------------------------------------------------- */
 TV_API int tv_gated_rmsnorm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,

@@ -294,8 +294,9 @@ cudaError_t prompt_dims(const LinAttnArgs& a, cudaStream_t s) {
 // Eight columns a thread, DK / 8 lanes a row, NP rows a thread: a CTA updates NP * (1024 / DK) rows of
 // one head's state.  The state is read and written once, straight through registers; k and q are the
 // same for every row and come from L1 after the first.  Bound by HBM: 200 sequences of 16 fp32 heads 54 us
-// = 6.4 TB/s, 0.95 of a plain copy's rate; 64 of 32 bf16 heads 23 us, 0.87.  NP = 4 is the best where that
-// counts (1: 33 us, 2: 23.8, 8: 22.9 with fewer CTAs for small batches).
+// = 6.4 TB/s, 0.95 of a plain copy's rate; 64 of 32 bf16 heads 24.6 us as a call, 0.81 (17 us replayed on one
+// state, part of which stays in L2).  NP = 4 is the best where that counts (64 of 32 bf16 heads, states out of
+// L2, 23 us; NP 1: 33, 2: 23.8, 8: 22.9 with fewer CTAs for small batches).
 template <typename TIO, typename TST, int DK, int NP>
 __global__ void __launch_bounds__(kThreads) linear_attn_step_kernel(LinStepArgs a) {
   constexpr int LPR = DK / 8, RPP = kThreads / LPR;  // lanes per row, rows per pass
@@ -352,11 +353,13 @@ int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io
     // One CTA per SM walks whole (segment, head) units.  Measured on a GB300, in us: a unit costs 5 and
     // 3.2 a chunk of 128 tokens, in the pass over states alone 5 and 1.2; a launch 4, the scan 3 and
     // 0.4 a segment.  The cheapest cut of the longest prompt into equal pieces, or none.  (16 heads, one
-    // prompt: 768 tokens 26 uncut and 24 in six pieces; 4096 tokens 108 uncut, 38 in eight pieces.  32
-    // heads, 32768 tokens: 816 uncut, 304 in four pieces, 315 in nine.)
-    // fp32 states take 1.2 to 1.3 times as long in both passes (third part of the keys) and are cut alike.
+    // prompt: 768 tokens 27 uncut and in six pieces; 4096 tokens 112 uncut, 39 in eight pieces.  32
+    // heads, 32768 tokens: 848 uncut, 317 in four pieces.)
+    // fp32 states take 1.2 to 1.3 times as long in both passes (third part of the keys) and are cut alike
+    // (32768 tokens 1001 uncut, 401; 8 ragged prompts of up to 3001, 32 heads, 129 and 109).
     const int longest = (max_len + 127) / 128;
-    // Prompts of one length run in rounds; of ragged ones the longest, which start first, or the sum counts.
+    // Prompts of one length run in rounds; of ragged ones the longest, which start first, or the sum counts,
+    // each with a margin for CTAs that draw more than their share.
     auto pass = [&](int chunks, double each) {
       const double units = (double)H * std::max(B, (T / 128 + chunks - 1) / chunks), alone = 5 + each * chunks;
       if ((long long)B * max_len == T) return 4 + std::ceil(units / sms) * alone;
@@ -373,6 +376,10 @@ int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io
     }
     return best < longest ? best * 128 : 0;
   }
+  // fp32: four CTAs for every SM, unless the prompts alone are near that.  Measured, in us, uncut and with two,
+  // four and eight an SM: one prompt of 300 tokens, 4 heads 57, 28, 28, 28; 1000 tokens, 32 heads 181, 139,
+  // 124, 131; 4096 tokens, 16 heads 726, 271, 263, 240; 32768 tokens, 8 heads 5755, 858, 877, 884; 8 ragged
+  // prompts of up to 3001, 8 heads 530, 163, 144, 153.
   long long seg = ((long long)T * H * (dv / kRows) + 4 * sms - 1) / (4 * sms);
   seg = (seg + 63) / 64 * 64;
   return max_len > 3 * seg ? (int)seg : 0;

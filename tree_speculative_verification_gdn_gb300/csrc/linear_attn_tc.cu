@@ -9,14 +9,18 @@
 // swizzle); accumulators, the state's transpose, P and K' fill the 512 columns of tensor memory:
 //     QK: scores [token i, token j]      A = Q,    B = K
 //     QS: O [token i, value]             A = Q,    B = S^T     (bf16 pair); its rows then scaled in place
-//     ST: S^T [key column, value]        A = K'^T, B = V       (bf16 pair, tensor memory), added to the state
-//         fp32 states: a third part as well (shared memory, in K's place), after QS
+//     ST: S^T [key column, value]        A = K'^T, B = V       (bf16 pair, tensor memory), added to what bf16
+//         leaves of the state; fp32 states: a third part as well (shared memory, in K's place), after QS
 //     PV: O, added to                    A = P,    B = V       (bf16 pair, tensor memory, over the scores)
 // P, K' and S are fp32 results and enter as value + remainder, two bf16 each (2^-16 left out): one
 // bf16 alone would put an error as large as the output's own rounding on every output, and 2^-9 on
 // an fp32 state.  For an fp32 state K' has a third part, written over K once the scores have read it:
-// without it the state is off by 2.5e-6 of its norm, with it by 5e-7 to 1e-6 (32 prompts of 2048 tokens
-// 398 -> 463 us; a bf16 state's own rounding is a thousand times either).  Exponents only ever go down:
+// without it the state is off by 2.5e-6 of its norm, with it by 5e-7 (32 prompts of 2048 tokens
+// 408 -> 476 us; a bf16 state's own rounding is a thousand times either).  The matrix units cut every sum that
+// they add to towards zero, a state by 1e-6 and more of itself per thousand tokens; how much depends on
+// what is added, so no factor makes up for it (one that did on average was off by 2e-4 after 32768 tokens of
+// zero keys).  They add to the state's remainder instead, 2^-9 of it, and its value joins outside
+// (batch of 32 prompts 394 -> 405 us).  Exponents only ever go down:
 // within 32 x 32 diagonal blocks each 2^(g_i - g_j) is taken directly, elsewhere as
 // 2^(g_i - g_r) 2^(g_r - g_j) with r the first row of i's block, so no factor exceeds 1 however fast
 // the decay.  g is summed and kept as two floats: after a reset (alpha
@@ -38,13 +42,16 @@
 //
 // In the pass over states alone (STATE_ONLY: the contributions of a cut prompt's segments) chunks come
 // last to first: with the decay from a chunk's end to the segment's folded into K', the state only adds
-// up, tensor memory holds two K', and nobody touches S until the end.  The warps without outputs to write
-// make the third part there (one prompt of 32768 tokens, fp32 states, 429 -> 386 us).
+// up.  Tensor memory holds two K' and two sums: a chunk's starts from zero and joins the segment's in the
+// registers of eight warps, 64 values a thread (one prompt of 32768 tokens 310 -> 316 us, a cut fp32 state off
+// by 5e-7 instead of up to 6e-6).  The warps without outputs to write make the third part there (the same
+// with fp32 states 429 -> 386 us), and one warp loads both K and V, so that two can sum the decays.
 //
-// Measured on a GB300: 32 prompts of 2048 tokens, 32 heads of 128, 392 us = 5.6 TB/s, 0.82 of a plain copy's
-// rate; the tensor pipe is busy half of the time, issue slots too.  What bounds it is the chain a chunk
-// hangs on, about 6000 clocks: the state's conversion 2300, ST 1300, QS 1500, scaling 600 (P alongside, 3400
-// from its scores), then PV and the next scores.  Alone an MMA takes 70 clocks, here about 100, beside the
+// Measured on a GB300: 32 prompts of 2048 tokens, 32 heads of 128, 408 us replayed in a graph = 5.4 TB/s, 0.79
+// of a plain copy's rate (434 us as a call on changing inputs, 0.74); the tensor pipe is busy half of the
+// time, issue slots too.  What bounds it is the chain a chunk hangs on, about 6300 clocks: the state's
+// conversion 2600, ST 1300, QS 1500, scaling 600 (P alongside, 3400 from its scores), then PV and, when PV has
+// read P, the next scores.  Alone an MMA takes 70 clocks, here about 100, beside the
 // other roles' traffic.  Other orders of the four products, more warps on the state (768 threads leave 80
 // registers, and K' spills) and copying the state in bulk were slower.
 #include <type_traits>

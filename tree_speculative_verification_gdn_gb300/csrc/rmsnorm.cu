@@ -60,8 +60,8 @@ __device__ __forceinline__ float row_sum(float x, float* s_part) {
 }
 
 // g / (1 + exp(-g)), to the precision that the element type can show: bf16 keeps 2^-8 of a value, the
-// hardware's 2^x and reciprocal are good to 2^-21 of it where the gate is not yet 0 or 1.  They flush
-// denormals, which neither 1 + exp(-g) nor a bf16 result has room for.
+// hardware's 2^x and reciprocal are good to 2^-21 of it where the gate is not yet 0 or 1.  Reciprocals of more
+// than 2^126 are 0 in both forms: silu of a gate below -87.3, at most 1e-36, is then 0.
 __device__ __forceinline__ float2 silu2(float2 g, bf16) {
   constexpr float k = -1.4426950408889634f;  // -log2(e)
   const float2 x = __fmul2_rn(g, make_float2(k, k));

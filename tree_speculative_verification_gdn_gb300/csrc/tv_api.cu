@@ -437,7 +437,7 @@ int tv_linear_attn_step(const void* q, int64_t q_stride, const void* k, int64_t 
 
 namespace {
 
-constexpr int kNormMax = 32768;  // widest row: 1024 threads of four 8-column vectors
+constexpr int kNormMax = 32768;  // widest row: five 8-column vectors for each of 832 threads, at any offset
 
 bool el(const void* p, int dtype) {  // aligned to its element
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype == TV_F32 ? 3u : 1u)) == 0;
