@@ -545,10 +545,10 @@ TV_API int tv_accept_walk(const int32_t* parents, const int32_t* draft_tokens, c
  * fp32 state of bf16 inputs is off by at most 1e-6 of its norm, whatever its length, its decays and
  * the share of tokens that add to it (measured: 5e-7 after 32768 tokens); what is left of an S0 to
  * which nothing was added, decayed to e^-x of itself, by x * 1e-7 more.
- * fp32 inputs (and bf16 prompts too short for a chunk) are walked token by token, as by
- * tv_linear_attn_step, and round an fp32 state once a token: off by 3e-7 where decays forget within
- * thousands of tokens, by 6e-6 after 32768 tokens of decays 1 or 1 - 1e-5; decays within 1e-6 of 1
- * round an element the same way again and again, 2e-4 after 32768 tokens at the worst (1 - 2^-24).
+ * fp32 inputs are walked token by token, and a state takes in each with one rounding to nearest: off
+ * by 3e-7 after some thousand tokens of mixed decays, by 1.1e-6 after 8192 and 2.2e-6 after 32768
+ * that do not decay; decays themselves cost nothing (a state to which nothing is added: 1e-7).
+ * Values beyond 2^106 may overflow there.
  * The states are not a gated delta rule's: no tv_gdn_* call takes them.
  * A non-finite input makes later tokens of its prompt and head non-finite, and may make earlier
  * ones of the same 128-token chunk so; other prompts are not touched.

@@ -110,3 +110,45 @@ def test_states_of_many_prompts_with_decays_per_token():
     want = torch.from_numpy(recurrence(c)[1]).to(DEV)
     assert not any(err)
     assert float((S.double() - want).norm() / want.norm()) <= bound(5)
+
+
+"""fp32 inputs.  A token's product is rounded into the state to nearest, once: mean zero, at most u, so sqrt(T) u
+in the norm if every one of T tokens remained.  Its dot products and scalings take a few u more, decays none: they
+are products of two floats.  A state to which nothing is added keeps to those few."""
+
+
+def bound32(tokens, adds=True):
+    return (tokens ** 0.5 * U if adds else 0.0) + 2.0 ** -22
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,H,dk,dv", [(8192, 128, 128, 128), (20000, 7, 128, 128), (9001, 7, 64, 64), (300, 7, 64, 128),
+                                       (333, 7, 128, 64)])
+def test_state_of_fp32_prompts(kind, T, H, dk, dv):
+    cut = tv.tv_linear_attn_workspace_size(1, T, T, H, dk, dv, torch.float32) > 0
+    assert cut == (H < 128)
+    c = make(T, H, dk, dv, kind, torch.float32)
+    _, S, err = L.prompt(c)
+    assert not any(err)
+    k, far = c["k"][:, 0].double(), torch.arange(T - 1, -1, -1, dtype=torch.float64, device=DEV)
+    for h in range(7):
+        a = c["alpha"][h].double()
+        want = (c["v"][:, h].double() * (a ** far)[:, None]).T @ k + c["S0"][0, h].double() * a ** T
+        off = float((S[0, h].double() - want).norm() / want.norm().clamp_min(1e-30))
+        assert off <= bound32(T, kind not in ("no keys", "no values", "first token")), (h, float(a), off)
+
+
+def test_fp32_outputs_across_fast_and_slow_blocks():
+    # blocks that pass the range of 1 / D between others, resets, decays of 1, a ragged end
+    T, H = 1501, 6
+    g = torch.Generator().manual_seed(5)
+    alpha = torch.rand(T, H, generator=g) ** torch.tensor([0.0, 1e-6, 1e-3, 0.1, 1.0, 8.0])
+    alpha[200:216, 1:] = 1e-3
+    alpha[640, :4] = 0.0
+    alpha[900:1000, 2] = 1.0
+    c = L.make([T - 7, 7], 3, H, 128, 128, "f32", "f32", seed=2, alpha=alpha)
+    out, S, err = L.prompt(c, max_len=T)
+    assert not any(err)
+    (o, s), (ao, as_) = recurrence(c), recurrence(c, absolute=True)
+    L.check(out, o, ao, T, 128, "f32", "out")
+    L.check(S, s, as_, T, 128, "f32", "S")

@@ -10,6 +10,13 @@
 // It is bound by the multiply-adds, three a state element and token, and by the loads of k and q from
 // shared memory that feed them: four rows a lane share each load, columns go in pairs (32 prompts of
 // 300 fp32 tokens, 32 heads: one row a lane 1418 us, two 866, four 702, four in pairs 627).
+// fp32 prompts may be long.  A state that takes in every decay as it comes is rounded by each, the same way for
+// thousands of tokens where decays are near to 1: 2e-4 of itself after 32768.  There, with D_t the decay since the
+// state was last scaled,
+//     Z_t = Z_{t-1} + (v_t / D_t) k_t^T,     o_t = D_t q_scale Z_t q_t:
+// two multiply-adds and one rounding a token (the 627 us above become 571).  Z is scaled by D, a product of two floats, only once that is below a
+// half.  kBlock tokens that decay below 2^-20 together (1 / D leaves the range) are walked as they stand, like bf16
+// prompts, which come here only when they are short.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -25,6 +32,7 @@ constexpr int kLPR = 8;                                // lanes per state row
 constexpr int kRPL = 4;                                // rows per lane
 constexpr int kRows = kThreads / kLPR * kRPL;          // rows per CTA
 constexpr int kBlock = 16;                             // tokens staged at a time
+constexpr float kDirect = 1.f / (1 << 20);             // decay of a block below which it is walked as it stands
 
 // Eight elements as stored, then as floats.
 template <typename T> struct Raw8;
@@ -65,16 +73,24 @@ __device__ __forceinline__ float sum8(const float* v, int l) {
   return mine + __shfl_xor_sync(0xffffffffu, give, 1);
 }
 
+// Product of two numbers of two floats each, the second at most half a step of the first.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  const float x = a.x * b.x, y = fmaf(a.x, b.x, -x) + fmaf(a.x, b.y, a.y * b.x), hi = x + y;
+  return make_float2(hi, y - (hi - x));
+}
+
 // One segment of one prompt, kRows rows of one head's state.  STATE_ONLY: the segment's own
 // contribution to the state (from zero) and its total decay, into the workspace.
 template <typename TIO, typename TST, int DK, int DV, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
+  constexpr bool SPLIT = std::is_same<TIO, float>::value;  // S = D Z
   constexpr int CPL = DK / kLPR;         // columns per lane: four at 4 l + 32 j
   constexpr int kSlabs = DV / kRows;
   constexpr int kVec = kBlock * DK / 8 / kThreads;   // 8-column vectors of k (and of q) per thread
   constexpr int kVPT = kBlock * kRows / kThreads;    // values of v per thread
-  __shared__ float s_k[kBlock][DK], s_q[STATE_ONLY ? 1 : kBlock][DK], s_v[kBlock][kRows], s_a[kBlock];
-  __shared__ float s_o[STATE_ONLY ? 1 : kBlock][kRows];
+  __shared__ __align__(16) float s_k[kBlock][DK], s_q[STATE_ONLY ? 1 : kBlock][DK], s_v[kBlock][kRows];
+  __shared__ __align__(16) float s_o[STATE_ONLY ? 1 : kBlock][kRows];
+  __shared__ float s_a[kBlock];
 
   const int tid = threadIdx.x;
   const int slab = blockIdx.x % kSlabs, u = blockIdx.x / kSlabs;
@@ -92,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
   TIO* op = static_cast<TIO*>(a.out) + h * DV + slab * kRows;
 
   const int l = tid % kLPR, row0 = tid / kLPR * kRPL;  // this lane's first row of the slab
-  float2 s2[kRPL][CPL / 2];  // column pairs
+  float2 s2[kRPL][CPL / 2];  // column pairs of S, or of Z
   float(&s)[kRPL][CPL] = reinterpret_cast<float(&)[kRPL][CPL]>(s2);
   const size_t head = (size_t)seg.b * a.H + h, slot = u;
 #pragma unroll
@@ -110,7 +126,16 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
       }
     }
   }
-  float2 total = make_float2(1.f, 0.f);  // the segment's decay, as two floats
+  float2 since = make_float2(1.f, 0.f), total = since;  // D, and the segment's decay so far
+  auto scale = [&] {  // Z becomes S
+#pragma unroll
+    for (int r = 0; r < kRPL; ++r)
+#pragma unroll
+      for (int c = 0; c < CPL / 2; ++c)
+        s2[r][c] = __ffma2_rn(s2[r][c], make_float2(since.x, since.x),
+                              __fmul2_rn(s2[r][c], make_float2(since.y, since.y)));
+    since = make_float2(1.f, 0.f);
+  };
 
   Raw8<TIO> rk[kVec], rq[kVec];
   TIO rv[kVPT];
@@ -133,10 +158,36 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
       const int e = tid + i * kThreads, tok = t + e / kRows;
       rv[i] = tok < seg.t1 ? vp[tok * a.v_stride + e % kRows] : from_f32<TIO>(0.f);
     }
-    if (tid < kBlock) ra = t + tid < seg.t1 ? __ldg(a.alpha + (t + tid) * a.alpha_stride + h) : 1.f;
+    const int tok = t + tid % kBlock;  // every warp has them all
+    ra = tok < seg.t1 ? __ldg(a.alpha + tok * a.alpha_stride + h) : 1.f;
   };
   fetch(seg.t0);
+  auto last_of = [](float2 x) {
+    return make_float2(__shfl_sync(0xffffffffu, x.x, kBlock - 1), __shfl_sync(0xffffffffu, x.y, kBlock - 1));
+  };
   for (int t = seg.t0; t < seg.t1; t += kBlock) {
+    float2 now = make_float2(1.f, 0.f);  // SPLIT: D_i in lane i % kBlock, and 1 / D_i
+    float inverse = 1.f;
+    bool direct = true;
+    if (SPLIT) {
+      float2 p = make_float2(ra, 0.f);  // the product of the block's decays up to token i
+#pragma unroll
+      for (int o = 1; o < kBlock; o <<= 1) {
+        const float2 up = make_float2(__shfl_up_sync(0xffffffffu, p.x, o, kBlock),
+                                      __shfl_up_sync(0xffffffffu, p.y, o, kBlock));
+        const float2 both = mul2(up, p);
+        if (tid % kBlock >= o) p = both;
+      }
+      const float2 whole = last_of(p);
+      direct = !(whole.x >= kDirect);
+      if (direct) {
+        scale();
+      } else {
+        now = mul2(since, p);
+        inverse = 1.f / now.x;
+      }
+      if (STATE_ONLY) total = mul2(total, whole);
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -151,34 +202,30 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < kVPT; ++i) {
-      const int e = tid + i * kThreads;
-      s_v[e / kRows][e % kRows] = to_f32(rv[i]);
+      const int e = tid + i * kThreads;  // one token a warp
+      s_v[e / kRows][e % kRows] = to_f32(rv[i]) * (SPLIT ? __shfl_sync(0xffffffffu, inverse, e / kRows) : 1.f);
     }
     if (tid < kBlock) s_a[tid] = ra;
     __syncthreads();
     if (t + kBlock < seg.t1) fetch(t + kBlock);
     // Eight tokens; with SOME only those of the segment.
-    auto walk = [&](int u, auto some) {
-      constexpr bool SOME = decltype(some)::value;
+    auto walk = [&](int u, auto some, auto as_it_stands) {
+      constexpr bool SOME = decltype(some)::value, DIRECT = decltype(as_it_stands)::value;
       float dot[kRPL][8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
 #pragma unroll
         for (int r = 0; r < kRPL; ++r) dot[r][i] = 0.f;
         if (SOME && t + u + i >= seg.t1) continue;  // the same for the whole CTA
-        const float al = s_a[u + i];
-        float2 v[kRPL], d[kRPL];
+        const float al = DIRECT ? s_a[u + i] : 1.f;
+        float2 v[kRPL], sum[kRPL];
 #pragma unroll
         for (int r = 0; r < kRPL; ++r) {
           const float x = s_v[u + i][row0 + r];
           v[r] = make_float2(x, x);
-          d[r] = make_float2(0.f, 0.f);
+          sum[r] = make_float2(0.f, 0.f);
         }
         const float2 al2 = make_float2(al, al);
-        if (STATE_ONLY) {
-          const float x = total.x * al;
-          total = make_float2(x, fmaf(total.y, al, fmaf(total.x, al, -x)));
-        }
 #pragma unroll
         for (int j = 0; j < CPL / 4; ++j) {
           const float4 k4 = *reinterpret_cast<const float4*>(&s_k[u + i][4 * l + 32 * j]);
@@ -191,21 +238,37 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float2& x = s2[r][2 * j + c];
-              x = __ffma2_rn(v[r], kk[c], __fmul2_rn(al2, x));
-              if (!STATE_ONLY) d[r] = __ffma2_rn(x, qq[c], d[r]);
+              x = __ffma2_rn(v[r], kk[c], DIRECT ? __fmul2_rn(al2, x) : x);
+              if (!STATE_ONLY) sum[r] = __ffma2_rn(x, qq[c], sum[r]);
             }
         }
 #pragma unroll
-        for (int r = 0; r < kRPL; ++r) dot[r][i] = d[r].x + d[r].y;
+        for (int r = 0; r < kRPL; ++r) dot[r][i] = sum[r].x + sum[r].y;
       }
-      if (!STATE_ONLY)
+      if (!STATE_ONLY) {
+        const float by = SPLIT ? __shfl_sync(0xffffffffu, now.x, u + l) * a.q_scale : a.q_scale;
 #pragma unroll
-        for (int r = 0; r < kRPL; ++r) s_o[u + l][row0 + r] = sum8(dot[r], l) * a.q_scale;
+        for (int r = 0; r < kRPL; ++r) s_o[u + l][row0 + r] = sum8(dot[r], l) * by;
+      }
     };
+    const std::true_type yes;
+    const std::false_type no;
 #pragma unroll 1
     for (int u = 0; u < kBlock && t + u < seg.t1; u += 8) {
-      if (t + u + 8 <= seg.t1) walk(u, std::false_type());
-      else walk(u, std::true_type());
+      const bool whole = t + u + 8 <= seg.t1;
+      if constexpr (SPLIT) {
+        if (!direct) {
+          if (whole) walk(u, no, no);
+          else walk(u, yes, no);
+          continue;
+        }
+      }
+      if (whole) walk(u, no, yes);
+      else walk(u, yes, yes);
+    }
+    if (SPLIT && !direct) {
+      since = last_of(now);
+      if (!(since.x >= 0.5f)) scale();
     }
     if (!STATE_ONLY) {
       __syncthreads();
@@ -218,6 +281,7 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
   }
   const bool last = seg.index + 1 == seg.count;
   if (!STATE_ONLY && !last) return;
+  if (SPLIT) scale();
 #pragma unroll
   for (int r = 0; r < kRPL; ++r) {
     const int at = (slab * kRows + row0 + r) * DK + 4 * l;
@@ -232,7 +296,8 @@ __global__ void __launch_bounds__(kThreads) linear_attn_kernel(LinAttnArgs a) {
 
 // ------------------------------------------------------------------ states between segments
 // Slot s of a cut prompt holds the segment's own contribution dS_s and receives the state that
-// segment s starts from: X_0 = S0, X_{s+1} = decay_s X_s + dS_s.  Four columns a thread.  S0 itself
+// segment s starts from: X_0 = S0, X_{s+1} = decay_s X_s + dS_s, by two floats (a decay near 1 would round an
+// element the same way in every segment).  Four columns a thread.  S0 itself
 // is copied into slot 0, so that the last segment may write S over it while the first one runs.
 template <typename TST>
 __global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, int parts) {
@@ -243,7 +308,7 @@ __global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, in
   const int first = first_segment(a, b);
   const size_t size = (size_t)a.dv * a.dk, at = ((size_t)part * 256 + threadIdx.x) * 4;
   if (at >= size) return;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  float x[4] = {0.f, 0.f, 0.f, 0.f}, rest[4] = {0.f, 0.f, 0.f, 0.f};  // X as two floats
   if (a.S0 != nullptr) load_vec_rw<4>(static_cast<const TST*>(a.S0) + ((size_t)b * a.H + h) * size + at, x);
   // Four segments' values are asked for before the first is needed (one by one, a segment took 4 us).
   constexpr int kAhead = 4;
@@ -265,7 +330,13 @@ __global__ void __launch_bounds__(256) linear_attn_scan_kernel(LinAttnArgs a, in
         store_vec<4>(p + i * stride, x);
         if (s + i + 1 < n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = fmaf(g[i].x, x[c], fmaf(g[i].y, x[c], d[i][c]));
+          for (int c = 0; c < 4; ++c) {
+            const float2 kept = mul2(g[i], make_float2(x[c], rest[c]));
+            const float sum = kept.x + d[i][c], part = sum - kept.x;
+            const float low = kept.y + ((kept.x - (sum - part)) + (d[i][c] - part));
+            x[c] = sum + low;
+            rest[c] = low - (x[c] - sum);
+          }
       }
   }
 }
@@ -275,10 +346,12 @@ cudaError_t prompt_simt(const LinAttnArgs& a, cudaStream_t s) {
   const long long segments = a.seg_len > 0 ? (long long)a.B + a.T / a.seg_len : a.B;
   const long long grid = segments * a.H * (DV / kRows);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (a.seg_len > 0) {
-    linear_attn_kernel<TIO, TST, DK, DV, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    const cudaError_t e = launch_linear_attn_scan(a, s);
-    if (e != cudaSuccess) return e;
+  if constexpr (std::is_same<TIO, float>::value) {  // bf16 prompts are cut by the tensor-core form alone
+    if (a.seg_len > 0) {
+      linear_attn_kernel<TIO, TST, DK, DV, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
+      const cudaError_t e = launch_linear_attn_scan(a, s);
+      if (e != cudaSuccess) return e;
+    }
   }
   linear_attn_kernel<TIO, TST, DK, DV, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
@@ -377,9 +450,9 @@ int linear_attn_segment(int B, int T, int max_len, int H, int dk, int dv, int io
     return best < longest ? best * 128 : 0;
   }
   // fp32: four CTAs for every SM, unless the prompts alone are near that.  Measured, in us, uncut and with two,
-  // four and eight an SM: one prompt of 300 tokens, 4 heads 57, 28, 28, 28; 1000 tokens, 32 heads 181, 139,
-  // 124, 131; 4096 tokens, 16 heads 726, 271, 263, 240; 32768 tokens, 8 heads 5755, 858, 877, 884; 8 ragged
-  // prompts of up to 3001, 8 heads 530, 163, 144, 153.
+  // four and eight an SM: one prompt of 300 tokens, 4 heads 58, 30, 30, 30; 1000 tokens, 32 heads 185, 123,
+  // 111, 120; 4096 tokens, 16 heads 742, 238, 237, 218; 32768 tokens, 8 heads 5900, 788, 794, 787; 8 ragged
+  // prompts of up to 3001, 8 heads 544, 144, 134, 141; 4 prompts of 5000, 32 heads 1415, 1415, 1415, 1743.
   long long seg = ((long long)T * H * (dv / kRows) + 4 * sms - 1) / (4 * sms);
   seg = (seg + 63) / 64 * 64;
   return max_len > 3 * seg ? (int)seg : 0;
@@ -408,7 +481,7 @@ cudaError_t launch_linear_attn_scan(const LinAttnArgs& a, cudaStream_t s) {
 // 11.7 and 12.4.  32 prompts of 32 heads: 4 tokens 27 and 44; 16 tokens 50 and 44.)
 static bool short_prompts(const LinAttnArgs& a) {
   if (a.T == 0) return true;
-  if (a.max_len > 128) return false;
+  if (a.max_len > 128 || a.seg_len > 0) return false;
   const double units = (double)a.B * a.H, sms = device_sm_count();
   return 3 + 0.016 * units + a.max_len * (0.12 + 0.002 * units) < 6 + 5.5 * (long long)((units + sms - 1) / sms);
 }
