@@ -73,8 +73,9 @@ enum tv_status {
                                two logical blocks of the tree's window on one physical block */
   TV_ERR_SCRATCH = -9,      /* tv_tree_attn_static: the call needs more than
                                TV_STATIC_SCRATCH_BYTES of scratch */
-  TV_ERR_BAD_SEQLEN = -10   /* tv_linear_attn_prompt: cu_seqlens decreases, leaves [0, T], or
-                               holds a prompt longer than max_len */
+  TV_ERR_BAD_SEQLEN = -10,  /* packed prompts: cu_seqlens decreases, leaves [0, T], or holds a
+                               prompt longer than max_len */
+  TV_ERR_BAD_PROBS = -11    /* tv_accept_sample: no token has a positive probability */
 };
 
 enum tv_dtype { TV_F32 = 0, TV_BF16 = 1 };
@@ -620,6 +621,145 @@ TV_API int tv_residual_rmsnorm(const void* y, int64_t y_stride, const void* resi
                                const void* weight, int rows, int D, int io_dtype, int residual_dtype, float eps,
                                float weight_offset, void* residual_out, int64_t residual_out_stride, void* out,
                                int64_t out_stride, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_qk_norm_rope -- norms of queries and keys per head, their rotation by position, and the new
+ * keys and values into the paged cache, in one pass.
+ *
+ * What lies between a softmax layer's projections and its attention.  For every head of q and k
+ *     y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)      (norm = 0: y = x)
+ * over its hd columns, then the first rotary_dim columns are rotated as in tv_tree_attn: pairs
+ * (y_c, y_{c + rotary_dim/2}) by the angle position * rope_theta^(-2c/rotary_dim).  The i-th new
+ * token of sequence b has position prefix_len[b] + i and goes to that logical slot of the cache;
+ * values are copied as they are.  Angles are formed from whole turns in 64-bit fixed point, exact
+ * to 2^-27 of a turn for every position below 2^31.
+ *
+ *   q            [T, Hq, hd], k, v [T, Hkv, hd] io_dtype  in   token t's heads start at
+ *                q + t * q_stride (elements); k_stride, v_stride and the output strides alike
+ *   q_weight, k_weight [hd] io_dtype, or NULL (no weight, and weight_offset is not used)
+ *   cu_seqlens   [B + 1] int32  in   sequence b's new tokens are cu_seqlens[b] .. cu_seqlens[b+1]-1;
+ *                NULL: one token for each sequence, T = B
+ *   prefix_len   [B] int32      in   tokens before the new ones; may be NULL (zero) without a cache
+ *   live         [B] int32, optional (NULL: all)  in   a sequence with live[b] = 0 is skipped, its
+ *                rows of every output left as they are
+ *   q_out        [T, Hq, hd]  io_dtype  out  may be q itself
+ *   k_out        [T, Hkv, hd] io_dtype  out  optional (NULL: not written); may be k itself
+ *   k_cache, v_cache [num_blocks, Hkv, block_size, hd] bf16  out  optional, both or neither (then v,
+ *                block_table, num_blocks, max_blocks and block_size are not used); at least one of
+ *                k_out and the caches is given.  The blocks that new tokens go to belong to one
+ *                sequence each
+ *   block_table  [B, max_blocks] int32   in
+ *   err          [B] int32   out  0, TV_ERR_BAD_SEQLEN in every entry (cu_seqlens decreases or leaves
+ *                [0, T]; nothing else is written), TV_ERR_CAPACITY (prefix_len + tokens passes the
+ *                block table, or 2^31 - 1; prefix_len < 0) or TV_ERR_BAD_BLOCK (a block that a new
+ *                token goes to); a failed sequence's rows are left as they are
+ * Rows of no sequence are not written.  Arithmetic is fp32, rounded once on store.  Supported: hd in
+ * {64, 128, 256}; rotary_dim a multiple of 16 from 0 (no rotation) to hd; block_size = 16; io F32 or
+ * BF16, the caches with BF16 only.  rope_theta >= 1.  Strides: at least the dense row and whole
+ * multiples of 16 bytes.  With rotary_dim = 0 and no cache it makes the norms alone, as before
+ * tv_tree_attn, which rotates itself.
+ * ---------------------------------------------------------------------------------------- */
+TV_API int tv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const void* q_weight, const void* k_weight, const int32_t* cu_seqlens,
+                           const int32_t* prefix_len, const int32_t* live, int B, int T, int Hq, int Hkv, int hd,
+                           int rotary_dim, int io_dtype, int norm, float eps, float weight_offset, float rope_theta,
+                           void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* k_cache,
+                           void* v_cache, int num_blocks, const int32_t* block_table, int max_blocks, int block_size,
+                           int32_t* err, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_window_attn_prompt -- GQA attention of new tokens over the paged cache, within a window.
+ *
+ * Whole prompts, later parts of them, or drafted chains: the n new tokens of a sequence stand at
+ * positions prefix_len .. prefix_len + n - 1, and their keys and values already lie in the cache
+ * (tv_qk_norm_rope puts them there).  The query at position p sees key j <= p if
+ *     p - j < window (window = 0: every j),   or   j < sinks (a few first tokens that stay visible);
+ * query head h reads KV head h / (Hq / Hkv); o = sum_j softmax_j(sm_scale q . k_j) v_j.
+ *
+ *   q            [T, Hq, hd] bf16  in   rotated; token t's heads start at q + t * q_stride (elements)
+ *   k_cache, v_cache [num_blocks, Hkv, block_size, hd] bf16   in
+ *   block_table  [B, max_blocks] int32   in   entries of blocks that no query of the call sees are not
+ *                read (blocks behind the window may have been given back)
+ *   cu_seqlens   [B + 1] int32     in   sequence b's new tokens; it may have none
+ *   prefix_len   [B] int32         in   tokens before the new ones
+ *   max_len      an upper bound of the numbers of new tokens (T serves; closer is faster)
+ *   out          [T, Hq, hd] bf16  out  strided like q; rows of no sequence are not written
+ *   workspace    device scratch of at least tv_window_attn_workspace_size(...) bytes, 16-byte
+ *                aligned (may be NULL when that is 0); contents on entry are ignored.  Calls that
+ *                share a workspace must not overlap in time.
+ *   err          [B] int32         out  0, TV_ERR_BAD_SEQLEN in every entry (nothing else is written
+ *                then), TV_ERR_CAPACITY (prefix_len + tokens passes the block table; prefix_len < 0),
+ *                TV_ERR_BAD_BLOCK (a block that some query sees is outside the cache), or
+ *                TV_ERR_TIMEOUT (a bounded device wait gave up; that sequence's outputs are then
+ *                unspecified)
+ * Scores, softmax statistics and sums are fp32; the weights enter the product with the values as bf16.
+ * Results depend on the sizes and on no other sequence of the call.  A non-finite key or value that
+ * some query sees may reach other queries of its sequence and KV head; one that no query of the
+ * sequence sees reaches none.
+ * Supported: hd in {64, 128, 256}; block_size = 16; Hq a multiple of Hkv, Hq / Hkv <= 128; window and
+ * sinks from 0; sequences up to 2^30 tokens.  Strides: at least the dense row and whole multiples of
+ * 16 bytes.  max_blocks * 16 <= 2^30.
+ * ---------------------------------------------------------------------------------------- */
+TV_API size_t tv_window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, int hd, int max_blocks,
+                                            int block_size, int window, int sinks);
+TV_API int tv_window_attn_prompt(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                 int num_blocks, const int32_t* block_table, int max_blocks,
+                                 const int32_t* cu_seqlens, const int32_t* prefix_len, int B, int T, int max_len,
+                                 int Hq, int Hkv, int hd, int block_size, int window, int sinks, float sm_scale,
+                                 void* out, int64_t out_stride, void* workspace, size_t workspace_bytes, int32_t* err,
+                                 tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_window_attn_step -- the same attention for one new token of every sequence.
+ *
+ * The token of sequence b stands at position prefix_len[b]; its key and value lie in the cache.
+ *
+ *   q, out       [B, Hq, hd] bf16, strided as tv_window_attn_prompt
+ *   live         [B] int32, optional (NULL: all)   in   a sequence with live[b] = 0 is skipped: its
+ *                output row is left as it is, its err is 0 (rows of a padded batch)
+ *   workspace    of at least tv_window_attn_workspace_size(B, B, 1, ...) bytes
+ *   err          [B] int32   out  0, TV_ERR_CAPACITY, TV_ERR_BAD_BLOCK or TV_ERR_TIMEOUT
+ * Everything else as tv_window_attn_prompt.
+ * ---------------------------------------------------------------------------------------- */
+TV_API int tv_window_attn_step(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                               int num_blocks, const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                               const int32_t* live, int B, int Hq, int Hkv, int hd, int block_size, int window,
+                               int sinks, float sm_scale, void* out, int64_t out_stride, void* workspace,
+                               size_t workspace_bytes, int32_t* err, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * tv_accept_sample -- acceptance of B draft trees by probabilities, on the device.
+ *
+ * The sampled counterpart of tv_accept_walk: the accepted tokens and the one after them are
+ * distributed as if the target model had drawn them, given uniform random numbers.  From node 0 the
+ * walk tests the children of the last accepted node in ascending order.  With p = target_probs[node]
+ * and, as the tokens are refused one after another, R_0 = p and M_0 = 1:
+ *   draft_probs given (every child's token was drawn from q = draft_probs[node]):
+ *     accept child c with token x if uniforms[c] * q(x) * M_k < R_k(x), else
+ *     R_{k+1} = max(R_k - M_k q, 0),  M_{k+1} = sum R_{k+1};
+ *     where that sum is 0, R and M start again from p and 1;
+ *   draft_probs NULL (children are chosen, not drawn, and distinct):
+ *     accept if uniforms[c] * M_k < R_k(x), else R_{k+1} = R_k with R(x) = 0, M_{k+1} = M_k - R_k(x).
+ * Without a child accepted, or once Lmax nodes are, next_token is the smallest x with
+ *     R(0) + ... + R(x) > uniforms[0] * sum R        (R is p where nothing was refused, or sum R = 0).
+ * Probabilities are taken as they are, negative ones and NaN as 0.  A token outside [0, V) is never
+ * accepted.  All sums are carried to 2^-44 of their value or better.  A chain is a tree too, and N = 1
+ * draws one token from target_probs.
+ *
+ *   parents, draft_tokens [B, N] int32     in   as tv_accept_walk
+ *   target_probs   [B, N, V] probs_dtype   in   row i: the target's probabilities after node i
+ *   draft_probs    [B, N, V] probs_dtype   in   row i: what node i's children were drawn from; or NULL
+ *   uniforms       [B, N] fp32             in   in [0, 1); entry 0 draws the next token
+ *   accepted_path  [B, Lmax], accepted_len [B], next_token [B] int32   out   as tv_accept_walk
+ *   err            [B] int32               out  0, TV_ERR_BAD_TREE, or TV_ERR_BAD_PROBS when the row
+ *                                               that the next token is drawn from has no positive
+ *                                               entry (path -1, length 0, next_token -1 for both)
+ * Supported: N <= TV_MAX_NODES, V <= 2^24, probs F32 or BF16.
+ * ---------------------------------------------------------------------------------------- */
+TV_API int tv_accept_sample(const int32_t* parents, const int32_t* draft_tokens, const void* target_probs,
+                            const void* draft_probs, const float* uniforms, int B, int N, int V, int Lmax,
+                            int probs_dtype, int32_t* accepted_path, int32_t* accepted_len, int32_t* next_token,
+                            int32_t* err, tv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * tv_test_bounded_wait -- test support for the bounded device waits.

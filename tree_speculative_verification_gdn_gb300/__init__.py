@@ -31,6 +31,7 @@ TV_ERR_CAPACITY = -7
 TV_ERR_BAD_BLOCK = -8
 TV_ERR_SCRATCH = -9
 TV_ERR_BAD_SEQLEN = -10
+TV_ERR_BAD_PROBS = -11
 TV_F32 = 0
 TV_BF16 = 1
 TV_MODE_FORK = 0
@@ -46,7 +47,9 @@ EXPORTED = ("tv_status_string", "tv_last_cuda_error", "tv_version", "tv_tree_pre
             "tv_gdn_tree_verify_wy_lazy", "tv_gdn_fork_workspace_size", "tv_gdn_tree_verify_fork_ws",
             "tv_gdn_fork_materialize", "tv_gdn_fork_materialize_selective", "tv_gdn_commit_layers",
             "tv_kv_compact_remap", "tv_linear_attn_workspace_size", "tv_linear_attn_prompt",
-            "tv_linear_attn_step", "tv_gated_rmsnorm", "tv_residual_rmsnorm", "tv_test_bounded_wait")
+            "tv_linear_attn_step", "tv_gated_rmsnorm", "tv_residual_rmsnorm", "tv_qk_norm_rope",
+            "tv_window_attn_workspace_size", "tv_window_attn_prompt", "tv_window_attn_step", "tv_accept_sample",
+            "tv_test_bounded_wait")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -91,6 +94,14 @@ _SIGNATURES = {
                                  _P]),
     "tv_gated_rmsnorm": (_I, [_P, _L, _P, _L, _P, _I, _I, _I, _I, _F, _F, _I, _P, _L, _P]),
     "tv_residual_rmsnorm": (_I, [_P, _L, _P, _L, _P, _P, _L, _F, _P, _I, _I, _I, _I, _F, _F, _P, _L, _P, _L, _P]),
+    "tv_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _F, _P,
+                             _L, _P, _L, _P, _P, _I, _P, _I, _I, _P, _P]),
+    "tv_window_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "tv_window_attn_prompt": (_I, [_P, _L, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _L,
+                                   _P, _Z, _P, _P]),
+    "tv_window_attn_step": (_I, [_P, _L, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _L, _P, _Z, _P,
+                                 _P]),
+    "tv_accept_sample": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
     "tv_test_bounded_wait": (_I, [ctypes.c_uint, _I, _P, _P, _P]),
 }
 
@@ -478,6 +489,130 @@ def tv_residual_rmsnorm(y, residual, residual_out, eps: float, out=None, weight=
     _check(lib.tv_residual_rmsnorm(py, sy, pr, sr, _whole("post_weight", post_weight, (D,), io), pg, sg, scale,
                                    _whole("weight", weight, (D,), io), rows, D, _DTYPES[io], _DTYPES[res], eps,
                                    weight_offset, pro, sro, po, so, _stream(stream)), "tv_residual_rmsnorm")
+
+
+def _scratch(size: int, device, stream):
+    """``size`` bytes from torch's allocator for a call on ``stream``; None for none."""
+    if not size:
+        return None
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _here(*tensors) -> None:
+    """The calls launch on the current device's stream: tensors of another device are refused."""
+    device = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else -1
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != device:
+            raise ValueError(f"a tensor on {t.device} was passed while cuda:{device} is the current device")
+
+
+def tv_qk_norm_rope(q, k, q_out, prefix_len, err, *, k_out=None, v=None, k_cache=None, v_cache=None, block_table=None,
+                    cu_seqlens=None, live=None, q_weight=None, k_weight=None, norm: bool = True, eps: float = 1e-6,
+                    weight_offset: float = 0.0, rotary_dim: int | None = None, rope_theta: float = 10000.0,
+                    stream=None) -> None:
+    """rmsnorm of q [T, Hq, hd] and k [T, Hkv, hd] per head (``norm``), rotated over the first ``rotary_dim``
+    columns (default: all) by the position prefix_len [B] + index in the sequence; queries to ``q_out``, keys to
+    ``k_out`` and, with v as it is, to the paged ``k_cache``, ``v_cache`` [num_blocks, Hkv, 16, hd] through
+    ``block_table`` [B, max_blocks].  Sequences are packed by ``cu_seqlens`` [B + 1], or one token each without it.
+    Token strides are free.  ``prefix_len`` may be None (zero) without a cache; ``live`` [B] skips rows."""
+    T, Hq, hd = q.shape
+    Hkv = k.shape[1]
+    B = T if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    io, keys = q.dtype, (T, Hkv, hd)
+    if io not in _DTYPES:
+        _refuse("q", q, q.shape, "float32 or bfloat16")
+    _here(q, k, q_out, err, k_out, v, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, q_weight, k_weight)
+    pq, sq = _rows("q", q, q.shape, io, Hq * hd)
+    pk, sk = _rows("k", k, keys, io, Hkv * hd)
+    pqo, sqo = _rows("q_out", q_out, q.shape, io, Hq * hd)
+    pko, sko = _rows("k_out", k_out, keys, io, Hkv * hd)
+    pv, sv, pkc, pvc, ptab, blocks, most, bs = None, Hkv * hd, None, None, None, 0, 0, 0
+    if k_cache is not None or v_cache is not None:
+        if k_cache is None or v_cache is None or v is None or block_table is None:
+            raise ValueError("k_cache, v_cache, v and block_table go together")
+        blocks, bs, most = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+        cache = (blocks, Hkv, bs, hd)
+        pv, sv = _rows("v", v, keys, io, Hkv * hd)
+        pkc, pvc = _whole("k_cache", k_cache, cache, torch.bfloat16), _whole("v_cache", v_cache, cache, torch.bfloat16)
+        ptab = _whole("block_table", block_table, (B, most), torch.int32)
+    _check(lib.tv_qk_norm_rope(
+        pq, sq, pk, sk, pv, sv, _whole("q_weight", q_weight, (hd,), io), _whole("k_weight", k_weight, (hd,), io),
+        _whole("cu_seqlens", cu_seqlens, (B + 1,), torch.int32), _whole("prefix_len", prefix_len, (B,), torch.int32),
+        _whole("live", live, (B,), torch.int32), B, T, Hq, Hkv, hd, hd if rotary_dim is None else rotary_dim, _DTYPES[io],
+        int(norm), eps, weight_offset, rope_theta, pqo, sqo, pko, sko, pkc, pvc, blocks, ptab, most, bs,
+        _whole("err", err, (B,), torch.int32), _stream(stream)), "tv_qk_norm_rope")
+
+
+def tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, window: int = 0, sinks: int = 0,
+                                  block_size=TV_BLOCK_SIZE) -> int:
+    return int(lib.tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, block_size, window, sinks))
+
+
+def _window_attn(name, q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, out, err, window, sinks, max_len,
+                 workspace, sm_scale, stream):
+    T, Hq, hd = q.shape
+    blocks, Hkv, bs, _ = k_cache.shape
+    B, most = block_table.shape
+    bf, cache = torch.bfloat16, (blocks, Hkv, bs, hd)
+    _here(q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, out, err, workspace)
+    pq, sq = _rows("q", q, (T if cu_seqlens is not None else B, Hq, hd), bf, Hq * hd)
+    po, so = _rows("out", out, (T, Hq, hd), bf, Hq * hd)
+    if workspace is None:
+        size = lib.tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, most, bs, window, sinks)
+        workspace = _scratch(size, q.device, stream)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    head = (pq, sq, _whole("k_cache", k_cache, cache, bf), _whole("v_cache", v_cache, cache, bf), blocks,
+            _whole("block_table", block_table, (B, most), torch.int32), most)
+    prefix = _whole("prefix_len", prefix_len, (B,), torch.int32)
+    tail = (Hq, Hkv, hd, bs, window, sinks, hd ** -0.5 if sm_scale is None else sm_scale, po, so, _ptr(workspace), size,
+            _whole("err", err, (B,), torch.int32), _stream(stream))
+    if cu_seqlens is not None:
+        _check(lib.tv_window_attn_prompt(*head, _whole("cu_seqlens", cu_seqlens, (B + 1,), torch.int32), prefix, B, T,
+                                         max_len, *tail), name)
+    else:
+        _check(lib.tv_window_attn_step(*head, prefix, _whole("live", live, (B,), torch.int32), B, *tail), name)
+
+
+def tv_window_attn_prompt(q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, out, err, window: int = 0,
+                          sinks: int = 0, max_len: int | None = None, workspace=None, sm_scale: float | None = None,
+                          stream=None) -> None:
+    """Attention of the new tokens q [T, Hq, hd] bf16, packed by cu_seqlens [B + 1] and standing behind prefix_len [B]
+    tokens, over the paged cache that already holds their keys: key j for the query at position p if j <= p and
+    (p - j < window, or j < sinks); window 0: every j <= p.  out [T, Hq, hd]; token strides free.  Without a
+    ``workspace`` one is taken from torch's allocator when the call needs it."""
+    _window_attn("tv_window_attn_prompt", q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, None, out, err, window,
+                 sinks, q.shape[0] if max_len is None else int(max_len), workspace, sm_scale, stream)
+
+
+def tv_window_attn_step(q, k_cache, v_cache, block_table, prefix_len, out, err, window: int = 0, sinks: int = 0,
+                        live=None, workspace=None, sm_scale: float | None = None, stream=None) -> None:
+    """The same for one new token of every sequence, q and out [B, Hq, hd], at position prefix_len [B]; sequences with
+    live[b] = 0 are left alone."""
+    _window_attn("tv_window_attn_step", q, k_cache, v_cache, block_table, None, prefix_len, live, out, err, window, sinks, 1,
+                 workspace, sm_scale, stream)
+
+
+def tv_accept_sample(parents, draft_tokens, target_probs, draft_probs, uniforms, accepted_path, accepted_len, next_token,
+                     err, stream=None) -> None:
+    """Acceptance by probabilities: parents, draft_tokens [B, N] int32, target_probs and draft_probs [B, N, V] (fp32 or
+    bf16; draft_probs None: the drafted tokens were chosen, not drawn), uniforms [B, N] fp32 in [0, 1) -> accepted_path
+    [B, Lmax], accepted_len [B], next_token [B], err [B] (all int32)."""
+    B, N, V = target_probs.shape
+    Lmax, io, whole = accepted_path.shape[1], target_probs.dtype, torch.int32
+    if io not in _DTYPES:
+        _refuse("target_probs", target_probs, target_probs.shape, "float32 or bfloat16")
+    _here(parents, draft_tokens, target_probs, draft_probs, uniforms, accepted_path, accepted_len, next_token, err)
+    _check(lib.tv_accept_sample(
+        _whole("parents", parents, (B, N), whole), _whole("draft_tokens", draft_tokens, (B, N), whole),
+        _whole("target_probs", target_probs, (B, N, V), io), _whole("draft_probs", draft_probs, (B, N, V), io),
+        _whole("uniforms", uniforms, (B, N), torch.float32), B, N, V, Lmax, _DTYPES[io],
+        _whole("accepted_path", accepted_path, (B, Lmax), whole), _whole("accepted_len", accepted_len, (B,), whole),
+        _whole("next_token", next_token, (B,), whole), _whole("err", err, (B,), whole), _stream(stream)),
+        "tv_accept_sample")
 
 
 def tv_test_bounded_wait(max_polls: int, arrive: bool, status, elapsed_ns, stream=None) -> None:

@@ -77,6 +77,7 @@ const char* tv_status_string(int status) {
     case TV_ERR_CAPACITY: return "block table too short for prefix_len + N slots";
     case TV_ERR_BAD_BLOCK: return "block-table entry outside the cache";
     case TV_ERR_BAD_SEQLEN: return "cu_seqlens decreases, leaves [0, T] or holds a prompt longer than max_len";
+    case TV_ERR_BAD_PROBS: return "no token has a positive probability";
     case TV_ERR_SCRATCH: return "request needs more than the static scratch of TV_STATIC_SCRATCH_BYTES";
     default: return "unknown status";
   }
@@ -488,6 +489,130 @@ int tv_residual_rmsnorm(const void* y, int64_t y_stride, const void* residual, i
                          gate_stride, residual_out_stride, out_stride, rows, D, io_dtype, residual_dtype, scale, eps,
                          weight_offset};
   return cuda_status(tv::launch_residual_rmsnorm(a, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and the row strides shared by the calls over a paged cache of 16-token blocks; rows in whole 16 bytes.
+bool rows_ok(int64_t stride, int64_t row, int dtype) {
+  return stride >= row && stride % (dtype == TV_BF16 ? 8 : 4) == 0;
+}
+bool head_ok(int hd) { return hd == 64 || hd == 128 || hd == 256; }
+
+int window_attn_common(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int num_blocks,
+                       const int32_t* block_table, int max_blocks, const int32_t* prefix_len, int B, int Hq, int Hkv,
+                       int hd, int block_size, int window, int sinks, float sm_scale, const void* out,
+                       int64_t out_stride, const int32_t* err) {
+  if (!a16(q) || !a16(k_cache) || !a16(v_cache) || !a4(block_table) || !a4(prefix_len) || !a16(out) || !a4(err))
+    return TV_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || num_blocks < 1 || max_blocks < 1 || window < 0 || sinks < 0 ||
+      !isfinite(sm_scale))
+    return TV_ERR_INVALID_ARG;
+  if (!head_ok(hd) || block_size != TV_BLOCK_SIZE || Hq / Hkv > 128 || max_blocks > (1 << 26)) return TV_ERR_UNSUPPORTED;
+  if (Hq > (1 << 16) || (long long)B * Hkv > (1 << 24)) return TV_ERR_UNSUPPORTED;
+  if (!rows_ok(q_stride, (int64_t)Hq * hd, TV_BF16) || !rows_ok(out_stride, (int64_t)Hq * hd, TV_BF16))
+    return TV_ERR_INVALID_ARG;
+  return TV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                    const void* q_weight, const void* k_weight, const int32_t* cu_seqlens, const int32_t* prefix_len,
+                    const int32_t* live, int B, int T, int Hq, int Hkv, int hd, int rotary_dim, int io_dtype, int norm,
+                    float eps, float weight_offset, float rope_theta, void* q_out, int64_t q_out_stride, void* k_out,
+                    int64_t k_out_stride, void* k_cache, void* v_cache, int num_blocks, const int32_t* block_table,
+                    int max_blocks, int block_size, int32_t* err, tv_stream_t stream) {
+  const bool cache = k_cache != nullptr || v_cache != nullptr;
+  if (io_dtype != TV_F32 && io_dtype != TV_BF16) return TV_ERR_INVALID_ARG;
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || norm < 0 || norm > 1 || !(eps >= 0.f) || !isfinite(eps) ||
+      !isfinite(weight_offset) || rotary_dim < 0 || rotary_dim > hd ||
+      (rotary_dim > 0 && (!(rope_theta >= 1.f) || !isfinite(rope_theta))) || (cu_seqlens == nullptr && T != B))
+    return TV_ERR_INVALID_ARG;
+  if (!head_ok(hd) || rotary_dim % 16 || Hq > (1 << 16) || Hkv > (1 << 16)) return TV_ERR_UNSUPPORTED;
+  if (cache && (block_size != TV_BLOCK_SIZE || io_dtype != TV_BF16 || max_blocks > (1 << 26))) return TV_ERR_UNSUPPORTED;
+  if ((cu_seqlens != nullptr && !a4(cu_seqlens)) || (prefix_len != nullptr && !a4(prefix_len)) ||
+      (live != nullptr && !a4(live)) || (q_weight != nullptr && !a16(q_weight)) ||
+      (k_weight != nullptr && !a16(k_weight)) || !a4(err))
+    return TV_ERR_INVALID_ARG;
+  if (cache && (!a16(k_cache) || !a16(v_cache) || !a4(block_table) || prefix_len == nullptr || num_blocks < 1 ||
+                max_blocks < 1))
+    return TV_ERR_INVALID_ARG;
+  if (!cache && k_out == nullptr) return TV_ERR_INVALID_ARG;
+  const int64_t qrow = (int64_t)Hq * hd, krow = (int64_t)Hkv * hd;
+  // With no token at all (T = 0) the token tensors may be null.
+  if (T > 0 && (!a16(q) || !a16(k) || !a16(q_out) || (cache && !a16(v)) || (k_out != nullptr && !a16(k_out))))
+    return TV_ERR_INVALID_ARG;
+  if (!rows_ok(q_stride, qrow, io_dtype) || !rows_ok(k_stride, krow, io_dtype) ||
+      !rows_ok(q_out_stride, qrow, io_dtype) || (cache && !rows_ok(v_stride, krow, io_dtype)) ||
+      (k_out != nullptr && !rows_ok(k_out_stride, krow, io_dtype)))
+    return TV_ERR_INVALID_ARG;
+  tv::QkRopeArgs a{q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, cu_seqlens, prefix_len, live,
+                   B, T, Hq, Hkv, hd, rotary_dim, io_dtype, norm, eps, weight_offset, rope_theta,
+                   q_out, k_out, q_out_stride, k_out_stride, k_cache, v_cache, num_blocks, block_table, max_blocks, err};
+  return cuda_status(tv::launch_qk_norm_rope(a, stream));
+}
+
+size_t tv_window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, int hd, int max_blocks,
+                                     int block_size, int window, int sinks) {
+  if (B < 1 || T < 0 || max_len < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || !head_ok(hd) || max_blocks < 1 ||
+      max_blocks > (1 << 26) || block_size != TV_BLOCK_SIZE || window < 0 || sinks < 0 || Hq / Hkv > 128)
+    return 0;
+  return tv::window_attn_workspace_size(B, T, max_len < T ? max_len : T, Hq, Hkv, hd, max_blocks, window, sinks);
+}
+
+int tv_window_attn_prompt(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int num_blocks,
+                          const int32_t* block_table, int max_blocks, const int32_t* cu_seqlens,
+                          const int32_t* prefix_len, int B, int T, int max_len, int Hq, int Hkv, int hd,
+                          int block_size, int window, int sinks, float sm_scale, void* out, int64_t out_stride,
+                          void* workspace, size_t workspace_bytes, int32_t* err, tv_stream_t stream) {
+  if (T < 0 || max_len < 0 || !a4(cu_seqlens)) return TV_ERR_INVALID_ARG;
+  // With no token at all (T = 0) the token tensors may be null.
+  const int st = window_attn_common(T > 0 ? q : k_cache, q_stride, k_cache, v_cache, num_blocks, block_table,
+                                    max_blocks, prefix_len, B, Hq, Hkv, hd, block_size, window, sinks, sm_scale,
+                                    T > 0 ? out : k_cache, out_stride, err);
+  if (st != TV_OK) return st;
+  if (max_len > T) max_len = T;
+  const size_t need = tv::window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, window, sinks);
+  if (need > 0 && (!a16(workspace) || workspace_bytes < need)) return TV_ERR_INVALID_ARG;
+  tv::WinAttnArgs a{q, q_stride, k_cache, v_cache, num_blocks, block_table, max_blocks, cu_seqlens, prefix_len, nullptr,
+                    B, T, max_len, Hq, Hkv, hd, window, sinks, sm_scale, out, out_stride, err};
+  return cuda_status(tv::launch_window_attn(a, workspace, stream));
+}
+
+int tv_window_attn_step(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int num_blocks,
+                        const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* live,
+                        int B, int Hq, int Hkv, int hd, int block_size, int window, int sinks, float sm_scale,
+                        void* out, int64_t out_stride, void* workspace, size_t workspace_bytes, int32_t* err,
+                        tv_stream_t stream) {
+  if (live != nullptr && !a4(live)) return TV_ERR_INVALID_ARG;
+  const int st = window_attn_common(q, q_stride, k_cache, v_cache, num_blocks, block_table, max_blocks, prefix_len, B,
+                                    Hq, Hkv, hd, block_size, window, sinks, sm_scale, out, out_stride, err);
+  if (st != TV_OK) return st;
+  const size_t need = tv::window_attn_workspace_size(B, B, 1, Hq, Hkv, hd, max_blocks, window, sinks);
+  if (need > 0 && (!a16(workspace) || workspace_bytes < need)) return TV_ERR_INVALID_ARG;
+  tv::WinAttnArgs a{q, q_stride, k_cache, v_cache, num_blocks, block_table, max_blocks, nullptr, prefix_len, live,
+                    B, B, 1, Hq, Hkv, hd, window, sinks, sm_scale, out, out_stride, err};
+  return cuda_status(tv::launch_window_attn(a, workspace, stream));
+}
+
+int tv_accept_sample(const int32_t* parents, const int32_t* draft_tokens, const void* target_probs,
+                     const void* draft_probs, const float* uniforms, int B, int N, int V, int Lmax, int probs_dtype,
+                     int32_t* accepted_path, int32_t* accepted_len, int32_t* next_token, int32_t* err,
+                     tv_stream_t stream) {
+  if (probs_dtype != TV_F32 && probs_dtype != TV_BF16) return TV_ERR_INVALID_ARG;
+  if (!a4(parents) || !a4(draft_tokens) || !a16(target_probs) || (draft_probs != nullptr && !a16(draft_probs)) ||
+      !a4(uniforms) || !a4(accepted_path) || !a4(accepted_len) || !a4(next_token) || !a4(err))
+    return TV_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || V < 1 || Lmax < 1) return TV_ERR_INVALID_ARG;
+  if (N > TV_MAX_NODES || V > (1 << 24) || B > (1 << 24)) return TV_ERR_UNSUPPORTED;
+  tv::SampleArgs a{parents, draft_tokens, target_probs, draft_probs, uniforms, B, N, V, Lmax, probs_dtype,
+                   accepted_path, accepted_len, next_token, err};
+  return cuda_status(tv::launch_accept_sample(a, stream));
 }
 
 }  // extern "C"

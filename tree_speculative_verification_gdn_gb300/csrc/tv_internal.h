@@ -239,4 +239,78 @@ struct ResidualNormArgs {
 };
 cudaError_t launch_residual_rmsnorm(const ResidualNormArgs& a, cudaStream_t s);
 
+// Per-head norms with the rotation, into dense outputs and the paged cache.  Strides are in elements, per token.
+struct QkRopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* cu;          // [B + 1], or nullptr: one token a sequence
+  const int32_t* prefix_len;  // nullptr: zero
+  const int32_t* live;        // nullptr: all
+  int B, T, Hq, Hkv, hd, rotary, io, norm;
+  float eps, weight_offset, theta;
+  void* q_out;
+  void* k_out;
+  long long q_out_stride, k_out_stride;
+  void* k_cache;  // nullptr: no cache
+  void* v_cache;
+  int num_blocks;
+  const int32_t* block_table;
+  int max_blocks;
+  int32_t* err;
+};
+cudaError_t launch_qk_norm_rope(const QkRopeArgs& a, cudaStream_t s);
+
+// Windowed attention over the paged cache.  cu == nullptr: one token a sequence (T = B).
+struct WinAttnArgs {
+  const void* q;
+  long long q_stride;
+  const void* k_cache;
+  const void* v_cache;
+  int num_blocks;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* cu;
+  const int32_t* prefix_len;
+  const int32_t* live;
+  int B, T, max_len, Hq, Hkv, hd, window, sinks;
+  float sm_scale;
+  void* out;
+  long long out_stride;
+  int32_t* err;
+};
+size_t window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, int hd, int max_blocks, int window,
+                                  int sinks);
+cudaError_t launch_window_attn(const WinAttnArgs& a, void* workspace, cudaStream_t s);
+
+// Sequences of new tokens over a paged cache, checked before anything is written: packed lengths, room in the
+// table, and the blocks between the first and the last new token (window < 0), or those that some new token
+// sees.  table == nullptr: no cache.  err[b] is final after it.
+struct PagedCheckArgs {
+  const int32_t* cu;
+  const int32_t* prefix_len;
+  const int32_t* live;
+  const int32_t* table;
+  int B, T, max_len, max_blocks, num_blocks, window, sinks;
+  int32_t* err;
+};
+cudaError_t launch_paged_check(const PagedCheckArgs& a, cudaStream_t s);
+
+struct SampleArgs {
+  const int32_t* parents;
+  const int32_t* tokens;
+  const void* target;
+  const void* draft;  // nullptr: not known
+  const float* uniforms;
+  int B, N, V, Lmax, probs;
+  int32_t* path;
+  int32_t* len;
+  int32_t* next_token;
+  int32_t* err;
+};
+cudaError_t launch_accept_sample(const SampleArgs& a, cudaStream_t s);
+
 }  // namespace tv
