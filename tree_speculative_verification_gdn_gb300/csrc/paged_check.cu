@@ -9,6 +9,7 @@ namespace {
 
 __global__ void __launch_bounds__(256) paged_check_kernel(PagedCheckArgs a) {
   const int b = blockIdx.x;
+  for (int h = threadIdx.x; h < a.counters; h += blockDim.x) a.zeros[(long long)b * a.counters + h] = 0;
   bool bad = false;
   if (a.cu != nullptr)
     for (int i = threadIdx.x; i < a.B; i += blockDim.x) {

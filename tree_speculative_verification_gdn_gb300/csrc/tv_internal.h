@@ -296,6 +296,8 @@ struct PagedCheckArgs {
   const int32_t* table;
   int B, T, max_len, max_blocks, num_blocks, window, sinks;
   int32_t* err;
+  int32_t* zeros = nullptr;  // [B, counters], set to zero
+  int counters = 0;
 };
 cudaError_t launch_paged_check(const PagedCheckArgs& a, cudaStream_t s);
 

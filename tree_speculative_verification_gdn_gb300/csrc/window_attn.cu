@@ -2,8 +2,7 @@
 //
 // o = sum_j softmax_j(scale q . k_j) v_j over the keys j <= p of a query at position p with p - j < window, or
 // j < sinks.  A warp takes one query head of one token and walks its keys with a running maximum and sum.
-#include "tv_common.cuh"
-#include "tv_internal.h"
+#include "window_attn.cuh"
 
 namespace tv {
 namespace {
@@ -56,14 +55,18 @@ __global__ void __launch_bounds__(256) window_attn_kernel(WinAttnArgs a) {
 
 size_t window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, int hd, int max_blocks, int window,
                                   int sinks) {
-  return 0;
+  const long long rows = (long long)max_len * (Hq / Hkv);
+  if (T == 0) return 0;
+  return rows <= rows_limit(hd) ? window_rows_workspace(B, Hkv, (int)rows, hd) : 0;
 }
 
 cudaError_t launch_window_attn(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
+  const bool few = a.T > 0 && (long long)a.max_len * (a.Hq / a.Hkv) <= rows_limit(a.hd);
   const PagedCheckArgs c{a.cu, a.prefix_len, a.live, a.block_table, a.B, a.T, a.max_len, a.max_blocks, a.num_blocks,
-                         a.window, a.sinks, a.err};
+                         a.window, a.sinks, a.err, static_cast<int32_t*>(workspace), few ? a.Hkv : 0};
   const cudaError_t e = launch_paged_check(c, s);
   if (e != cudaSuccess || a.T == 0) return e;
+  if (few) return launch_window_rows(a, workspace, s);
   const unsigned grid = (unsigned)(((long long)a.T * a.Hq + 7) / 8);
   if (a.hd == 64) window_attn_kernel<64><<<grid, 256, 0, s>>>(a);
   else if (a.hd == 128) window_attn_kernel<128><<<grid, 256, 0, s>>>(a);

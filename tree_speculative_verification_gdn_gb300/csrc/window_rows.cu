@@ -1,0 +1,402 @@
+// Windowed attention of few query rows -- single tokens, short drafted chains -- over long contexts.
+//
+// The rows of a sequence and KV head, (new token, query head of the group), are at most 4096 / hd, and every visible key and
+// value is read once for all of them: bound by HBM.  The visible pages of all sequences and KV heads, one behind the
+// other, are dealt out to the grid in equal runs, so that ragged lengths and few sequences spread alike.  A CTA's four warps
+// take the pages of its run in turn, each with its own ring of copies in flight, its own running maximum, sum and
+// output; no two warps meet inside a run.  Scores and outputs go through m16n8k16 products: at 16 rows a page, the
+// matrix units are idle nine tenths of the time, and their registers need no detour through tensor memory.  Rows of
+// a page that no token sees are not read; the copy fills them with zeros.
+//
+// A (sequence, KV head) that lies in several CTAs' runs leaves maximum, sum and unnormalised output per CTA in the
+// workspace; the last of them to finish joins them in the order of the runs, so the result does not depend on which that is.
+#include "tv_async.cuh"
+#include "window_attn.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kLeast = 8;      // pages a run, at least: below, joining costs more than the pages
+constexpr float kRaise = 8.f;  // the running maximum is raised only by more than this (log2): sums grow by 2^8 at most
+
+constexpr int per_sm(int hd, int tiles) { return hd == 256 ? 1 : hd == 128 || tiles == 4 ? 2 : 3; }
+
+template <int HD>
+struct Shape {
+  static constexpr int kStages = HD == 64 ? 4 : 3;
+  static constexpr int kPage = 16 * HD * 2;  // bytes of one page of keys (or values) of a head
+  static constexpr int kRing = kWarps * kStages * 2 * kPage;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16-byte chunk c of a row, its low three bits turned by the row: eight rows of one chunk meet all banks.
+template <int HD>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return row * (HD * 2) + ((c ^ (row & 7)) << 4);
+}
+
+template <int HD, int MT>
+__global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
+    window_rows_kernel(WinAttnArgs a, float* __restrict__ slots, int* __restrict__ arrived) {
+  using S = Shape<HD>;
+  constexpr int kSlot = MT * 16 * (HD + 2);  // floats: outputs, then (maximum, sum) per row
+  constexpr int CH = HD / 8;                 // 16-byte chunks of a row
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* sQ = smem;                          // MT * 16 rows
+  unsigned char* ring = smem + MT * 16 * HD * 2;
+  __shared__ long long s_ll[kWarps];
+  __shared__ long long s_base;
+  __shared__ int s_b, s_last;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int G = a.Hq / a.Hkv;
+
+  // The pages of all sequences and heads, and this CTA's run of them.  upto: sum over the threads before this one and it.
+  auto block_scan = [&](long long x, long long& upto) -> long long {
+    upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_ll[warp] = upto;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += s_ll[w];
+      all += s_ll[w];
+    }
+    return all;
+  };
+  long long mine = 0, upto;
+  for (int b = tid; b < a.B; b += kThreads) mine += seen_by(a, b).pages;
+  const long long total = block_scan(mine, upto) * a.Hkv;
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kLeast) per = kLeast;
+  const long long x0 = blockIdx.x * per, x1 = min(total, x0 + per);
+  if (x0 >= x1) return;
+  // the sequence that the run starts in, and the pages before it
+  long long base = 0;
+  for (int b0 = 0;; b0 += kThreads) {
+    const long long own = (b0 + tid < a.B ? seen_by(a, b0 + tid).pages : 0) * (long long)a.Hkv;
+    const long long here = block_scan(own, upto);
+    if (base + here > x0) {
+      if (base + upto - own <= x0 && base + upto > x0) s_b = b0 + tid, s_base = base + upto - own;
+      break;
+    }
+    base += here;
+  }
+  __syncthreads();
+  int b = s_b;
+  base = s_base;
+  Seen q = seen_by(a, b);
+
+  const float scale = a.sm_scale * 1.4426950408889634f;
+  const uint32_t my_ring = smem_addr(ring) + warp * (S::kStages * 2 * S::kPage);
+  for (long long x = x0; x < x1;) {
+    while (x - base >= (long long)q.pages * a.Hkv) {
+      base += (long long)q.pages * a.Hkv;
+      q = seen_by(a, ++b);
+    }
+    const int kvh = (int)((x - base) / q.pages);
+    const long long u0 = base + (long long)kvh * q.pages, u1 = u0 + q.pages;
+    const int p0 = (int)(x - u0), p1 = (int)(min(x1, u1) - u0);
+    const int R = q.n * G;
+    const int start = a.cu != nullptr ? a.cu[b] : b;
+    const int32_t* table = a.block_table + (long long)b * a.max_blocks;
+
+    __syncthreads();  // the last unit's outputs have left shared memory
+    for (int i = tid; i < MT * 16 * CH; i += kThreads) {
+      const int r = i / CH, c = i % CH;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < R)
+        v = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (long long)(start + r / G) * a.q_stride +
+                                            (long long)(kvh * G + r % G) * HD + c * 8);
+      *reinterpret_cast<uint4*>(sQ + chunk_at<HD>(r, c)) = v;
+    }
+
+    const int last = q.P + q.n - 1;
+    const int steps = (p1 - p0 - warp + kWarps - 1) / kWarps;  // pages of this warp; may be 0 or less
+    int ids = 0;
+    auto ids_from = [&](int k) {  // block of this warp's page k + lane
+      const int page = p0 + warp + (k + lane) * kWarps;
+      ids = page < p1 ? table[q.position(page) / 16] : 0;
+    };
+    auto issue = [&](int k) {
+      if (k < steps) {
+        if (k % 32 == 0) ids_from(k);
+        const int blk = __shfl_sync(0xffffffffu, ids, k % 32);
+        const int at = q.position(p0 + warp + k * kWarps);
+        const long long row0 = ((long long)blk * a.Hkv + kvh) * 16;
+        const bf16* ks = static_cast<const bf16*>(a.k_cache) + row0 * HD;
+        const bf16* vs = static_cast<const bf16*>(a.v_cache) + row0 * HD;
+        const uint32_t dst = my_ring + (k % S::kStages) * 2 * S::kPage;
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+          const int j = at + r;
+          const bool real = j <= last && (j >= q.lo || j < q.s);
+          copy16(dst + chunk_at<HD>(r, c), ks + r * HD + c * 8, real);
+          copy16(dst + S::kPage + chunk_at<HD>(r, c), vs + r * HD + c * 8, real);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S::kStages - 1; ++k) issue(k);
+    __syncthreads();
+
+    // a thread's rows are lane / 4 and lane / 4 + 8 of each tile of 16
+    int pos[MT][2];
+    float m[MT][2], l[MT][2], o[MT][HD / 8][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        pos[t][h] = q.P + min((t * 16 + lane / 4 + 8 * h) / G, q.n - 1);
+        m[t][h] = -INFINITY, l[t][h] = 0.f;
+      }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    constexpr bool kHeld = MT == 1 && HD <= 128;  // queries stay in registers
+    uint32_t qr[kHeld ? HD / 16 : 1][4];
+    const uint32_t q_addr = smem_addr(sQ);
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) ldsm4(q_addr + chunk_at<HD>(lane % 16, 2 * c + lane / 16), qr[c]);
+    }
+
+    for (int k = 0; k < steps; ++k) {
+      issue(k + S::kStages - 1);
+      cp_async_wait<S::kStages - 1>();
+      __syncwarp();
+      const uint32_t kp = my_ring + (k % S::kStages) * 2 * S::kPage, vp = kp + S::kPage;
+      float s[MT][2][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[t][i][0] = s[t][i][1] = s[t][i][2] = s[t][i][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) {
+        uint32_t kf[4];
+        ldsm4(kp + chunk_at<HD>(lane % 8 + (lane / 16) * 8, 2 * c + (lane / 8) % 2), kf);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t qf[4];
+          if constexpr (kHeld) {
+            qf[0] = qr[c][0], qf[1] = qr[c][1], qf[2] = qr[c][2], qf[3] = qr[c][3];
+          } else {
+            ldsm4(q_addr + t * 16 * HD * 2 + chunk_at<HD>(lane % 16, 2 * c + lane / 16), qf);
+          }
+          mma16816(s[t][0], qf, kf[0], kf[1]);
+          mma16816(s[t][1], qf, kf[2], kf[3]);
+        }
+      }
+      const int at = q.position(p0 + warp + k * kWarps);
+      // every row sees the whole page: up to the first token, and within the last one's window or among the first tokens
+      const bool open = at + 15 <= q.P && (a.window == 0 || at > last - a.window || at + 15 < a.sinks);
+      uint32_t pf[MT][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = s[t][i][e] * scale;
+            if (!open) {
+              const int j = at + i * 8 + (lane % 4) * 2 + (e & 1), p = pos[t][e / 2];
+              if (j > p || (a.window > 0 && p - j >= a.window && j >= a.sinks)) v = -INFINITY;
+            }
+            s[t][i][e] = v;
+          }
+        float mx[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]), fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[t][0] + kRaise || mx[1] > m[t][1] + kRaise)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float to = fmaxf(m[t][h], mx[h]);
+            const float f = m[t][h] == -INFINITY ? 0.f : ex2(m[t][h] - to);
+            m[t][h] = to;
+            l[t][h] *= f;
+#pragma unroll
+            for (int i = 0; i < HD / 8; ++i) o[t][i][2 * h] *= f, o[t][i][2 * h + 1] *= f;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float neg = m[t][h] == -INFINITY ? 0.f : -m[t][h];  // nothing seen yet: 2^-inf = 0
+          pf[t][h] = pack_bf16x2(ex2(s[t][0][2 * h] + neg), ex2(s[t][0][2 * h + 1] + neg));
+          pf[t][2 + h] = pack_bf16x2(ex2(s[t][1][2 * h] + neg), ex2(s[t][1][2 * h + 1] + neg));
+          // the sum of what the product with the values will use
+          l[t][h] += (bf16lo(pf[t][h]) + bf16hi(pf[t][h])) + (bf16lo(pf[t][2 + h]) + bf16hi(pf[t][2 + h]));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < CH; c += 2) {
+        uint32_t vf[4];
+        ldsm4_t(vp + chunk_at<HD>(lane % 16, c + lane / 16), vf);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          mma16816(o[t][c], pf[t], vf[0], vf[1]);
+          mma16816(o[t][c + 1], pf[t], vf[2], vf[3]);
+        }
+      }
+      __syncwarp();  // the stage is free
+    }
+    cp_async_wait<0>();
+
+    // The four warps' outputs meet in shared memory, over the rings.
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 1);
+        l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 2);
+      }
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(ring);                 // [kWarps][MT * 16][HD]
+    float* ml = reinterpret_cast<float*>(sQ);                    // [kWarps][MT * 16][2]
+    static_assert(kWarps * MT * 16 * HD * 4 <= S::kRing, "outputs fit over the rings");
+    static_assert(kWarps * 2 * 4 <= HD * 2, "maxima and sums fit over the queries");
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = t * 16 + lane / 4 + 8 * h;
+        float* row = acc + (warp * MT * 16 + r) * HD;
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i)
+          *reinterpret_cast<float2*>(row + i * 8 + (lane % 4) * 2) = make_float2(o[t][i][2 * h], o[t][i][2 * h + 1]);
+        if (lane % 4 == 0) ml[(warp * MT * 16 + r) * 2] = m[t][h], ml[(warp * MT * 16 + r) * 2 + 1] = l[t][h];
+      }
+    __syncthreads();
+    const bool alone = p0 == 0 && p1 == q.pages;
+    const long long c0 = u0 / per, c1 = (u1 - 1) / per;  // the CTAs that share the unit
+    // a CTA's first unit goes to its slot 0, a later one that runs past its end to slot 1
+    auto slot_of = [&](long long c) { return slots + (2 * c + (c * per < u0 ? 1 : 0)) * kSlot; };
+    auto put = [&](int r, int c, const float* v) {
+      uint2 w = pack4(v);
+      *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (long long)(start + r / G) * a.out_stride +
+                                (long long)(kvh * G + r % G) * HD + c) = w;
+    };
+    for (int i = tid; i < R * (HD / 4); i += kThreads) {
+      const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+      float top = -INFINITY, f[kWarps], sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * MT * 16 + r) * 2]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = ml[(w * MT * 16 + r) * 2];
+        f[w] = mw == -INFINITY ? 0.f : ex2(mw - top);
+        sum += f[w] * ml[(w * MT * 16 + r) * 2 + 1];
+        const float4 y = *reinterpret_cast<const float4*>(acc + (w * MT * 16 + r) * HD + c);
+        v[0] += f[w] * y.x, v[1] += f[w] * y.y, v[2] += f[w] * y.z, v[3] += f[w] * y.w;
+      }
+      if (alone) {
+        const float inv = 1.f / sum;
+        v[0] *= inv, v[1] *= inv, v[2] *= inv, v[3] *= inv;
+        put(r, c, v);
+      } else {
+        float* slot = slot_of(blockIdx.x);
+        *reinterpret_cast<float4*>(slot + r * HD + c) = make_float4(v[0], v[1], v[2], v[3]);
+        if (c == 0) slot[MT * 16 * HD + r * 2] = top, slot[MT * 16 * HD + r * 2 + 1] = sum;
+      }
+    }
+    if (!alone) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(arrived + (long long)b * a.Hkv + kvh, 1) == (int)(c1 - c0);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int i = tid; i < R * (HD / 4); i += kThreads) {
+          const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+          float top = -INFINITY, sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+          for (long long k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(slot_of(k) + MT * 16 * HD + r * 2));
+          for (long long k = c0; k <= c1; ++k) {
+            const float* slot = slot_of(k);
+            const float2 w = __ldcg(reinterpret_cast<const float2*>(slot + MT * 16 * HD + r * 2));
+            const float f = w.x == -INFINITY ? 0.f : ex2(w.x - top);
+            sum += f * w.y;
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(slot + r * HD + c));
+            v[0] += f * y.x, v[1] += f * y.y, v[2] += f * y.z, v[3] += f * y.w;
+          }
+          const float inv = 1.f / sum;
+          v[0] *= inv, v[1] *= inv, v[2] *= inv, v[3] *= inv;
+          put(r, c, v);
+        }
+      }
+    }
+    x = u0 + p1;
+  }
+}
+
+int tiles_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+size_t slots_bytes(int rows, int hd) {
+  const int tiles = tiles_of(rows);
+  return (size_t)kSms * per_sm(hd, tiles) * 2 * tiles * 16 * (hd + 2) * sizeof(float);
+}
+
+template <int HD, int MT>
+cudaError_t go(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
+  const size_t smem = MT * 16 * HD * 2 + Shape<HD>::kRing;
+  auto kern = window_rows_kernel<HD, MT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  int* arrived = reinterpret_cast<int*>(workspace);
+  float* slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((size_t)a.B * a.Hkv * 4 + 15) / 16 * 16);
+  kern<<<kSms * per_sm(HD, MT), kThreads, smem, s>>>(a, slots, arrived);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_rows_workspace(int B, int Hkv, int rows, int hd) {
+  return ((size_t)B * Hkv * 4 + 15) / 16 * 16 + slots_bytes(rows, hd);
+}
+
+cudaError_t launch_window_rows(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
+  const int tiles = tiles_of(a.max_len * (a.Hq / a.Hkv));
+  if (a.hd == 256) return go<256, 1>(a, workspace, s);
+  if (a.hd == 128) return tiles == 1 ? go<128, 1>(a, workspace, s) : go<128, 2>(a, workspace, s);
+  return tiles == 1 ? go<64, 1>(a, workspace, s) : tiles == 2 ? go<64, 2>(a, workspace, s) : go<64, 4>(a, workspace, s);
+}
+
+}  // namespace tv
