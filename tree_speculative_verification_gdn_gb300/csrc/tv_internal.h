@@ -286,21 +286,6 @@ size_t window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, in
                                   int sinks);
 cudaError_t launch_window_attn(const WinAttnArgs& a, void* workspace, cudaStream_t s);
 
-// Sequences of new tokens over a paged cache, checked before anything is written: packed lengths, room in the
-// table, and the blocks between the first and the last new token (window < 0), or those that some new token
-// sees.  table == nullptr: no cache.  err[b] is final after it.
-struct PagedCheckArgs {
-  const int32_t* cu;
-  const int32_t* prefix_len;
-  const int32_t* live;
-  const int32_t* table;
-  int B, T, max_len, max_blocks, num_blocks, window, sinks;
-  int32_t* err;
-  int32_t* zeros = nullptr;  // [B, counters], set to zero
-  int counters = 0;
-};
-cudaError_t launch_paged_check(const PagedCheckArgs& a, cudaStream_t s);
-
 struct SampleArgs {
   const int32_t* parents;
   const int32_t* tokens;

@@ -1,4 +1,4 @@
-// What the kernels of the windowed attention share: which pages of a sequence some new token sees.
+// What the kernels of the windowed attention share: which keys some new token sees, and how the work is dealt out.
 #pragma once
 
 #include "tv_common.cuh"
@@ -6,34 +6,99 @@
 
 namespace tv {
 
-// New tokens of a sequence and the pages that they see between them, numbered without the hidden ones: first
-// `front` pages of the first tokens, then those from logical page `from` on.
+// A run of new tokens of one sequence, and the pages that they see between them, numbered without the hidden ones:
+// first `front` pages of the first tokens, then those from logical page `from` on.
 struct Seen {
-  int n, P;     // new tokens (0: nothing to do), tokens before them
+  int n, P;     // tokens (0: nothing to do), tokens before them
   int lo, s;    // first position in the first token's window; first tokens that stay visible before it
   int front, from, pages;
   __device__ int position(int page) const { return (page < front ? page : page - front + from) * 16; }
 };
 
-__device__ __forceinline__ Seen seen_by(const WinAttnArgs& a, int b) {
+__device__ __forceinline__ Seen seen_by(const WinAttnArgs& a, int P, int n) {
   Seen x;
-  x.n = 0, x.pages = 0;
-  if (a.err[b] != 0 || (a.live != nullptr && a.live[b] == 0)) return x;
-  x.n = a.cu != nullptr ? a.cu[b + 1] - a.cu[b] : 1;
-  if (x.n == 0) return x;
-  x.P = a.prefix_len[b];
-  x.lo = a.window > 0 ? max(0, x.P - a.window + 1) : 0;
+  x.n = n, x.P = P;
+  x.lo = a.window > 0 ? max(0, P - a.window + 1) : 0;
   x.s = min(a.sinks, x.lo);
   x.front = (x.s + 15) / 16, x.from = x.lo / 16;
   if (x.from <= x.front) x.front = x.from = 0;  // nothing hidden between them
-  x.pages = x.front + (x.P + x.n - 1) / 16 - x.from + 1;
+  x.pages = x.front + (P + n - 1) / 16 - x.from + 1;
   return x;
 }
 
-// Head dims 64, 128, 256; a.cu or one token a sequence.  Few rows: sequences of at most rows_limit(hd) query rows
-// (new tokens x query heads of a KV head).
+constexpr int kSms = 152;
+
+// The costs of all sequences, Hkv times each, lie one behind the other; CTA i of the grid takes the i-th of equal runs of
+// at least `least`.
+struct Run {
+  long long per, x0, x1;  // a run's length; this CTA's
+  int b;                  // the sequence that it starts in, and the cost before that
+  long long base;
+};
+// The whole block; false in every thread where the run is empty.  THREADS = blockDim.x.
+template <int THREADS>
+__device__ __forceinline__ bool find_run(const long long* cost, int B, int Hkv, int least, Run& r) {
+  constexpr int W = THREADS / 32;
+  __shared__ long long part[W], s_base;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // sum over the block; upto: over the threads before this one and it
+  auto scan = [&](long long x, long long& upto) -> long long {
+    upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) upto += part[w];
+      all += part[w];
+    }
+    return all;
+  };
+  long long mine = 0, upto;
+  for (int b = tid; b < B; b += THREADS) mine += cost[b];
+  const long long total = scan(mine, upto) * Hkv;
+  r.per = (total + gridDim.x - 1) / gridDim.x;
+  if (r.per < least) r.per = least;
+  r.x0 = blockIdx.x * r.per, r.x1 = min(total, r.x0 + r.per);
+  if (r.x0 >= r.x1) return false;
+  r.base = 0;
+  for (int b0 = 0;; b0 += THREADS) {
+    const long long own = b0 + tid < B ? cost[b0 + tid] * Hkv : 0;
+    const long long here = scan(own, upto);
+    if (r.base + here > r.x0) {
+      if (r.base + upto - own <= r.x0 && r.base + upto > r.x0) s_b = b0 + tid, s_base = r.base + upto - own;
+      break;
+    }
+    r.base += here;
+  }
+  __syncthreads();
+  r.b = s_b, r.base = s_base;
+  return true;
+}
+
+// Head dims 64, 128, 256; a.cu or one token a sequence.  cost [B]: of a sequence for one KV head.
+// Few rows: sequences of at most rows_limit(hd) query rows (new tokens x query heads of a KV head); cost: pages.
 constexpr int rows_limit(int hd) { return 4096 / hd; }
-size_t window_rows_workspace(int B, int Hkv, int rows, int hd);
-cudaError_t launch_window_rows(const WinAttnArgs& a, void* workspace, cudaStream_t s);
+// arrived [B * Hkv], zero; slots: bytes as window_rows_slots.
+size_t window_rows_slots(int rows, int hd);
+cudaError_t launch_window_rows(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s);
+
+// Any number of rows: units of `tokens` tokens; cost: per unit its key tiles and kUnitCost more.
+struct TileShape {
+  int tokens;  // of a unit
+  int keys;    // of a tile
+};
+constexpr int kUnitCost = 2;
+TileShape window_tile_shape(int Hq, int Hkv, int hd);
+// arrived [kSms * 8], zero; slots: bytes as window_tiles_slots.
+size_t window_tiles_slots(int hd);
+cudaError_t launch_window_tiles(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s);
 
 }  // namespace tv

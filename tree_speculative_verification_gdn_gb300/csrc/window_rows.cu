@@ -16,7 +16,6 @@
 namespace tv {
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kLeast = 8;      // pages a run, at least: below, joining costs more than the pages
@@ -66,67 +65,33 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
 
 template <int HD, int MT>
 __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
-    window_rows_kernel(WinAttnArgs a, float* __restrict__ slots, int* __restrict__ arrived) {
+    window_rows_kernel(WinAttnArgs a, const long long* __restrict__ cost, float* __restrict__ slots,
+                       int* __restrict__ arrived) {
   using S = Shape<HD>;
   constexpr int kSlot = MT * 16 * (HD + 2);  // floats: outputs, then (maximum, sum) per row
   constexpr int CH = HD / 8;                 // 16-byte chunks of a row
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* sQ = smem;                          // MT * 16 rows
   unsigned char* ring = smem + MT * 16 * HD * 2;
-  __shared__ long long s_ll[kWarps];
-  __shared__ long long s_base;
-  __shared__ int s_b, s_last;
+  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int G = a.Hq / a.Hkv;
 
-  // The pages of all sequences and heads, and this CTA's run of them.  upto: sum over the threads before this one and it.
-  auto block_scan = [&](long long x, long long& upto) -> long long {
-    upto = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_ll[warp] = upto;
-    __syncthreads();
-    long long all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) upto += s_ll[w];
-      all += s_ll[w];
-    }
-    return all;
-  };
-  long long mine = 0, upto;
-  for (int b = tid; b < a.B; b += kThreads) mine += seen_by(a, b).pages;
-  const long long total = block_scan(mine, upto) * a.Hkv;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kLeast) per = kLeast;
-  const long long x0 = blockIdx.x * per, x1 = min(total, x0 + per);
-  if (x0 >= x1) return;
-  // the sequence that the run starts in, and the pages before it
-  long long base = 0;
-  for (int b0 = 0;; b0 += kThreads) {
-    const long long own = (b0 + tid < a.B ? seen_by(a, b0 + tid).pages : 0) * (long long)a.Hkv;
-    const long long here = block_scan(own, upto);
-    if (base + here > x0) {
-      if (base + upto - own <= x0 && base + upto > x0) s_b = b0 + tid, s_base = base + upto - own;
-      break;
-    }
-    base += here;
-  }
-  __syncthreads();
-  int b = s_b;
-  base = s_base;
-  Seen q = seen_by(a, b);
+  Run run;
+  if (!find_run<kThreads>(cost, a.B, a.Hkv, kLeast, run)) return;
+  int b = run.b;
+  long long base = run.base;
+  const long long per = run.per, x0 = run.x0, x1 = run.x1;
+  auto seen = [&]() { return seen_by(a, a.prefix_len[b], a.cu != nullptr ? a.cu[b + 1] - a.cu[b] : 1); };
+  Seen q = seen();
 
   const float scale = a.sm_scale * 1.4426950408889634f;
   const uint32_t my_ring = smem_addr(ring) + warp * (S::kStages * 2 * S::kPage);
   for (long long x = x0; x < x1;) {
-    while (x - base >= (long long)q.pages * a.Hkv) {
+    if (x - base >= (long long)q.pages * a.Hkv) {
       base += (long long)q.pages * a.Hkv;
-      q = seen_by(a, ++b);
+      while (cost[++b] == 0) {}
+      q = seen();
     }
     const int kvh = (int)((x - base) / q.pages);
     const long long u0 = base + (long long)kvh * q.pages, u1 = u0 + q.pages;
@@ -369,34 +334,28 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
 }
 
 int tiles_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-size_t slots_bytes(int rows, int hd) {
-  const int tiles = tiles_of(rows);
-  return (size_t)kSms * per_sm(hd, tiles) * 2 * tiles * 16 * (hd + 2) * sizeof(float);
-}
-
 template <int HD, int MT>
-cudaError_t go(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
   const size_t smem = MT * 16 * HD * 2 + Shape<HD>::kRing;
   auto kern = window_rows_kernel<HD, MT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  int* arrived = reinterpret_cast<int*>(workspace);
-  float* slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((size_t)a.B * a.Hkv * 4 + 15) / 16 * 16);
-  kern<<<kSms * per_sm(HD, MT), kThreads, smem, s>>>(a, slots, arrived);
+  kern<<<kSms * per_sm(HD, MT), kThreads, smem, s>>>(a, cost, slots, arrived);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t window_rows_workspace(int B, int Hkv, int rows, int hd) {
-  return ((size_t)B * Hkv * 4 + 15) / 16 * 16 + slots_bytes(rows, hd);
+size_t window_rows_slots(int rows, int hd) {
+  const int tiles = tiles_of(rows);
+  return (size_t)kSms * per_sm(hd, tiles) * 2 * tiles * 16 * (hd + 2) * sizeof(float);
 }
 
-cudaError_t launch_window_rows(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_window_rows(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
   const int tiles = tiles_of(a.max_len * (a.Hq / a.Hkv));
-  if (a.hd == 256) return go<256, 1>(a, workspace, s);
-  if (a.hd == 128) return tiles == 1 ? go<128, 1>(a, workspace, s) : go<128, 2>(a, workspace, s);
-  return tiles == 1 ? go<64, 1>(a, workspace, s) : tiles == 2 ? go<64, 2>(a, workspace, s) : go<64, 4>(a, workspace, s);
+  if (a.hd == 256) return go<256, 1>(a, cost, arrived, slots, s);
+  if (a.hd == 128) return tiles == 1 ? go<128, 1>(a, cost, arrived, slots, s) : go<128, 2>(a, cost, arrived, slots, s);
+  return tiles == 1 ? go<64, 1>(a, cost, arrived, slots, s) : tiles == 2 ? go<64, 2>(a, cost, arrived, slots, s) : go<64, 4>(a, cost, arrived, slots, s);
 }
 
 }  // namespace tv

@@ -1,0 +1,634 @@
+// Windowed attention of many query rows -- prompts -- on the 5th-generation tensor cores.
+//
+// A unit is a run of new tokens of one sequence for one KV head; its query rows, (token, query head of the group), fill
+// tiles of 128.  Head dims 64 and 128: two tiles, 128 keys at a time, the scores of one tile made while the softmax
+// of the other runs.  Head dim 256: one tile, 64 keys at a time, scores in two buffers.  Every unit walks its visible
+// pages alone, sixteen tokens each, hidden pages between the first tokens and the window left out.  Units of all
+// sequences and KV heads lie one behind the other, each as long as its key tiles and kUnitCost more, and a persistent grid
+// takes equal runs of that, so that ragged and causal work ends together; a unit cut by a run's end leaves maximum, sum and
+// unnormalised output per row in the workspace, and the last of its CTAs joins them in the order of the runs.
+//
+// Scores S = Q K^T go to tensor memory; a thread takes a row (TMEM lane), 2^(S scale - m) as bf16 goes back over the
+// scores' columns, and O += P V reads it from there.  The running maximum is raised only when a tile passes it by more
+// than 2^8, so O is hardly ever rescaled; the sum is of the fp32 weights before their rounding, whose errors average out.
+//   warps 0-3, 4-7   softmax of tile 0 and tile 1, output of each
+//   warp 8           TMA: queries, and K and V tiles in turn through one ring of stages
+//   warp 10          the run's units, up to four ahead
+//   warp 9           MMAs: item e of a unit is (key tile, row tile); S(e + 2) follows P V(e)
+// Values that no token of the unit sees may be anything, and 0 times that is not 0: their rows are cleared in
+// shared memory before P V.  Every wait is bounded; a role that gives up makes all leave.
+#include "tv_tma_host.h"
+#include "tv_tc.cuh"
+#include "window_attn.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kThreads = 352;
+constexpr int kUnits = 4;       // units known ahead
+constexpr int kLeast = 4;       // cost of a run, at least: a unit of two key tiles
+constexpr float kRaise = 8.0f;  // log2
+
+template <int HD>
+struct Shape {
+  static constexpr int NT = HD == 256 ? 1 : 2;          // row tiles
+  static constexpr int KT = HD == 256 ? 64 : 128;       // keys of a tile
+  static constexpr int NST = HD == 64 ? 8 : 5;          // K or V tiles in the ring
+  static constexpr uint32_t QCHUNK = kRows * 128;       // 64 columns of a row tile
+  static constexpr uint32_t QTILE = HD / 64 * QCHUNK;
+  static constexpr uint32_t KCHUNK = KT * 128;          // 64 columns of a key tile
+  static constexpr uint32_t STAGE = HD / 64 * KCHUNK;
+  static constexpr uint32_t RING = NT * QTILE;
+  static constexpr uint32_t BARS = RING + NST * STAGE;
+  static constexpr uint32_t TOTAL = BARS + 1024;
+  static constexpr uint32_t S0 = NT * HD;               // TMEM: outputs, then two buffers of scores
+  static constexpr int SLOT = NT * kRows * (HD + 2);    // floats of a cut unit
+  static_assert(S0 + 2 * KT <= 512, "tensor memory");
+  static_assert(TOTAL + 1024 <= 232448, "shared memory");
+};
+
+// A phase of the barrier, or false after some seconds at most, or once another role has given up.  A try sleeps
+// in the barrier unit for about a microsecond.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t it = 0; it < (1u << 20); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (done) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A unit, or the part of its key tiles that lies in the CTA's run.
+struct Unit {
+  int more;                // 0: the run has ended
+  int b, kvh, token;       // sequence, KV head, first token's row
+  int tiles, first, last;  // key tiles of the unit, the run's part of them
+  int c0, c1;              // the CTAs that share it
+  Seen seen;
+};
+
+struct Bars {
+  uint64_t q_full, q_free;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  Unit units[kUnits];
+};
+static_assert(sizeof(Bars) <= 1024, "barriers fit their region");
+
+// The units of a run, in order.  Made by a whole warp, walked by any thread of it.
+struct Walk {
+  const WinAttnArgs& a;
+  const long long* cost;
+  const Run& run;
+  TileShape shape;
+  int t, start, n, P;  // first token of the unit in the sequence; the sequence
+  long long u0;        // where the unit's cost starts
+  Unit u;
+
+  __device__ void sequence() {
+    start = a.cu != nullptr ? a.cu[u.b] : u.b;
+    n = a.cu != nullptr ? a.cu[u.b + 1] - start : 1;
+    P = a.prefix_len[u.b];
+    t = 0;
+  }
+  __device__ int tiles_of(int first_token) const {
+    return (seen_by(a, P + first_token, min(shape.tokens, n - first_token)).pages * 16 + shape.keys - 1) / shape.keys;
+  }
+  __device__ void unit() {
+    u.seen = seen_by(a, P + t, min(shape.tokens, n - t));
+    u.token = start + t;
+    u.tiles = (u.seen.pages * 16 + shape.keys - 1) / shape.keys;
+    const long long k0 = u0 + kUnitCost;
+    u.first = (int)min((long long)u.tiles, max(0LL, run.x0 - k0));
+    u.last = (int)max(0LL, min((long long)u.tiles, run.x1 - k0));
+  }
+  __device__ Walk(const WinAttnArgs& a_, const long long* cost_, const Run& run_, TileShape s)
+      : a(a_), cost(cost_), run(run_), shape(s) {
+    u.b = run.b;
+    sequence();
+    const long long c = cost[u.b];
+    u.kvh = (int)((run.x0 - run.base) / c);
+    u0 = run.base + u.kvh * c;
+    // a unit a lane, 32 at a time
+    for (;;) {
+      const int lane = threadIdx.x % 32;
+      const long long t_lane = t + (long long)lane * shape.tokens;
+      int upto = t_lane < n ? kUnitCost + tiles_of((int)t_lane) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, u0 + upto > run.x0);
+      const int skip = past != 0 ? __ffs(past) - 1 : 32;
+      if (skip > 0) u0 += __shfl_sync(0xffffffffu, upto, skip - 1);
+      t += skip * shape.tokens;
+      if (past != 0) break;
+    }
+    unit();
+    settle();
+  }
+  // On from a unit that has no key tile in the run.
+  __device__ void settle() {
+    while (u0 < run.x1 && u.first >= u.last) step();
+    u.more = u0 < run.x1;
+    const long long k0 = u0 + kUnitCost;
+    u.c0 = (int)(k0 / run.per), u.c1 = (int)((k0 + u.tiles - 1) / run.per);
+  }
+  __device__ void step() {
+    u0 += kUnitCost + u.tiles;
+    if (u0 >= run.x1) return;
+    t += shape.tokens;
+    if (t >= n) {
+      t = 0;
+      if (++u.kvh == a.Hkv) {
+        u.kvh = 0;
+        while (cost[++u.b] == 0) {}
+        sequence();
+      }
+    }
+    unit();
+  }
+  __device__ void next() {
+    step();
+    settle();
+  }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_tiles_kernel(const __grid_constant__ WinAttnArgs a, const long long* __restrict__ cost,
+                        int* __restrict__ arrived, float* __restrict__ slots, int npt,
+                        const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                        const __grid_constant__ CUtensorMap mV) {
+  using L = Shape<HD>;
+  constexpr int NT = L::NT, KT = L::KT, NST = L::NST;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  Bars& bar = *reinterpret_cast<Bars*>(sm + L::BARS);
+  volatile int* abort = &bar.abort;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int G = a.Hq / a.Hkv;
+
+  Run run;
+  if (!find_run<kThreads>(cost, a.B, a.Hkv, kLeast, run)) return;
+  if (tid == 0) {
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_free, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&bar.kv_full[s], 1);
+      mbar_init(&bar.kv_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.p_full[s], 4);
+      mbar_init(&bar.pv_done[s], 1);
+      mbar_init(&bar.o_free[s], 4);
+    }
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(&bar.unit_full[s], 1);
+      mbar_init(&bar.unit_empty[s], 10);
+    }
+    mbar_init(&bar.drain, 1);
+    bar.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) tmem_alloc(&bar.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  auto stage_of = [&](uint32_t seq) { return sm + L::RING + seq % NST * L::STAGE; };
+  uint32_t loads = 0, queries = 0;  // what the producer has started
+  // the k-th unit, once it is known; a warp hands it back when it needs no more of it
+  auto known = [&](uint32_t k) -> bool {
+    return __all_sync(0xffffffffu, wait_for(&bar.unit_full[k % kUnits], k / kUnits & 1, abort));
+  };
+  auto hand_back = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.unit_empty[k % kUnits]);
+  };
+
+  if (warp == 10) {
+    // ---------------------------------------------------------------- units
+    Walk w(a, cost, run, TileShape{NT * npt, KT});
+    if (lane == 0) {
+      for (uint32_t k = 0;; ++k) {
+        if (k >= kUnits && !wait_for(&bar.unit_empty[k % kUnits], (k / kUnits - 1) & 1, abort)) break;
+        bar.units[k % kUnits] = w.u;
+        mbar_arrive(&bar.unit_full[k % kUnits]);
+        if (!w.u.more) break;
+        w.next();
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- TMA (whole warp; lane p has page p of a tile)
+    constexpr int PAGES = KT / 16;
+    bool ok = true;
+    for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
+      const Unit w = bar.units[unit % kUnits];
+      if (!w.more) break;
+      const int32_t* table = a.block_table + (long long)w.b * a.max_blocks;
+      auto block_of = [&](int tile) {  // pages past the last are that one again: their columns are masked
+        const int page = min(tile * PAGES + lane, w.seen.pages - 1);
+        return lane < PAGES && tile < w.last ? table[w.seen.position(page) / 16] : 0;
+      };
+      int blk = block_of(w.first);
+      for (int i = 0; i < 2 * (w.last - w.first) && ok; ++i, ++loads) {
+        const uint32_t st = loads % NST;
+        if (loads >= NST) ok = __all_sync(0xffffffffu, wait_for(&bar.kv_empty[st], (loads / NST - 1) & 1, abort));
+        if (!ok) break;
+        uint64_t* full = &bar.kv_full[st];
+        if (lane == 0) mbar_arrive_expect_tx(full, L::STAGE);
+        __syncwarp();
+        unsigned char* dst = stage_of(loads) + lane * 2048;
+        if (lane < PAGES)
+          for (int c = 0; c < HD / 64; ++c)
+            tma_load_4d(dst + c * L::KCHUNK, i & 1 ? &mV : &mK, c * 64, 0, w.kvh, blk, full);
+        if (i & 1) blk = block_of(w.first + i / 2 + 1);
+        if (i == 1) {  // queries behind the first keys and values, which need not wait for the last unit's queries
+          if (unit > 0) ok = __all_sync(0xffffffffu, wait_for(&bar.q_free, (unit - 1) & 1, abort));
+          if (!ok) {
+            ++loads;
+            break;
+          }
+          const int tiles = NT == 2 && w.seen.n > npt ? 2 : 1;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar.q_full, tiles * (uint32_t)(HD * G * npt * 2));
+            for (int x = 0; x < tiles; ++x)
+              for (int c = 0; c < HD / 64; ++c)
+                tma_load_4d(sm + x * L::QTILE + c * L::QCHUNK, &mQ, c * 64, 0, w.kvh, w.token + x * npt, &bar.q_full);
+          }
+          ++queries;
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMAs
+    constexpr uint32_t idS = idesc_bf16_f32(128, KT), idO = idesc_bf16_f32(128, HD, true);
+    const uint32_t q0 = smem_addr(sm);
+    uint32_t seq = 0, np[2] = {0, 0}, units[2] = {0, 0};
+    bool ok = true;
+    for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
+      const Unit& w = bar.units[unit % kUnits];
+      if (!w.more) break;
+      const bool two = NT == 2 && w.seen.n > npt;
+      const int tiles = w.last - w.first, items = two ? 2 * tiles : tiles;
+      if (lane == 0) {
+      ok = wait_for(&bar.q_full, unit & 1, abort);
+      auto scores = [&](int e) -> bool {
+        const int x = two ? e & 1 : 0, j = two ? e >> 1 : e;
+        const uint32_t ks = seq + 2 * j;
+        if (!wait_for(&bar.kv_full[ks % NST], ks / NST & 1, abort)) return false;
+        tc_fence_after();
+        const uint32_t k0 = smem_addr(stage_of(ks)), d = tmem + L::S0 + (e & 1) * KT;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          mma_bf16(d, sw128_desc(q0 + x * L::QTILE + kk / 4 * L::QCHUNK + kk % 4 * 32),
+                   sw128_desc(k0 + kk / 4 * L::KCHUNK + kk % 4 * 32), idS, kk ? 1u : 0u);
+        mma_commit(&bar.s_full[e & 1]);
+        if (!two || x == 1) mma_commit(&bar.kv_empty[ks % NST]);
+        if (e == items - 1) mma_commit(&bar.q_free);
+        return true;
+      };
+      ok = ok && scores(0);
+      if (items > 1) ok = ok && scores(1);
+      for (int e = 0; ok && e < items; ++e) {
+        const int x = two ? e & 1 : 0, j = two ? e >> 1 : e;
+        const uint32_t vs = seq + 2 * j + 1;
+        ok = wait_for(&bar.p_full[e & 1], np[e & 1] & 1, abort) &&
+             wait_for(&bar.kv_full[vs % NST], vs / NST & 1, abort);
+        ++np[e & 1];
+        if (j == 0 && units[x] > 0) ok = ok && wait_for(&bar.o_free[x], (units[x] - 1) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v0 = smem_addr(stage_of(vs)), p = tmem + L::S0 + (e & 1) * KT;
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          mma_bf16_tmem_a(tmem + x * HD, p + kk * 8, sw128_mn_desc(v0 + kk * 2048, L::KCHUNK), idO,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&bar.pv_done[x]);
+        if (!two || x == 1) mma_commit(&bar.kv_empty[vs % NST]);
+        if (e + 2 < items) ok = scores(e + 2);
+      }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      seq += 2 * tiles;
+      ++units[0];
+      if (two) ++units[1];
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- softmax and output, a row a thread
+    const int wg = warp / 4;                 // row tile
+    const int r = tid % kRows, i_row = r / G, g = r % G;
+    const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
+    const float sign = a.sm_scale < 0.f ? -1.f : 1.f;
+    // a scale of 0 has to leave hidden keys at -inf: the smallest number serves
+    const float scale = fmaxf(fabsf(a.sm_scale) * 1.4426950408889634f, 1.17549435e-38f);
+    uint32_t ns[2] = {0, 0}, npv = 0, seq = 0;
+    bool ok = true;
+    for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
+      const Unit& w = bar.units[unit % kUnits];
+      if (!w.more) break;
+      const bool two = NT == 2 && w.seen.n > npt;
+      const int tiles = w.last - w.first, items = two ? 2 * tiles : tiles;
+      if (wg == 0 || two) {
+        const Seen& q = w.seen;
+        const int token = wg * npt + i_row;  // in the unit
+        const bool active = i_row < npt && token < q.n;
+        // Columns, numbered by visible pages: [0, vs) and [va, ve) are this row's; [h0, h1) and from `end` on no row's.
+        int vs = 0, va = 0, ve = 0;
+        const int shift = (q.front - q.from) * 16, end = q.P + q.n + shift, h0 = q.s, h1 = q.lo + shift;
+        if (active) {
+          const int pos = q.P + token;
+          ve = pos + 1 + shift;
+          va = (a.window > 0 ? max(0, pos - a.window + 1) : 0) + shift;
+          vs = min(a.sinks, q.front > 0 ? q.front * 16 : ve);
+          if (q.from > 0 && q.front == 0) vs = 0;
+        }
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < tiles; ++j) {
+          const int e = two ? 2 * j + wg : j, sb = e & 1;
+          ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[sb], (ns[sb] + (two ? j : j >> 1)) & 1, abort));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ts = tmem + L::S0 + sb * KT + lanes;
+          uint32_t s[KT];
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) tmem_ld32_nowait(ts + c, s + c);
+          tmem_wait_ld();
+          if (sign < 0.f) {
+#pragma unroll
+            for (int c = 0; c < KT; ++c) s[c] ^= 0x80000000u;
+          }
+          const int c0 = (w.first + j) * KT;
+          const bool open = (c0 >= va && c0 + KT <= ve) || c0 + KT <= vs;
+          if (!__all_sync(0xffffffffu, open)) {
+            // bits of the columns below x in a half of 64
+            auto below = [](int x) -> uint64_t { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1ull; };
+#pragma unroll
+            for (int h = 0; h < KT / 64; ++h) {
+              const int at = c0 + 64 * h;
+              const uint64_t bits = below(vs - at) | (below(ve - at) & ~below(va - at));
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (!((c < 32 ? (uint32_t)bits >> c : (uint32_t)(bits >> 32) >> (c - 32)) & 1u))
+                  s[64 * h + c] = 0xff800000u;
+            }
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < KT; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              top[k] = fmaxf(top[k], fmaxf(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])));
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+          const bool raise = mx > m + kRaise;
+          const bool rescale = raise && m != -INFINITY;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // O holds earlier tiles: the last P V has to be done before this warp's rows are scaled
+            ok = __all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv + j - 1) & 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+            const float f = rescale ? ex2_approx(m - mx) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_nowait(tmem + wg * HD + lanes + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32_nowait(tmem + wg * HD + lanes + c, o);
+            }
+            tmem_wait_st();
+          }
+          if (raise) {
+            l = rescale ? l * ex2_approx(m - mx) : 0.f;
+            m = mx;
+          }
+          // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
+          const float neg = m == -INFINITY ? 0.f : -m;
+          const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])), scale2, neg2);
+              const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              p[k] = pack_bf16x2(y.x, y.y);
+              if (k & 1) sum1 = __fadd2_rn(sum1, y);
+              else sum0 = __fadd2_rn(sum0, y);
+            }
+            tmem_st16_nowait(ts + c / 2, p);
+          }
+          tmem_wait_st();
+          sum0 = __fadd2_rn(sum0, sum1);
+          l += sum0.x + sum0.y;
+          if (wg == 0 && ((h0 < h1 && h0 < c0 + KT && h1 > c0) || end < c0 + KT)) {
+            const uint32_t vq = seq + 2 * j + 1;
+            ok = __all_sync(0xffffffffu, wait_for(&bar.kv_full[vq % NST], vq / NST & 1, abort));
+            if (!ok) break;
+            unsigned char* v = stage_of(vq);
+            for (int row = r / 8; row < KT; row += 16) {
+              const int c = c0 + row;
+              if ((c >= h0 && c < h1) || c >= end)
+#pragma unroll
+                for (int k = 0; k < HD / 64; ++k)
+                  *reinterpret_cast<uint4*>(v + k * L::KCHUNK + row * 128 + r % 8 * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[sb]);
+        }
+        npv += tiles;
+        // With one row tile the scores of the last key tile came before the P V of the one in front of it: a wait for the
+        // last P V alone would take the phase before for its own.
+        if (!two && tiles > 1)
+          ok = ok && __all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv - 2) & 1, abort));
+        ok = ok && __all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv - 1) & 1, abort));
+        if (ok) {
+          tc_fence_after();
+          const bool whole = tiles == w.tiles;
+          bf16* out = static_cast<bf16*>(a.out) + (long long)(w.token + token) * a.out_stride +
+                      (long long)(w.kvh * G + g) * HD;
+          const int c0 = w.c0, c1 = w.c1;
+          // a unit that ends in a later run lies in its first CTA's slot 1, in the others' slot 0
+          auto slot_of = [&](int c) { return slots + (long long)(2 * c + (c == c0 ? 1 : 0)) * L::SLOT + warp * 32 * (HD + 2); };
+          const float inv = 1.f / l;
+          float* mine = slot_of(blockIdx.x);
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32_nowait(tmem + wg * HD + lanes + c, o);
+            tmem_wait_ld();
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(mine + (c / 4 + k) * 128 + lane * 4) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            } else if (active) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float y[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) y[x] = __uint_as_float(o[8 * k + x]) * inv;
+                *reinterpret_cast<uint4*>(out + c + 8 * k) = pack8(y);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.o_free[wg]);
+          if (!whole) {
+            *reinterpret_cast<float2*>(mine + 32 * HD + lane * 2) = make_float2(m, l);
+            __threadfence();
+            __syncwarp();
+            int before = 0;
+            if (lane == 0) before = atomicAdd(arrived + c0 * 8 + warp, 1);
+            if (__shfl_sync(0xffffffffu, before, 0) == c1 - c0) {
+              __threadfence();
+              float top = -INFINITY, sum = 0.f;
+              for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot_of(c) + 32 * HD + lane * 2));
+              for (int c = c0; c <= c1; ++c) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(slot_of(c) + 32 * HD + lane * 2));
+                sum += x.x == -INFINITY ? 0.f : ex2_approx(x.x - top) * x.y;
+              }
+#pragma unroll 1
+              for (int k = 0; k < HD / 8; ++k) {
+                float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int c = c0; c <= c1; ++c) {
+                  const float* slot = slot_of(c);
+                  const float mc = __ldcg(slot + 32 * HD + lane * 2);
+                  const float f = (mc == -INFINITY ? 0.f : ex2_approx(mc - top)) / sum;
+                  const float4 u = __ldcg(reinterpret_cast<const float4*>(slot + (2 * k) * 128 + lane * 4));
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(slot + (2 * k + 1) * 128 + lane * 4));
+                  y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
+                  y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+                }
+                if (active) *reinterpret_cast<uint4*>(out + 8 * k) = pack8(y);
+              }
+            }
+          }
+        }
+      }
+      ns[0] += (items + 1) / 2;
+      ns[1] += items / 2;
+      seq += 2 * tiles;
+    }
+  }
+  __syncthreads();
+  if (bar.abort) {  // what this CTA started ends before its memory goes away
+    if (warp == 9 && lane == 0) {
+      mma_commit(&bar.drain);
+      mbar_wait(&bar.drain, 0);
+    }
+    if (warp == 8 && lane == 0) {
+      if (queries > 0) mbar_wait(&bar.q_full, (queries - 1) & 1);
+      for (uint32_t k = loads > NST ? loads - NST : 0; k < loads; ++k) mbar_wait(&bar.kv_full[k % NST], k / NST & 1);
+    }
+    if (tid == 0) {
+      long long x = run.base;
+      for (int b = run.b; x < run.x1; ++b) {
+        if (cost[b] > 0) a.err[b] = TV_ERR_TIMEOUT;
+        x += cost[b] * a.Hkv;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int HD>
+cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
+  using L = Shape<HD>;
+  const int G = a.Hq / a.Hkv, npt = kRows / G;
+  CUtensorMap mQ, mK, mV;
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)HD, (cuuint64_t)G, (cuuint64_t)a.Hkv, (cuuint64_t)a.T};
+    const cuuint64_t strides[3] = {(cuuint64_t)HD * 2, (cuuint64_t)G * HD * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)npt};
+    if (!make_map_bf16_sw128(&mQ, a.q, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)HD, 16, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)HD * 2, (cuuint64_t)16 * HD * 2, (cuuint64_t)a.Hkv * 16 * HD * 2};
+    const cuuint32_t box[4] = {64, 16, 1, 1};
+    if (!make_map_bf16_sw128(&mK, a.k_cache, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!make_map_bf16_sw128(&mV, a.v_cache, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  const size_t smem = L::TOTAL + 1024;
+  auto kern = window_tiles_kernel<HD>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<kSms, kThreads, smem, s>>>(a, cost, arrived, slots, npt, mQ, mK, mV);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+TileShape window_tile_shape(int Hq, int Hkv, int hd) {
+  const int npt = kRows / (Hq / Hkv);
+  return hd == 256 ? TileShape{npt, 64} : TileShape{2 * npt, 128};
+}
+
+size_t window_tiles_slots(int hd) {
+  const size_t slot = (size_t)(hd == 256 ? 1 : 2) * kRows * (hd + 2) * sizeof(float);
+  return 2 * kSms * slot;
+}
+
+cudaError_t launch_window_tiles(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
+  if (a.hd == 64) return go<64>(a, cost, arrived, slots, s);
+  return a.hd == 128 ? go<128>(a, cost, arrived, slots, s) : go<256>(a, cost, arrived, slots, s);
+}
+
+}  // namespace tv
