@@ -9,8 +9,8 @@
 // unnormalised output per row in the workspace, and the last of its CTAs joins them in the order of the runs.
 //
 // Scores S = Q K^T go to tensor memory; a thread takes a row (TMEM lane), 2^(S scale - m) as bf16 goes back over the
-// scores' columns, and O += P V reads it from there.  The running maximum is raised only when a tile passes it by more
-// than 2^8, so O is hardly ever rescaled; the sum is of the fp32 weights before their rounding, whose errors average out.
+// scores' columns, and O += P V reads it from there, half a tile at a time.  The sum is of the fp32 weights before their
+// rounding, whose errors average out.
 //   warps 0-3, 4-7   softmax of tile 0 and tile 1, output of each
 //   warp 8           TMA: queries, and K and V tiles in turn through one ring of stages
 //   warp 10          the run's units, up to four ahead
@@ -28,7 +28,8 @@ constexpr int kRows = 128;
 constexpr int kThreads = 352;
 constexpr int kUnits = 4;       // units known ahead
 constexpr int kLeast = 4;       // cost of a run, at least: a unit of two key tiles
-constexpr float kRaise = 8.0f;  // log2
+constexpr float kRaise = 8.0f;     // log2
+constexpr float kMost = 65536.f;   // of 64 weights, as sums against the maximum held
 
 template <int HD>
 struct Shape {
@@ -48,9 +49,9 @@ struct Shape {
   static_assert(TOTAL + 1024 <= 232448, "shared memory");
 };
 
-// A phase of the barrier, or false after some seconds at most, or once another role has given up.  A try sleeps
-// in the barrier unit for about a microsecond.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// A phase of the barrier, or false after some seconds at most, or once another role has given up.  Looks once, then
+// tries, each try asleep in the barrier unit for about a microsecond.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
   for (uint32_t it = 0; it < (1u << 20); ++it) {
     uint32_t done;
     asm volatile(
@@ -65,6 +66,48 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   }
   *abort = 1;
   return false;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, abort);
+}
+
+// The MMA warp runs as one, so that addresses stay in uniform registers; one elected lane issues.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// Descriptors as sw128_desc and sw128_mn_desc make them, in two words: the second is always the same.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) {
+  return (saddr >> 4) | (leading >> 4) << 16;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(elected)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
@@ -108,7 +151,7 @@ struct Unit {
 struct Bars {
   uint64_t q_full, q_free;
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], pv_half[2], pv_done[2], o_free[2];
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t drain;
   uint32_t tmem;
@@ -224,7 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.p_half[s], 4);
       mbar_init(&bar.p_full[s], 4);
+      mbar_init(&bar.pv_half[s], 1);
       mbar_init(&bar.pv_done[s], 1);
       mbar_init(&bar.o_free[s], 4);
     }
@@ -309,54 +354,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
     constexpr uint32_t idS = idesc_bf16_f32(128, KT), idO = idesc_bf16_f32(128, HD, true);
-    const uint32_t q0 = smem_addr(sm);
-    uint32_t seq = 0, np[2] = {0, 0}, units[2] = {0, 0};
+    const uint32_t elected = elect_lane();
+    const uint32_t q_low = desc_low(smem_addr(sm), 16);
+    const uint32_t k_low = desc_low(smem_addr(sm + L::RING), 16), v_low = desc_low(smem_addr(sm + L::RING), L::KCHUNK);
+    // the ring: keys and values take turns
+    uint32_t kst = 0, kph = 0, vst = 1, vph = 0;
+    auto advance = [](uint32_t& st, uint32_t& ph) {
+      st += 2;
+      if (st >= NST) st -= NST, ph ^= 1;
+    };
+    uint32_t pph[2] = {0, 0}, units[2] = {0, 0};
     bool ok = true;
+    auto wait = [&](uint64_t* w, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(w, parity, abort)); };
     for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
       const Unit& w = bar.units[unit % kUnits];
       if (!w.more) break;
-      const bool two = NT == 2 && w.seen.n > npt;
-      const int tiles = w.last - w.first, items = two ? 2 * tiles : tiles;
-      if (lane == 0) {
-      ok = wait_for(&bar.q_full, unit & 1, abort);
-      auto scores = [&](int e) -> bool {
-        const int x = two ? e & 1 : 0, j = two ? e >> 1 : e;
-        const uint32_t ks = seq + 2 * j;
-        if (!wait_for(&bar.kv_full[ks % NST], ks / NST & 1, abort)) return false;
+      const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.seen.n, 0) > npt;
+      const int tiles = __shfl_sync(0xffffffffu, w.last - w.first, 0);
+      ok = wait(&bar.q_full, unit & 1);
+      // scores of row tile X from the next keys into buffer SB
+      auto scores = [&](int x, int sb, bool done, bool last) -> bool {
+        if (!wait(&bar.kv_full[kst], kph)) return false;
         tc_fence_after();
-        const uint32_t k0 = smem_addr(stage_of(ks)), d = tmem + L::S0 + (e & 1) * KT;
+        const uint32_t q = q_low + x * (L::QTILE >> 4), k = k_low + kst * (L::STAGE >> 4), d = tmem + L::S0 + sb * KT;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_bf16(d, sw128_desc(q0 + x * L::QTILE + kk / 4 * L::QCHUNK + kk % 4 * 32),
-                   sw128_desc(k0 + kk / 4 * L::KCHUNK + kk % 4 * 32), idS, kk ? 1u : 0u);
-        mma_commit(&bar.s_full[e & 1]);
-        if (!two || x == 1) mma_commit(&bar.kv_empty[ks % NST]);
-        if (e == items - 1) mma_commit(&bar.q_free);
+          mma_ss(elected, d, q + ((kk / 4 * L::QCHUNK + kk % 4 * 32) >> 4), k + ((kk / 4 * L::KCHUNK + kk % 4 * 32) >> 4), idS,
+                 kk ? 1u : 0u);
+        commit_to(elected, &bar.s_full[sb]);
+        if (done) {
+          commit_to(elected, &bar.kv_empty[kst]);
+          advance(kst, kph);
+        }
+        if (last) commit_to(elected, &bar.q_free);
         return true;
       };
-      ok = ok && scores(0);
-      if (items > 1) ok = ok && scores(1);
-      for (int e = 0; ok && e < items; ++e) {
-        const int x = two ? e & 1 : 0, j = two ? e >> 1 : e;
-        const uint32_t vs = seq + 2 * j + 1;
-        ok = wait_for(&bar.p_full[e & 1], np[e & 1] & 1, abort) &&
-             wait_for(&bar.kv_full[vs % NST], vs / NST & 1, abort);
-        ++np[e & 1];
-        if (j == 0 && units[x] > 0) ok = ok && wait_for(&bar.o_free[x], (units[x] - 1) & 1, abort);
-        if (!ok) break;
+      // output of row tile x from the next values and the weights in buffer sb
+      auto outputs = [&](int x, int sb, bool fresh, bool done) -> bool {
+        if (!wait(KT == 128 ? &bar.p_half[sb] : &bar.p_full[sb], pph[sb])) return false;
+        if (!wait(&bar.kv_full[vst], vph)) return false;
+        if (fresh && units[x] > 0 && !wait(&bar.o_free[x], (units[x] - 1) & 1)) return false;
         tc_fence_after();
-        const uint32_t v0 = smem_addr(stage_of(vs)), p = tmem + L::S0 + (e & 1) * KT;
+        const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::S0 + sb * KT;
 #pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk)
-          mma_bf16_tmem_a(tmem + x * HD, p + kk * 8, sw128_mn_desc(v0 + kk * 2048, L::KCHUNK), idO,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&bar.pv_done[x]);
-        if (!two || x == 1) mma_commit(&bar.kv_empty[vs % NST]);
-        if (e + 2 < items) ok = scores(e + 2);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(elected, tmem + x * HD, p + kk * 8, v + (kk * 2048 >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
+        if constexpr (KT == 128) {
+          commit_to(elected, &bar.pv_half[x]);
+          if (!wait(&bar.p_full[sb], pph[sb])) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) mma_ts(elected, tmem + x * HD, p + kk * 8, v + (kk * 2048 >> 4), idO, 1u);
+        }
+        pph[sb] ^= 1;
+        commit_to(elected, &bar.pv_done[x]);
+        if (done) {
+          commit_to(elected, &bar.kv_empty[vst]);
+          advance(vst, vph);
+        }
+        return true;
+      };
+      if (two) {
+        const bool one = tiles == 1;
+        ok = ok && scores(0, 0, false, false) && scores(1, 1, true, one);
+        for (int j = 0; ok && j < tiles; ++j) {
+          const bool more = j + 1 < tiles;
+          ok = outputs(0, 0, j == 0, false) && (!more || scores(0, 0, false, false)) && outputs(1, 1, j == 0, true) &&
+               (!more || scores(1, 1, true, j + 2 == tiles));
+        }
+      } else {
+        ok = ok && scores(0, 0, true, tiles == 1) && (tiles == 1 || scores(0, 1, true, tiles == 2));
+        for (int j = 0; ok && j < tiles; ++j)
+          ok = outputs(0, j & 1, j == 0, true) && (j + 2 >= tiles || scores(0, j & 1, true, j + 3 == tiles));
       }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      seq += 2 * tiles;
       ++units[0];
       if (two) ++units[1];
     }
@@ -368,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sign = a.sm_scale < 0.f ? -1.f : 1.f;
     // a scale of 0 has to leave hidden keys at -inf: the smallest number serves
     const float scale = fmaxf(fabsf(a.sm_scale) * 1.4426950408889634f, 1.17549435e-38f);
-    uint32_t ns[2] = {0, 0}, npv = 0, seq = 0;
+    uint32_t s_phase = 0, npv = 0, seq = 0;  // s_phase: a bit a buffer of scores
     bool ok = true;
     for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
       const Unit& w = bar.units[unit % kUnits];
@@ -392,89 +462,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < tiles; ++j) {
           const int e = two ? 2 * j + wg : j, sb = e & 1;
-          ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[sb], (ns[sb] + (two ? j : j >> 1)) & 1, abort));
+          ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[sb], ((s_phase >> sb) ^ (two ? j : j >> 1)) & 1, abort));
           if (!ok) break;
           tc_fence_after();
           const uint32_t ts = tmem + L::S0 + sb * KT + lanes;
-          uint32_t s[KT];
-#pragma unroll
-          for (int c = 0; c < KT; c += 32) tmem_ld32_nowait(ts + c, s + c);
-          tmem_wait_ld();
-          if (sign < 0.f) {
-#pragma unroll
-            for (int c = 0; c < KT; ++c) s[c] ^= 0x80000000u;
-          }
           const int c0 = (w.first + j) * KT;
           const bool open = (c0 >= va && c0 + KT <= ve) || c0 + KT <= vs;
-          if (!__all_sync(0xffffffffu, open)) {
-            // bits of the columns below x in a half of 64
-            auto below = [](int x) -> uint64_t { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1ull; };
-#pragma unroll
-            for (int h = 0; h < KT / 64; ++h) {
-              const int at = c0 + 64 * h;
-              const uint64_t bits = below(vs - at) | (below(ve - at) & ~below(va - at));
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (!((c < 32 ? (uint32_t)bits >> c : (uint32_t)(bits >> 32) >> (c - 32)) & 1u))
-                  s[64 * h + c] = 0xff800000u;
-            }
-          }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < KT; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top[k] = fmaxf(top[k], fmaxf(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])));
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-          const bool raise = mx > m + kRaise;
-          const bool rescale = raise && m != -INFINITY;
-          if (__any_sync(0xffffffffu, rescale)) {
-            // O holds earlier tiles: the last P V has to be done before this warp's rows are scaled
-            ok = __all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv + j - 1) & 1, abort));
-            if (!ok) break;
-            tc_fence_after();
-            const float f = rescale ? ex2_approx(m - mx) : 1.f;
+          if (sign < 0.f || !__all_sync(0xffffffffu, open)) {
+            // hidden keys to -inf, in place
+            auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 32) {
-              uint32_t o[32];
-              tmem_ld32_nowait(tmem + wg * HD + lanes + c, o);
+            for (int c = 0; c < KT; c += 32) {
+              const int at = c0 + c;
+              const uint32_t bits = below(vs - at) | (below(ve - at) & ~below(va - at));
+              uint32_t x[32];
+              tmem_ld32_nowait(ts + c, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32_nowait(tmem + wg * HD + lanes + c, o);
+              for (int k = 0; k < 32; ++k)
+                x[k] = (bits >> k) & 1u ? __float_as_uint(__uint_as_float(x[k]) * sign) : 0xff800000u;
+              tmem_st32_nowait(ts + c, x);
             }
             tmem_wait_st();
           }
-          if (raise) {
-            l = rescale ? l * ex2_approx(m - mx) : 0.f;
-            m = mx;
-          }
-          // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
-          const float neg = m == -INFINITY ? 0.f : -m;
-          const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-          for (int c = 0; c < KT; c += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])), scale2, neg2);
-              const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-              p[k] = pack_bf16x2(y.x, y.y);
-              if (k & 1) sum1 = __fadd2_rn(sum1, y);
-              else sum0 = __fadd2_rn(sum0, y);
-            }
-            tmem_st16_nowait(ts + c / 2, p);
-          }
-          tmem_wait_st();
-          sum0 = __fadd2_rn(sum0, sum1);
-          l += sum0.x + sum0.y;
           if (wg == 0 && ((h0 < h1 && h0 < c0 + KT && h1 > c0) || end < c0 + KT)) {
             const uint32_t vq = seq + 2 * j + 1;
             ok = __all_sync(0xffffffffu, wait_for(&bar.kv_full[vq % NST], vq / NST & 1, abort));
             if (!ok) break;
             unsigned char* v = stage_of(vq);
+#pragma unroll 1
             for (int row = r / 8; row < KT; row += 16) {
               const int c = c0 + row;
               if ((c >= h0 && c < h1) || c >= end)
@@ -484,8 +500,91 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async();
           }
-          tc_fence_before();
-          __syncwarp();
+          // The weights of 64 keys, scores x (the first 32) and y, to columns `to` on.  The maximum need not be looked for:
+          // m is that of some earlier keys of the row, and weights up to 2^kMost of the largest of those do no harm
+          // in fp32 and bf16.  Where a row has no m yet, or its sum shows a larger weight, the maximum is taken, O and l are
+          // scaled to it, and the weights are made again.
+          auto weigh = [&](const uint32_t* x, const uint32_t* y, uint32_t to, int half) -> bool {
+            for (bool again = false;; again = true) {
+              if (again || __any_sync(0xffffffffu, m == -INFINITY)) {
+                tmem_wait_ld();
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[c + k]), __uint_as_float(y[c + k])));
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                const bool raise = mx > m + kRaise;
+                const bool rescale = raise && m != -INFINITY;
+                if (__any_sync(0xffffffffu, rescale)) {
+                  // O holds earlier keys: their products have to be done before this warp's rows are scaled
+                  if (j > 0 && !__all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv + j - 1) & 1, abort))) return false;
+                  if (half > 0 && !__all_sync(0xffffffffu, wait_for(&bar.pv_half[wg], (npv + j) & 1, abort))) return false;
+                  tc_fence_after();
+                  const float f = rescale ? ex2_approx(m - mx) : 1.f;
+                  l *= f;
+#pragma unroll 1
+                  for (int c = 0; c < HD; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16_nowait(tmem + wg * HD + lanes + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st16_nowait(tmem + wg * HD + lanes + c, o);
+                  }
+                  tmem_wait_st();
+                }
+                if (raise) m = mx;
+              }
+              // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
+              const float neg = m == -INFINITY ? 0.f : -m;
+              const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+              float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+              auto part = [&](const uint32_t* v, uint32_t at) {
+                uint32_t p[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float2 e = __ffma2_rn(
+                      make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), scale2, neg2);
+                  const float2 w2 = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                  p[k] = pack_bf16x2(w2.x, w2.y);
+                  if (k & 1) sum1 = __fadd2_rn(sum1, w2);
+                  else sum0 = __fadd2_rn(sum0, w2);
+                }
+                tmem_st16_nowait(at, p);
+              };
+              part(x, to);
+              tmem_wait_ld();
+              part(y, to + 16);
+              sum0 = __fadd2_rn(sum0, sum1);
+              const float sum = sum0.x + sum0.y;
+              if (again || !__any_sync(0xffffffffu, !(sum < kMost))) {
+                l += sum;
+                break;
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            return true;
+          };
+          uint32_t s0[32], s1[32], s2[32];
+          tmem_ld32_nowait(ts, s0);
+          tmem_ld32_nowait(ts + 32, s1);
+          tmem_wait_ld();
+          if constexpr (KT == 128) {
+            // the second half: its first scores are on their way while the first half's weights are made
+            tmem_ld32_nowait(ts + 64, s2);
+            ok = weigh(s0, s1, ts, 0);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&bar.p_half[sb]);
+            tmem_ld32_nowait(ts + 96, s1);
+            ok = weigh(s2, s1, ts + 32, 1);
+          } else {
+            ok = weigh(s0, s1, ts, 0);
+          }
+          if (!ok) break;
           if (lane == 0) mbar_arrive(&bar.p_full[sb]);
         }
         npv += tiles;
@@ -536,38 +635,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__shfl_sync(0xffffffffu, before, 0) == c1 - c0) {
               __threadfence();
               float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
               for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot_of(c) + 32 * HD + lane * 2));
-              for (int c = c0; c <= c1; ++c) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(slot_of(c) + 32 * HD + lane * 2));
-                sum += x.x == -INFINITY ? 0.f : ex2_approx(x.x - top) * x.y;
-              }
 #pragma unroll 1
-              for (int k = 0; k < HD / 8; ++k) {
-                float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              for (int k = 0; k < HD / 4; k += 8) {  // 32 columns: eight loads at once
+                float y[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) y[x] = 0.f;
+                sum = 0.f;
+#pragma unroll 1
                 for (int c = c0; c <= c1; ++c) {
                   const float* slot = slot_of(c);
-                  const float mc = __ldcg(slot + 32 * HD + lane * 2);
-                  const float f = (mc == -INFINITY ? 0.f : ex2_approx(mc - top)) / sum;
-                  const float4 u = __ldcg(reinterpret_cast<const float4*>(slot + (2 * k) * 128 + lane * 4));
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(slot + (2 * k + 1) * 128 + lane * 4));
-                  y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
-                  y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+                  const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot + 32 * HD + lane * 2));
+                  float4 u[8];
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) u[x] = __ldcg(reinterpret_cast<const float4*>(slot + (k + x) * 128 + lane * 4));
+                  const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+                  sum += f * ml.y;
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) {
+                    y[4 * x] += f * u[x].x, y[4 * x + 1] += f * u[x].y;
+                    y[4 * x + 2] += f * u[x].z, y[4 * x + 3] += f * u[x].w;
+                  }
                 }
-                if (active) *reinterpret_cast<uint4*>(out + 8 * k) = pack8(y);
+                const float total = 1.f / sum;
+#pragma unroll
+                for (int x = 0; x < 32; ++x) y[x] *= total;
+                if (active)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(out + 4 * k + 8 * x) = pack8(y + 8 * x);
               }
             }
           }
         }
       }
-      ns[0] += (items + 1) / 2;
-      ns[1] += items / 2;
+      s_phase ^= ((items + 1) / 2 & 1) | (items / 2 & 1) << 1;
       seq += 2 * tiles;
     }
   }
   __syncthreads();
   if (bar.abort) {  // what this CTA started ends before its memory goes away
-    if (warp == 9 && lane == 0) {
-      mma_commit(&bar.drain);
+    if (warp == 9) {
+      commit_to(elect_lane(), &bar.drain);
       mbar_wait(&bar.drain, 0);
     }
     if (warp == 8 && lane == 0) {
