@@ -12,7 +12,7 @@
 // scores' columns, and O += P V reads it from there, half a tile at a time.  The sum is of the fp32 weights before their
 // rounding, whose errors average out.
 //   warps 0-3, 4-7   softmax of tile 0 and tile 1, output of each
-//   warp 8           TMA: queries, and K and V tiles in turn through one ring of stages
+//   warp 8           TMA: queries, K and V tiles through a ring each
 //   warp 10          the run's units, up to four ahead
 //   warp 9           MMAs: item e of a unit is (key tile, row tile); S(e + 2) follows P V(e)
 // Values that no token of the unit sees may be anything, and 0 times that is not 0: their rows are cleared in
@@ -35,13 +35,15 @@ template <int HD>
 struct Shape {
   static constexpr int NT = HD == 256 ? 1 : 2;          // row tiles
   static constexpr int KT = HD == 256 ? 64 : 128;       // keys of a tile
-  static constexpr int NST = HD == 64 ? 8 : 5;          // K or V tiles in the ring
+  static constexpr int KS = HD == 64 ? 4 : 3;           // K tiles in their ring
+  static constexpr int VS = HD == 64 ? 4 : 2;           // V tiles in theirs
   static constexpr uint32_t QCHUNK = kRows * 128;       // 64 columns of a row tile
   static constexpr uint32_t QTILE = HD / 64 * QCHUNK;
   static constexpr uint32_t KCHUNK = KT * 128;          // 64 columns of a key tile
   static constexpr uint32_t STAGE = HD / 64 * KCHUNK;
-  static constexpr uint32_t RING = NT * QTILE;
-  static constexpr uint32_t BARS = RING + NST * STAGE;
+  static constexpr uint32_t K0 = NT * QTILE;
+  static constexpr uint32_t V0 = K0 + KS * STAGE;
+  static constexpr uint32_t BARS = V0 + VS * STAGE;
   static constexpr uint32_t TOTAL = BARS + 1024;
   static constexpr uint32_t S0 = NT * HD;               // TMEM: outputs, then two buffers of scores
   static constexpr int SLOT = NT * kRows * (HD + 2);    // floats of a cut unit
@@ -150,7 +152,7 @@ struct Unit {
 
 struct Bars {
   uint64_t q_full, q_free;
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_half[2], p_full[2], pv_half[2], pv_done[2], o_free[2];
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t drain;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                         const __grid_constant__ CUtensorMap mV) {
   using L = Shape<HD>;
-  constexpr int NT = L::NT, KT = L::KT, NST = L::NST;
+  constexpr int NT = L::NT, KT = L::KT, KS = L::KS, VS = L::VS;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -261,9 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_free, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&bar.kv_full[s], 1);
-      mbar_init(&bar.kv_empty[s], 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(&bar.v_full[s], 1);
+      mbar_init(&bar.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1);
@@ -286,8 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  auto stage_of = [&](uint32_t seq) { return sm + L::RING + seq % NST * L::STAGE; };
-  uint32_t loads = 0, queries = 0;  // what the producer has started
+  uint32_t k_loads = 0, v_loads = 0, q_loads = 0;  // what the producer has started
   // the k-th unit, once it is known; a warp hands it back when it needs no more of it
   auto known = [&](uint32_t k) -> bool {
     return __all_sync(0xffffffffu, wait_for(&bar.unit_full[k % kUnits], k / kUnits & 1, abort));
@@ -321,25 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int page = min(tile * PAGES + lane, w.seen.pages - 1);
         return lane < PAGES && tile < w.last ? table[w.seen.position(page) / 16] : 0;
       };
-      int blk = block_of(w.first);
-      for (int i = 0; i < 2 * (w.last - w.first) && ok; ++i, ++loads) {
-        const uint32_t st = loads % NST;
-        if (loads >= NST) ok = __all_sync(0xffffffffu, wait_for(&bar.kv_empty[st], (loads / NST - 1) & 1, abort));
-        if (!ok) break;
-        uint64_t* full = &bar.kv_full[st];
-        if (lane == 0) mbar_arrive_expect_tx(full, L::STAGE);
+      auto load = [&](const CUtensorMap* map, uint32_t ring, uint32_t stages, uint64_t* fulls, uint64_t* empties, uint32_t& loads,
+                      int blk) -> bool {
+        const uint32_t st = loads % stages;
+        if (loads >= stages && !__all_sync(0xffffffffu, wait_for(&empties[st], (loads / stages - 1) & 1, abort))) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&fulls[st], L::STAGE);
         __syncwarp();
-        unsigned char* dst = stage_of(loads) + lane * 2048;
         if (lane < PAGES)
           for (int c = 0; c < HD / 64; ++c)
-            tma_load_4d(dst + c * L::KCHUNK, i & 1 ? &mV : &mK, c * 64, 0, w.kvh, blk, full);
-        if (i & 1) blk = block_of(w.first + i / 2 + 1);
-        if (i == 1) {  // queries behind the first keys and values, which need not wait for the last unit's queries
+            tma_load_4d(sm + ring + st * L::STAGE + c * L::KCHUNK + lane * 2048, map, c * 64, 0, w.kvh, blk, &fulls[st]);
+        ++loads;
+        return true;
+      };
+      // keys run a tile ahead of values: scores are made that much earlier than outputs
+      int blk = block_of(w.first), ahead = block_of(w.first + 1);
+      ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, blk);
+      for (int i = w.first; ok && i < w.last; ++i) {
+        const int after = block_of(i + 2);
+        if (i + 1 < w.last) ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, ahead);
+        if (ok && i == w.first) {  // queries behind the first keys, which need not wait for the last unit's queries
           if (unit > 0) ok = __all_sync(0xffffffffu, wait_for(&bar.q_free, (unit - 1) & 1, abort));
-          if (!ok) {
-            ++loads;
-            break;
-          }
+          if (!ok) break;
           const int tiles = NT == 2 && w.seen.n > npt ? 2 : 1;
           if (lane == 0) {
             mbar_arrive_expect_tx(&bar.q_full, tiles * (uint32_t)(HD * G * npt * 2));
@@ -347,8 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < HD / 64; ++c)
                 tma_load_4d(sm + x * L::QTILE + c * L::QCHUNK, &mQ, c * 64, 0, w.kvh, w.token + x * npt, &bar.q_full);
           }
-          ++queries;
+          ++q_loads;
         }
+        ok = ok && load(&mV, L::V0, VS, bar.v_full, bar.v_empty, v_loads, blk);
+        blk = ahead, ahead = after;
       }
     }
   } else if (warp == 9) {
@@ -356,12 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idS = idesc_bf16_f32(128, KT), idO = idesc_bf16_f32(128, HD, true);
     const uint32_t elected = elect_lane();
     const uint32_t q_low = desc_low(smem_addr(sm), 16);
-    const uint32_t k_low = desc_low(smem_addr(sm + L::RING), 16), v_low = desc_low(smem_addr(sm + L::RING), L::KCHUNK);
-    // the ring: keys and values take turns
-    uint32_t kst = 0, kph = 0, vst = 1, vph = 0;
-    auto advance = [](uint32_t& st, uint32_t& ph) {
-      st += 2;
-      if (st >= NST) st -= NST, ph ^= 1;
+    const uint32_t k_low = desc_low(smem_addr(sm + L::K0), 16), v_low = desc_low(smem_addr(sm + L::V0), L::KCHUNK);
+    uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // stages and phases of the rings
+    auto advance = [](uint32_t& st, uint32_t& ph, uint32_t stages) {
+      if (++st == stages) st = 0, ph ^= 1;
     };
     uint32_t pph[2] = {0, 0}, units[2] = {0, 0};
     bool ok = true;
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(&bar.q_full, unit & 1);
       // scores of row tile X from the next keys into buffer SB
       auto scores = [&](int x, int sb, bool done, bool last) -> bool {
-        if (!wait(&bar.kv_full[kst], kph)) return false;
+        if (!wait(&bar.k_full[kst], kph)) return false;
         tc_fence_after();
         const uint32_t q = q_low + x * (L::QTILE >> 4), k = k_low + kst * (L::STAGE >> 4), d = tmem + L::S0 + sb * KT;
 #pragma unroll
@@ -383,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  kk ? 1u : 0u);
         commit_to(elected, &bar.s_full[sb]);
         if (done) {
-          commit_to(elected, &bar.kv_empty[kst]);
-          advance(kst, kph);
+          commit_to(elected, &bar.k_empty[kst]);
+          advance(kst, kph, KS);
         }
         if (last) commit_to(elected, &bar.q_free);
         return true;
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // output of row tile x from the next values and the weights in buffer sb
       auto outputs = [&](int x, int sb, bool fresh, bool done) -> bool {
         if (!wait(KT == 128 ? &bar.p_half[sb] : &bar.p_full[sb], pph[sb])) return false;
-        if (!wait(&bar.kv_full[vst], vph)) return false;
+        if (!wait(&bar.v_full[vst], vph)) return false;
         if (fresh && units[x] > 0 && !wait(&bar.o_free[x], (units[x] - 1) & 1)) return false;
         tc_fence_after();
         const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::S0 + sb * KT;
@@ -409,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         pph[sb] ^= 1;
         commit_to(elected, &bar.pv_done[x]);
         if (done) {
-          commit_to(elected, &bar.kv_empty[vst]);
-          advance(vst, vph);
+          commit_to(elected, &bar.v_empty[vst]);
+          advance(vst, vph, VS);
         }
         return true;
       };
@@ -486,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
           if (wg == 0 && ((h0 < h1 && h0 < c0 + KT && h1 > c0) || end < c0 + KT)) {
-            const uint32_t vq = seq + 2 * j + 1;
-            ok = __all_sync(0xffffffffu, wait_for(&bar.kv_full[vq % NST], vq / NST & 1, abort));
+            const uint32_t vq = seq + j, vst = vq % VS;
+            ok = __all_sync(0xffffffffu, wait_for(&bar.v_full[vst], vq / VS & 1, abort));
             if (!ok) break;
-            unsigned char* v = stage_of(vq);
+            unsigned char* v = sm + L::V0 + vst * L::STAGE;
 #pragma unroll 1
             for (int row = r / 8; row < KT; row += 16) {
               const int c = c0 + row;
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       s_phase ^= ((items + 1) / 2 & 1) | (items / 2 & 1) << 1;
-      seq += 2 * tiles;
+      seq += tiles;
     }
   }
   __syncthreads();
@@ -680,8 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&bar.drain, 0);
     }
     if (warp == 8 && lane == 0) {
-      if (queries > 0) mbar_wait(&bar.q_full, (queries - 1) & 1);
-      for (uint32_t k = loads > NST ? loads - NST : 0; k < loads; ++k) mbar_wait(&bar.kv_full[k % NST], k / NST & 1);
+      if (q_loads > 0) mbar_wait(&bar.q_full, (q_loads - 1) & 1);
+      for (uint32_t k = k_loads > KS ? k_loads - KS : 0; k < k_loads; ++k) mbar_wait(&bar.k_full[k % KS], k / KS & 1);
+      for (uint32_t k = v_loads > VS ? v_loads - VS : 0; k < v_loads; ++k) mbar_wait(&bar.v_full[k % VS], k / VS & 1);
     }
     if (tid == 0) {
       long long x = run.base;
