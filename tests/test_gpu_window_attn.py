@@ -256,3 +256,21 @@ def test_prompts_long_enough_for_many_tiles():
                     real=c["real"][[0 if r < 1500 else 1 for r in rows]])
         check(part, out[torch.tensor(rows, device=DEV)], window, sinks)
     assert np.isfinite(f64(out)).all()
+
+
+@pytest.mark.parametrize("hd,Hq", [(64, 8), (128, 8), (256, 8)])
+def test_units_of_one_and_two_row_tiles_side_by_side(hd, Hq):
+    # a CTA's run holds sequences of few query rows behind many keys, then ones of many rows, in any order
+    rng = np.random.default_rng(hd)
+    lens = [int(x) for x in rng.choice([3, 20, 33, 64, 70], size=150)]
+    prefix = [int(x) for x in rng.integers(300, 900, size=150)]
+    c = case(lens, prefix, Hq, 2, hd, seed=16)
+    for window, sinks in ((0, 0), (400, 4)):
+        out, err = attend(c, window, sinks, max_len=70)
+        assert not any(err)
+        rows = np.sort(rng.choice(sum(lens), size=120, replace=False))
+        seq = np.searchsorted(np.cumsum(lens), rows, side="right")
+        before = [prefix[b] + int(r) - c["starts"][b] for b, r in zip(seq, rows)]
+        at = torch.tensor(rows, device=DEV)
+        part = dict(c, q=c["q"][at], starts=list(range(len(rows))), lens=[1] * len(rows), before=before, real=c["real"][seq])
+        check(part, out[at], window, sinks)

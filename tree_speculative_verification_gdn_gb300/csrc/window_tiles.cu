@@ -675,6 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      } else {
+        // Every phase of its buffer is seen in turn, the ones for the other row tile too: a wait that is two phases ahead
+        // would be over before its time.
+        for (int k = 0; ok && k < items / 2; ++k)
+          ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[1], ((s_phase >> 1) ^ k) & 1, abort));
       }
       s_phase ^= ((items + 1) / 2 & 1) | (items / 2 & 1) << 1;
       seq += tiles;
