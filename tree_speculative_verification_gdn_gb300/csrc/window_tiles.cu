@@ -379,10 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.seen.n, 0) > npt;
       const int tiles = __shfl_sync(0xffffffffu, w.last - w.first, 0);
       ok = wait(&bar.q_full, unit & 1);
-      // scores of row tile X from the next keys into buffer SB
-      auto scores = [&](int x, int sb, bool done, bool last) -> bool {
-        if (!wait(&bar.k_full[kst], kph)) return false;
-        tc_fence_after();
+      // scores of row tile x from the next keys, which have landed, into buffer sb
+      auto scores = [&](int x, int sb, bool done, bool last) {
         const uint32_t q = q_low + x * (L::QTILE >> 4), k = k_low + kst * (L::STAGE >> 4), d = tmem + L::S0 + sb * KT;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
@@ -394,20 +392,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance(kst, kph, KS);
         }
         if (last) commit_to(elected, &bar.q_free);
-        return true;
       };
-      // output of row tile x from the next values and the weights in buffer sb
-      auto outputs = [&](int x, int sb, bool fresh, bool done) -> bool {
-        if (!wait(KT == 128 ? &bar.p_half[sb] : &bar.p_full[sb], pph[sb])) return false;
+      // Output of row tile x from the next values and the weights in buffer sb.  Whatever else is needed, the next keys too, is
+      // waited for first: the weights are what comes last.
+      auto outputs = [&](int x, int sb, bool fresh, bool done, bool more) -> bool {
         if (!wait(&bar.v_full[vst], vph)) return false;
         if (fresh && units[x] > 0 && !wait(&bar.o_free[x], (units[x] - 1) & 1)) return false;
-        tc_fence_after();
         const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::S0 + sb * KT;
+        if (KT == 64 && more && !wait(&bar.k_full[kst], kph)) return false;
+        if (!wait(KT == 128 ? &bar.p_half[sb] : &bar.p_full[sb], pph[sb])) return false;
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_ts(elected, tmem + x * HD, p + kk * 8, v + (kk * 2048 >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
         if constexpr (KT == 128) {
           commit_to(elected, &bar.pv_half[x]);
+          if (more && !wait(&bar.k_full[kst], kph)) return false;
           if (!wait(&bar.p_full[sb], pph[sb])) return false;
           tc_fence_after();
 #pragma unroll
@@ -421,18 +421,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
+      ok = ok && wait(&bar.k_full[kst], kph);
+      if (!ok) break;
+      tc_fence_after();
       if (two) {
-        const bool one = tiles == 1;
-        ok = ok && scores(0, 0, false, false) && scores(1, 1, true, one);
+        scores(0, 0, false, false);
+        scores(1, 1, true, tiles == 1);
         for (int j = 0; ok && j < tiles; ++j) {
           const bool more = j + 1 < tiles;
-          ok = outputs(0, 0, j == 0, false) && (!more || scores(0, 0, false, false)) && outputs(1, 1, j == 0, true) &&
-               (!more || scores(1, 1, true, j + 2 == tiles));
+          ok = outputs(0, 0, j == 0, false, more);
+          if (ok && more) scores(0, 0, false, false);
+          ok = ok && outputs(1, 1, j == 0, true, more);
+          if (ok && more) scores(1, 1, true, j + 2 == tiles);
         }
       } else {
-        ok = ok && scores(0, 0, true, tiles == 1) && (tiles == 1 || scores(0, 1, true, tiles == 2));
-        for (int j = 0; ok && j < tiles; ++j)
-          ok = outputs(0, j & 1, j == 0, true) && (j + 2 >= tiles || scores(0, j & 1, true, j + 3 == tiles));
+        scores(0, 0, true, tiles == 1);
+        if (tiles > 1) {
+          ok = wait(&bar.k_full[kst], kph);
+          if (!ok) break;
+          tc_fence_after();
+          scores(0, 1, true, tiles == 2);
+        }
+        for (int j = 0; ok && j < tiles; ++j) {
+          ok = outputs(0, j & 1, j == 0, true, j + 2 < tiles);
+          if (ok && j + 2 < tiles) scores(0, j & 1, true, j + 3 == tiles);
+        }
       }
       ++units[0];
       if (two) ++units[1];
@@ -678,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // Every phase of its buffer is seen in turn, the ones for the other row tile too: a wait that is two phases ahead
         // would be over before its time.
-        for (int k = 0; ok && k < items / 2; ++k)
+        for (int k = 0; NT == 2 && ok && k < items / 2; ++k)
           ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[1], ((s_phase >> 1) ^ k) & 1, abort));
       }
       s_phase ^= ((items + 1) / 2 & 1) | (items / 2 & 1) << 1;
