@@ -479,16 +479,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           vs = min(a.sinks, q.front > 0 ? q.front * 16 : ve);
           if (q.from > 0 && q.front == 0) vs = 0;
         }
+        // the columns that every row of the warp sees; rows of no token do not count, here and below
+        const int all_vs = __reduce_min_sync(0xffffffffu, active ? vs : 0x7fffffff),
+                  all_va = __reduce_max_sync(0xffffffffu, active ? va : 0),
+                  all_ve = __reduce_min_sync(0xffffffffu, active ? ve : 0x7fffffff);
         float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < tiles; ++j) {
+        bool begun = false;  // every row of the warp has an m
+        int c0 = w.first * KT;
+        for (int j = 0; j < tiles; ++j, c0 += KT) {
           const int e = two ? 2 * j + wg : j, sb = e & 1;
           ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[sb], ((s_phase >> sb) ^ (two ? j : j >> 1)) & 1, abort));
           if (!ok) break;
           tc_fence_after();
           const uint32_t ts = tmem + L::S0 + sb * KT + lanes;
-          const int c0 = (w.first + j) * KT;
-          const bool open = (c0 >= va && c0 + KT <= ve) || c0 + KT <= vs;
-          if (sign < 0.f || !__all_sync(0xffffffffu, open)) {
+          if (sign < 0.f || !((c0 >= all_va && c0 + KT <= all_ve) || c0 + KT <= all_vs)) {
             // hidden keys to -inf, in place
             auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
 #pragma unroll 1
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // scaled to it, and the weights are made again.
           auto weigh = [&](const uint32_t* x, const uint32_t* y, uint32_t to, int half) -> bool {
             for (bool again = false;; again = true) {
-              if (again || __any_sync(0xffffffffu, m == -INFINITY)) {
+              if (again || !begun) {
                 tmem_wait_ld();
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int k = 0; k < 4; ++k)
                     top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[c + k]), __uint_as_float(y[c + k])));
                 const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-                const bool raise = mx > m + kRaise;
+                const bool raise = active && mx > m + kRaise;
                 const bool rescale = raise && m != -INFINITY;
                 if (__any_sync(0xffffffffu, rescale)) {
                   // O holds earlier keys: their products have to be done before this warp's rows are scaled
@@ -556,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_wait_st();
                 }
                 if (raise) m = mx;
+                begun = __all_sync(0xffffffffu, m != -INFINITY || !active);
               }
               // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
               const float neg = m == -INFINITY ? 0.f : -m;
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               part(y, to + 16);
               sum0 = __fadd2_rn(sum0, sum1);
               const float sum = sum0.x + sum0.y;
-              if (again || !__any_sync(0xffffffffu, !(sum < kMost))) {
+              if (again || !__any_sync(0xffffffffu, active && !(sum < kMost))) {
                 l += sum;
                 break;
               }
