@@ -34,15 +34,18 @@ struct Run {
   long long per, x0, x1;  // a run's length; this CTA's
   int b;                  // the sequence that it starts in, and the cost before that
   long long base;
+  int start, n, P;        // first token, tokens, and tokens before them, of that sequence
 };
-// The whole block; false in every thread where the run is empty.  THREADS = blockDim.x.
+// The whole block; false in every thread where the run is empty.  THREADS = blockDim.x.  What up to THREADS sequences need is
+// asked for at once: a short call is a chain of such latencies.
 template <int THREADS>
-__device__ __forceinline__ bool find_run(const long long* cost, int B, int Hkv, int least, Run& r) {
+__device__ __forceinline__ bool find_run(const WinAttnArgs& a, const long long* cost, int least, Run& r) {
   constexpr int W = THREADS / 32;
-  __shared__ long long part[W], s_base;
-  __shared__ int s_b;
+  __shared__ long long part[2][W];
+  __shared__ Run found;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   // sum over the block; upto: over the threads before this one and it
+  int turn = 0;
   auto scan = [&](long long x, long long& upto) -> long long {
     upto = x;
 #pragma unroll
@@ -50,36 +53,54 @@ __device__ __forceinline__ bool find_run(const long long* cost, int B, int Hkv, 
       const long long y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    __syncthreads();
-    if (lane == 31) part[warp] = upto;
+    if (lane == 31) part[turn][warp] = upto;
     __syncthreads();
     long long all = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      if (w < warp) upto += part[w];
-      all += part[w];
+      if (w < warp) upto += part[turn][w];
+      all += part[turn][w];
     }
+    turn ^= 1;
     return all;
   };
+  auto tokens_of = [&](int b, int& start, int& n, int& P) {
+    start = a.cu != nullptr ? a.cu[b] : b;
+    n = (a.cu != nullptr ? a.cu[b + 1] : b + 1) - start;
+    P = a.prefix_len[b];
+  };
+  const bool few = a.B <= THREADS;
   long long mine = 0, upto;
-  for (int b = tid; b < B; b += THREADS) mine += cost[b];
-  const long long total = scan(mine, upto) * Hkv;
+  int start = 0, n = 0, P = 0;
+  for (int b = tid; b < a.B; b += THREADS) {
+    mine += cost[b] * a.Hkv;
+    if (few) tokens_of(b, start, n, P);
+  }
+  const long long total = scan(mine, upto);
   r.per = (total + gridDim.x - 1) / gridDim.x;
   if (r.per < least) r.per = least;
   r.x0 = blockIdx.x * r.per, r.x1 = min(total, r.x0 + r.per);
   if (r.x0 >= r.x1) return false;
   r.base = 0;
   for (int b0 = 0;; b0 += THREADS) {
-    const long long own = b0 + tid < B ? cost[b0 + tid] * Hkv : 0;
-    const long long here = scan(own, upto);
+    long long own = mine, here = total;
+    if (!few) {
+      own = b0 + tid < a.B ? cost[b0 + tid] * a.Hkv : 0;
+      here = scan(own, upto);
+    }
     if (r.base + here > r.x0) {
-      if (r.base + upto - own <= r.x0 && r.base + upto > r.x0) s_b = b0 + tid, s_base = r.base + upto - own;
+      if (r.base + upto - own <= r.x0 && r.base + upto > r.x0) {
+        if (!few) tokens_of(b0 + tid, start, n, P);
+        found.b = b0 + tid, found.base = r.base + upto - own;
+        found.start = start, found.n = n, found.P = P;
+      }
       break;
     }
     r.base += here;
   }
   __syncthreads();
-  r.b = s_b, r.base = s_base;
+  r.b = found.b, r.base = found.base;
+  r.start = found.start, r.n = found.n, r.P = found.P;
   return true;
 }
 

@@ -78,12 +78,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
   const int G = a.Hq / a.Hkv;
 
   Run run;
-  if (!find_run<kThreads>(cost, a.B, a.Hkv, kLeast, run)) return;
-  int b = run.b;
+  if (!find_run<kThreads>(a, cost, kLeast, run)) return;
+  int b = run.b, start = run.start;
   long long base = run.base;
   const long long per = run.per, x0 = run.x0, x1 = run.x1;
-  auto seen = [&]() { return seen_by(a, a.prefix_len[b], a.cu != nullptr ? a.cu[b + 1] - a.cu[b] : 1); };
-  Seen q = seen();
+  Seen q = seen_by(a, run.P, run.n);
 
   const float scale = a.sm_scale * 1.4426950408889634f;
   const uint32_t my_ring = smem_addr(ring) + warp * (S::kStages * 2 * S::kPage);
@@ -91,23 +90,21 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
     if (x - base >= (long long)q.pages * a.Hkv) {
       base += (long long)q.pages * a.Hkv;
       while (cost[++b] == 0) {}
-      q = seen();
+      start = a.cu != nullptr ? a.cu[b] : b;
+      q = seen_by(a, a.prefix_len[b], a.cu != nullptr ? a.cu[b + 1] - start : 1);
     }
     const int kvh = (int)((x - base) / q.pages);
     const long long u0 = base + (long long)kvh * q.pages, u1 = u0 + q.pages;
     const int p0 = (int)(x - u0), p1 = (int)(min(x1, u1) - u0);
     const int R = q.n * G;
-    const int start = a.cu != nullptr ? a.cu[b] : b;
     const int32_t* table = a.block_table + (long long)b * a.max_blocks;
 
-    __syncthreads();  // the last unit's outputs have left shared memory
+    if (x != x0) __syncthreads();  // the last unit's outputs have left shared memory
+    // the queries, zeros in place of rows past the last: in the first group of copies
     for (int i = tid; i < MT * 16 * CH; i += kThreads) {
       const int r = i / CH, c = i % CH;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < R)
-        v = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (long long)(start + r / G) * a.q_stride +
-                                            (long long)(kvh * G + r % G) * HD + c * 8);
-      *reinterpret_cast<uint4*>(sQ + chunk_at<HD>(r, c)) = v;
+      const long long at = r < R ? (long long)(start + r / G) * a.q_stride + (long long)(kvh * G + r % G) * HD + c * 8 : 0;
+      copy16(smem_addr(sQ) + chunk_at<HD>(r, c), static_cast<const bf16*>(a.q) + at, r < R);
     }
 
     const int last = q.P + q.n - 1;
@@ -139,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
     };
 #pragma unroll
     for (int k = 0; k < S::kStages - 1; ++k) issue(k);
+    cp_async_wait<S::kStages - 2>();
     __syncthreads();
 
     // a thread's rows are lane / 4 and lane / 4 + 8 of each tile of 16
@@ -305,23 +303,41 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
       }
     }
     if (!alone) {
-      __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(arrived + (long long)b * a.Hkv + kvh, 1) == (int)(c1 - c0);
+      if (tid == 0) {
+        __threadfence();
+        s_last = atomicAdd(arrived + (long long)b * a.Hkv + kvh, 1) == (int)(c1 - c0);
+      }
       __syncthreads();
       if (s_last) {
         __threadfence();
+        // twelve parts at a time: their loads do not wait for one another
+        constexpr int kBatch = 12;
+        const int parts = (int)(c1 - c0) + 1;
         for (int i = tid; i < R * (HD / 4); i += kThreads) {
           const int r = i / (HD / 4), c = i % (HD / 4) * 4;
           float top = -INFINITY, sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-          for (long long k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(slot_of(k) + MT * 16 * HD + r * 2));
-          for (long long k = c0; k <= c1; ++k) {
-            const float* slot = slot_of(k);
-            const float2 w = __ldcg(reinterpret_cast<const float2*>(slot + MT * 16 * HD + r * 2));
-            const float f = w.x == -INFINITY ? 0.f : ex2(w.x - top);
-            sum += f * w.y;
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(slot + r * HD + c));
-            v[0] += f * y.x, v[1] += f * y.y, v[2] += f * y.z, v[3] += f * y.w;
+          for (int k = 0; k < parts; k += kBatch) {
+            float2 w[kBatch];
+            float4 y[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const float* slot = slot_of(c0 + min(k + j, parts - 1));
+              w[j] = __ldcg(reinterpret_cast<const float2*>(slot + MT * 16 * HD + r * 2));
+              y[j] = __ldcg(reinterpret_cast<const float4*>(slot + r * HD + c));
+            }
+            float to = top;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) to = fmaxf(to, w[j].x);
+            const float f0 = top == -INFINITY ? 0.f : ex2(top - to);
+            top = to;
+            sum *= f0, v[0] *= f0, v[1] *= f0, v[2] *= f0, v[3] *= f0;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const float f = k + j >= parts || w[j].x == -INFINITY ? 0.f : ex2(w[j].x - to);
+              sum += f * w[j].y;
+              v[0] += f * y[j].x, v[1] += f * y[j].y, v[2] += f * y[j].z, v[3] += f * y[j].w;
+            }
           }
           const float inv = 1.f / sum;
           v[0] *= inv, v[1] *= inv, v[2] *= inv, v[3] *= inv;

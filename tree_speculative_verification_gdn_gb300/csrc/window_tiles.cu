@@ -192,7 +192,7 @@ struct Walk {
   __device__ Walk(const WinAttnArgs& a_, const long long* cost_, const Run& run_, TileShape s)
       : a(a_), cost(cost_), run(run_), shape(s) {
     u.b = run.b;
-    sequence();
+    start = run.start, n = run.n, P = run.P, t = 0;
     const long long c = cost[u.b];
     u.kvh = (int)((run.x0 - run.base) / c);
     u0 = run.base + u.kvh * c;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = a.Hq / a.Hkv;
 
   Run run;
-  if (!find_run<kThreads>(cost, a.B, a.Hkv, kLeast, run)) return;
+  if (!find_run<kThreads>(a, cost, kLeast, run)) return;
   if (tid == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_free, 1);
