@@ -501,12 +501,39 @@ def _scratch(size: int, device, stream):
         return torch.empty(size, dtype=torch.uint8, device=device)
 
 
-def _here(*tensors) -> None:
-    """The calls launch on the current device's stream: tensors of another device are refused."""
-    device = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else -1
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != device:
-            raise ValueError(f"a tensor on {t.device} was passed while cuda:{device} is the current device")
+def _dense(t, shape, dtype, device: int, name: str):
+    """Pointer of a dense tensor on the current device (the calls launch on its stream)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse_here(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _heads(t, shape, dtype, device: int, row: int, name: str):
+    """Pointer and token stride of [tokens, heads, hd] on the current device, the tokens' rows dense."""
+    if t is None:
+        return None, row
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+        _refuse_here(name, t, shape, dtype, device)
+    stride = t.stride()
+    if stride[2] != 1 or stride[1] != shape[2]:
+        return _rows(name, t, shape, dtype, row)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else row
+
+
+def _refuse_here(name: str, t, shape, dtype, device: int):
+    if t.is_cuda and t.get_device() != device:
+        raise ValueError(f"{name} lies on {t.device} while cuda:{device} is the current device")
+    if t.shape == shape and t.dtype == dtype and t.is_cuda:
+        raise ValueError(f"{name}: tensors passed to the library must be contiguous")
+    _refuse(name, t, shape, dtype)
+
+
+def _current(t, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors passed to the library must be CUDA tensors")
+    return torch.cuda.current_device()
 
 
 def tv_qk_norm_rope(q, k, q_out, prefix_len, err, *, k_out=None, v=None, k_cache=None, v_cache=None, block_table=None,
@@ -518,32 +545,34 @@ def tv_qk_norm_rope(q, k, q_out, prefix_len, err, *, k_out=None, v=None, k_cache
     ``k_out`` and, with v as it is, to the paged ``k_cache``, ``v_cache`` [num_blocks, Hkv, 16, hd] through
     ``block_table`` [B, max_blocks].  Sequences are packed by ``cu_seqlens`` [B + 1], or one token each without it.
     Token strides are free.  ``prefix_len`` may be None (zero) without a cache; ``live`` [B] skips rows."""
-    T, Hq, hd = q.shape
+    shape, io, device, whole = q.shape, q.dtype, _current(q, "q"), torch.int32
+    T, Hq, hd = shape
     Hkv = k.shape[1]
     B = T if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    io, keys = q.dtype, (T, Hkv, hd)
     if io not in _DTYPES:
-        _refuse("q", q, q.shape, "float32 or bfloat16")
-    _here(q, k, q_out, err, k_out, v, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, q_weight, k_weight)
-    pq, sq = _rows("q", q, q.shape, io, Hq * hd)
-    pk, sk = _rows("k", k, keys, io, Hkv * hd)
-    pqo, sqo = _rows("q_out", q_out, q.shape, io, Hq * hd)
-    pko, sko = _rows("k_out", k_out, keys, io, Hkv * hd)
+        _refuse("q", q, shape, "float32 or bfloat16")
+    keys = (T, Hkv, hd)
+    pq, sq = _heads(q, shape, io, device, Hq * hd, "q")
+    pk, sk = _heads(k, keys, io, device, Hkv * hd, "k")
+    pqo, sqo = _heads(q_out, shape, io, device, Hq * hd, "q_out")
+    pko, sko = _heads(k_out, keys, io, device, Hkv * hd, "k_out")
     pv, sv, pkc, pvc, ptab, blocks, most, bs = None, Hkv * hd, None, None, None, 0, 0, 0
     if k_cache is not None or v_cache is not None:
         if k_cache is None or v_cache is None or v is None or block_table is None:
             raise ValueError("k_cache, v_cache, v and block_table go together")
-        blocks, bs, most = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+        blocks, _, bs, _ = k_cache.shape
+        most = block_table.shape[1]
         cache = (blocks, Hkv, bs, hd)
-        pv, sv = _rows("v", v, keys, io, Hkv * hd)
-        pkc, pvc = _whole("k_cache", k_cache, cache, torch.bfloat16), _whole("v_cache", v_cache, cache, torch.bfloat16)
-        ptab = _whole("block_table", block_table, (B, most), torch.int32)
+        pv, sv = _heads(v, keys, io, device, Hkv * hd, "v")
+        pkc = _dense(k_cache, cache, torch.bfloat16, device, "k_cache")
+        pvc = _dense(v_cache, cache, torch.bfloat16, device, "v_cache")
+        ptab = _dense(block_table, (B, most), whole, device, "block_table")
     _check(lib.tv_qk_norm_rope(
-        pq, sq, pk, sk, pv, sv, _whole("q_weight", q_weight, (hd,), io), _whole("k_weight", k_weight, (hd,), io),
-        _whole("cu_seqlens", cu_seqlens, (B + 1,), torch.int32), _whole("prefix_len", prefix_len, (B,), torch.int32),
-        _whole("live", live, (B,), torch.int32), B, T, Hq, Hkv, hd, hd if rotary_dim is None else rotary_dim, _DTYPES[io],
-        int(norm), eps, weight_offset, rope_theta, pqo, sqo, pko, sko, pkc, pvc, blocks, ptab, most, bs,
-        _whole("err", err, (B,), torch.int32), _stream(stream)), "tv_qk_norm_rope")
+        pq, sq, pk, sk, pv, sv, _dense(q_weight, (hd,), io, device, "q_weight"),
+        _dense(k_weight, (hd,), io, device, "k_weight"), _dense(cu_seqlens, (B + 1,), whole, device, "cu_seqlens"),
+        _dense(prefix_len, (B,), whole, device, "prefix_len"), _dense(live, (B,), whole, device, "live"), B, T, Hq, Hkv, hd,
+        hd if rotary_dim is None else rotary_dim, _DTYPES[io], norm, eps, weight_offset, rope_theta, pqo, sqo, pko, sko, pkc,
+        pvc, blocks, ptab, most, bs, _dense(err, (B,), whole, device, "err"), _stream(stream)), "tv_qk_norm_rope")
 
 
 def tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, window: int = 0, sinks: int = 0,
@@ -553,28 +582,30 @@ def tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, window
 
 def _window_attn(name, q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, out, err, window, sinks, max_len,
                  workspace, sm_scale, stream):
+    device, bf, whole = _current(q, "q"), torch.bfloat16, torch.int32
     T, Hq, hd = q.shape
     blocks, Hkv, bs, _ = k_cache.shape
     B, most = block_table.shape
-    bf, cache = torch.bfloat16, (blocks, Hkv, bs, hd)
-    _here(q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, out, err, workspace)
-    pq, sq = _rows("q", q, (T if cu_seqlens is not None else B, Hq, hd), bf, Hq * hd)
-    po, so = _rows("out", out, (T, Hq, hd), bf, Hq * hd)
+    cache = (blocks, Hkv, bs, hd)
+    tokens = (T if cu_seqlens is not None else B, Hq, hd)
+    pq, sq = _heads(q, tokens, bf, device, Hq * hd, "q")
+    po, so = _heads(out, tokens, bf, device, Hq * hd, "out")
     if workspace is None:
         size = lib.tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, most, bs, window, sinks)
         workspace = _scratch(size, q.device, stream)
+        room = None if workspace is None else workspace.data_ptr()
     else:
-        size = workspace.numel() * workspace.element_size()
-    head = (pq, sq, _whole("k_cache", k_cache, cache, bf), _whole("v_cache", v_cache, cache, bf), blocks,
-            _whole("block_table", block_table, (B, most), torch.int32), most)
-    prefix = _whole("prefix_len", prefix_len, (B,), torch.int32)
-    tail = (Hq, Hkv, hd, bs, window, sinks, hd ** -0.5 if sm_scale is None else sm_scale, po, so, _ptr(workspace), size,
-            _whole("err", err, (B,), torch.int32), _stream(stream))
+        size, room = workspace.numel() * workspace.element_size(), _ptr(workspace)
+    head = (pq, sq, _dense(k_cache, cache, bf, device, "k_cache"), _dense(v_cache, cache, bf, device, "v_cache"), blocks,
+            _dense(block_table, (B, most), whole, device, "block_table"), most)
+    prefix = _dense(prefix_len, (B,), whole, device, "prefix_len")
+    tail = (Hq, Hkv, hd, bs, window, sinks, hd ** -0.5 if sm_scale is None else sm_scale, po, so, room, size,
+            _dense(err, (B,), whole, device, "err"), _stream(stream))
     if cu_seqlens is not None:
-        _check(lib.tv_window_attn_prompt(*head, _whole("cu_seqlens", cu_seqlens, (B + 1,), torch.int32), prefix, B, T,
+        _check(lib.tv_window_attn_prompt(*head, _dense(cu_seqlens, (B + 1,), whole, device, "cu_seqlens"), prefix, B, T,
                                          max_len, *tail), name)
     else:
-        _check(lib.tv_window_attn_step(*head, prefix, _whole("live", live, (B,), torch.int32), B, *tail), name)
+        _check(lib.tv_window_attn_step(*head, prefix, _dense(live, (B,), whole, device, "live"), B, *tail), name)
 
 
 def tv_window_attn_prompt(q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, out, err, window: int = 0,
@@ -601,17 +632,17 @@ def tv_accept_sample(parents, draft_tokens, target_probs, draft_probs, uniforms,
     """Acceptance by probabilities: parents, draft_tokens [B, N] int32, target_probs and draft_probs [B, N, V] (fp32 or
     bf16; draft_probs None: the drafted tokens were chosen, not drawn), uniforms [B, N] fp32 in [0, 1) -> accepted_path
     [B, Lmax], accepted_len [B], next_token [B], err [B] (all int32)."""
+    device, io, whole = _current(target_probs, "target_probs"), target_probs.dtype, torch.int32
     B, N, V = target_probs.shape
-    Lmax, io, whole = accepted_path.shape[1], target_probs.dtype, torch.int32
+    Lmax, tree, one = accepted_path.shape[1], (B, N), (B,)
     if io not in _DTYPES:
         _refuse("target_probs", target_probs, target_probs.shape, "float32 or bfloat16")
-    _here(parents, draft_tokens, target_probs, draft_probs, uniforms, accepted_path, accepted_len, next_token, err)
     _check(lib.tv_accept_sample(
-        _whole("parents", parents, (B, N), whole), _whole("draft_tokens", draft_tokens, (B, N), whole),
-        _whole("target_probs", target_probs, (B, N, V), io), _whole("draft_probs", draft_probs, (B, N, V), io),
-        _whole("uniforms", uniforms, (B, N), torch.float32), B, N, V, Lmax, _DTYPES[io],
-        _whole("accepted_path", accepted_path, (B, Lmax), whole), _whole("accepted_len", accepted_len, (B,), whole),
-        _whole("next_token", next_token, (B,), whole), _whole("err", err, (B,), whole), _stream(stream)),
+        _dense(parents, tree, whole, device, "parents"), _dense(draft_tokens, tree, whole, device, "draft_tokens"),
+        _dense(target_probs, (B, N, V), io, device, "target_probs"), _dense(draft_probs, (B, N, V), io, device, "draft_probs"),
+        _dense(uniforms, tree, torch.float32, device, "uniforms"), B, N, V, Lmax, _DTYPES[io],
+        _dense(accepted_path, (B, Lmax), whole, device, "accepted_path"), _dense(accepted_len, one, whole, device, "accepted_len"),
+        _dense(next_token, one, whole, device, "next_token"), _dense(err, one, whole, device, "err"), _stream(stream)),
         "tv_accept_sample")
 
 

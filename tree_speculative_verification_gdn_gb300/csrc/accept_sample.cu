@@ -9,9 +9,9 @@
 // sums by exact additions, about 2^-46), joined in doubles; a double per element would cost more than the row's bytes:
 // this chip adds two doubles a clock on an SM.
 //
-// A cluster of eight CTAs takes a sequence, each the eighth part of a row, each of its 16 warps a run of that part.  Every
-// CTA walks the tree by itself on the same sums.  The draw finds the warp's run from the 128 sums, and that warp
-// walks its run again, which lies in L2.  Bound by the latency of a pass where sequences are few, by HBM otherwise.
+// A cluster of up to eight CTAs takes a sequence, each an equal part of a row, each of its 16 warps a run of that part.
+// Every CTA walks the tree by itself on the same sums.  The draw finds the warp's run from the runs' sums, and its
+// CTA cuts that again, which lies in L2.  Bound by the latency of a pass where sequences are few, by HBM otherwise.
 #include "tv_common.cuh"
 #include "tv_internal.h"
 #include "tv_tc.cuh"
@@ -19,9 +19,7 @@
 namespace tv {
 namespace {
 
-constexpr int kParts = 8;
 constexpr int kWarps = 16;
-constexpr int kRuns = kParts * kWarps;
 
 // hi + lo, lo far below hi
 struct Pair {
@@ -51,11 +49,17 @@ __device__ __forceinline__ double warp_sum(double x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+__device__ __forceinline__ Pair warp_sum(Pair x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
+  return x;
+}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_st_f64(uint32_t caddr, double v) {
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(caddr), "d"(v) : "memory");
+__device__ __forceinline__ void cluster_st_pair(uint32_t caddr, Pair v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(caddr), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
 template <typename T>
@@ -76,12 +80,27 @@ struct Rows {  // rows p and q of a node, in vectors of 16 bytes from the bounda
   }
 };
 
-template <typename T>
-__global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32) accept_sample_kernel(SampleArgs a) {
+// What the walk, one warp's, asks of the others.
+struct Ask {
+  int node;
+  Pair A;
+  int refused;  // tokens left out
+  int draw;     // 0: another pass; 1: the draw, from the last pass's sums; < 0: a status to report
+  int run;      // the draw's run; the sum in front of it, and the number to pass (none: the last token with any)
+  double ahead, want;
+  int found;
+};
+
+// kParts CTAs a sequence.  All doubles are one warp's: sixteen warps' would take longer than the row.
+template <typename T, int kParts>
+__global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2) accept_sample_kernel(SampleArgs a) {
   constexpr int VE = Rows<T>::VE;
+  constexpr int kRuns = kParts * kWarps;
+  constexpr int kOwn = kRuns >= 32 ? kRuns / 32 : 1;  // sums of a lane of the walk's warp; the upper lanes may have none
   __shared__ int par[TV_MAX_NODES], tok[TV_MAX_NODES], path[TV_MAX_NODES], refused[TV_MAX_NODES];
   __shared__ float u[TV_MAX_NODES], pt[TV_MAX_NODES], qt[TV_MAX_NODES];
-  __shared__ double sums[2][kRuns];
+  __shared__ Pair sums[2][kRuns];
+  __shared__ Ask ask;
   const int b = blockIdx.x / kParts, rank = (int)cluster_ctarank();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int N = a.N, V = a.V;
@@ -100,205 +119,300 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32) ac
   }
   bad = __syncthreads_or(bad);
   cluster_wait();
-  auto fail = [&](int st) {
-    if (rank != 0) return;
-    for (int r = tid; r < a.Lmax; r += blockDim.x) a.path[(long long)b * a.Lmax + r] = -1;
-    if (tid == 0) a.len[b] = 0, a.next_token[b] = -1, a.err[b] = st;
-  };
-  if (bad) return fail(TV_ERR_BAD_TREE);
 
-  int parity = 0;
-  int count_refused = 0;  // tokens left out of p (q not known)
+  // The walk: the whole of warp 0 keeps the same state.
+  int node = 0, count = 1, at = 0;     // at: the last child looked at
+  int left_out = 0, parity = 0;
+  double A = 0.0, mass = 1.0;
+  bool have = false;  // mass is the sum of the last pass
+  if (tid == 0) path[0] = 0;
+  // On to the next pass, or to the draw.
+  auto walk = [&]() {
+    while (count < a.Lmax) {
+      int went = -1;
+      for (int base = (at + 1) & ~31; base < N && went < 0; base += 32) {
+        unsigned kids = __ballot_sync(0xffffffffu, base + lane < N && base + lane > at && par[base + lane] == node);
+        while (kids != 0) {
+          const int c = base + __ffs(kids) - 1;
+          kids &= kids - 1;
+          if (draft != nullptr) {
+            if ((double)u[c] * (double)qt[c] * mass < fmax((double)pt[c] - A * (double)qt[c], 0.0)) {
+              went = c;
+              break;
+            }
+            at = c;
+            A += mass;
+            ask.draw = 0;
+            return;  // for the sum of what is left
+          }
+          bool twice = false;
+          for (int k = lane; k < left_out; k += 32) twice |= refused[k] == tok[c];
+          const double rx = __any_sync(0xffffffffu, twice) ? 0.0 : (double)pt[c];
+          if ((double)u[c] * mass < rx) {
+            went = c;
+            break;
+          }
+          mass -= rx;
+          if (lane == 0) refused[left_out] = tok[c];
+          __syncwarp();
+          ++left_out;
+        }
+      }
+      if (went < 0) break;
+      node = at = went;
+      if (lane == 0) path[count] = node;
+      ++count;
+      A = 0.0, mass = 1.0, have = false, left_out = 0;
+    }
+    ask.draw = have ? 1 : 0;
+    at = N;  // no child is left to look at
+  };
+  // With the last pass's sums: goes on, or finds the run that the drawn token lies in.
+  auto take = [&]() {
+    double own[kOwn], before = 0.0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) before += own[k] = lane * kOwn + k < kRuns ? whole(sums[parity][lane * kOwn + k]) : 0.0;
+    mass = warp_sum(before);
+    have = true;
+    if (!(mass > 0.0)) {
+      if (at < N) {  // nothing is left: the next child is held against p again
+        A = 0.0, mass = 1.0, have = false;
+      } else if (A != 0.0 || left_out != 0) {
+        A = 0.0, left_out = 0;
+        ask.draw = 0;
+        return;
+      } else {
+        ask.draw = TV_ERR_BAD_PROBS;
+        return;
+      }
+    }
+    if (at < N) walk();
+    if (ask.draw == 0) {
+      if (at < N || !have) return;
+      ask.draw = 1;
+    }
+    const double want = (double)u[0] * mass, all = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    double upto = before - all, ahead = 0.0;  // of the runs in front of this lane's
+    int run = kRuns, last = -1;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      if (own[k] > 0.0) last = lane * kOwn + k;
+      if (run == kRuns && own[k] > 0.0 && upto + own[k] > want) run = lane * kOwn + k, ahead = upto;
+      upto += own[k];
+    }
+    const unsigned found = __ballot_sync(0xffffffffu, run < kRuns);
+    if (found != 0) {
+      run = __shfl_sync(0xffffffffu, run, __ffs(found) - 1);
+      ahead = __shfl_sync(0xffffffffu, ahead, __ffs(found) - 1);
+    } else {  // rounding, or a number past 1: the last token with a probability
+      run = __reduce_max_sync(0xffffffffu, last);
+    }
+    ask.run = run, ask.ahead = ahead, ask.want = want, ask.found = found != 0;
+  };
+  auto tell = [&]() {
+    ask.node = node, ask.refused = left_out;
+    ask.A = Pair{(float)A, (float)(A - (double)(float)A)};
+  };
+
   Rows<T> r;
   r.V = V;
   int v0 = 0, v1 = 0;  // this warp's run of vectors
-  auto rows_of = [&](int node) {
-    r.p = target + (long long)node * V;
-    r.q = draft != nullptr ? draft + (long long)node * V : nullptr;
+  bool some = false;   // it holds a token that was left out of p
+  Pair Ap{0.f, 0.f};
+  bool use_q = false;
+  auto listen = [&]() {
+    r.p = target + (long long)ask.node * V;
+    r.q = draft != nullptr ? draft + (long long)ask.node * V : nullptr;
     r.phase = (int)((reinterpret_cast<uintptr_t>(r.p) & 15u) / sizeof(T));
     const int vecs = (V + r.phase + VE - 1) / VE;
     const int per = ((vecs + kParts - 1) / kParts + kWarps - 1) / kWarps;
     v0 = min((rank * kWarps + warp) * per, vecs), v1 = min(v0 + per, vecs);
-  };
-  // whether this warp's run holds a token that was left out of p
-  auto any_refused = [&]() -> bool {
     bool in = false;
-    for (int k = lane; k < count_refused; k += 32) {
-      const int at = refused[k] + r.phase;
-      in |= at >= v0 * VE && at < v1 * VE;
+    for (int k = lane; k < ask.refused; k += 32) {
+      const int e = refused[k] + r.phase;
+      in |= e >= v0 * VE && e < v1 * VE;
     }
-    return __any_sync(0xffffffffu, in);
+    some = __any_sync(0xffffffffu, in);
+    Ap = ask.A;
+    use_q = Ap.hi != 0.f;
   };
   // R of vector j, as pairs
-  auto left = [&](int j, Pair A, bool use_q, bool some, Pair* x) {
+  auto left = [&](int j, Pair* x) {
     const int e = j * VE - r.phase;
     float p[VE], q[VE];
     Rows<T>::vector(r.p, e, V, p);
     if (use_q) Rows<T>::vector(r.q, e, V, q);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = use_q ? left_of(p[i], q[i], A) : Pair{p[i], 0.f};
-    for (int k = 0; some && k < count_refused; ++k) {
+    for (int i = 0; i < VE; ++i) x[i] = use_q ? left_of(p[i], q[i], Ap) : Pair{p[i], 0.f};
+    for (int k = 0; some && k < ask.refused; ++k) {
       const int at = refused[k] - e;
 #pragma unroll
       for (int i = 0; i < VE; ++i)
         if (i == at) x[i] = Pair{0.f, 0.f};
     }
   };
-  // sum R; every run's own sum in sums[parity]
-  auto pass = [&](double Ad) -> double {
-    const Pair A{(float)Ad, (float)(Ad - (double)(float)Ad)};
-    const bool use_q = Ad != 0.0, some = any_refused();
+
+  if (warp == 0) {
+    if (bad) {
+      ask.draw = TV_ERR_BAD_TREE;
+    } else {
+      walk();
+      tell();
+    }
+  }
+  __syncthreads();
+  // Every CTA of the cluster makes the same passes, on the same sums.
+  while (ask.draw == 0) {
+    listen();
     Pair acc{0.f, 0.f};
 #pragma unroll 4
     for (int j = v0 + lane; j < v1; j += 32) {
       Pair x[VE];
-      left(j, A, use_q, some, x);
+      left(j, x);
 #pragma unroll
       for (int i = 0; i < VE; ++i) add(acc, x[i]);
     }
-    const double run = warp_sum(whole(acc));
+    acc = warp_sum(acc);
     parity ^= 1;
-    if (lane < kParts) cluster_st_f64(cluster_map(smem_addr(&sums[parity][rank * kWarps + warp]), lane), run);
+    if (lane < kParts) cluster_st_pair(cluster_map(smem_addr(&sums[parity][rank * kWarps + warp]), lane), acc);
     cluster_sync();
-    double m = 0.0;
-#pragma unroll
-    for (int k = 0; k < kRuns / 32; ++k) m += sums[parity][lane * (kRuns / 32) + k];
-    return warp_sum(m);
-  };
-
-  int node = 0, count = 1;
-  if (tid == 0) path[0] = 0;
-  double A = 0.0, mass = 1.0;  // of the tokens refused at this node
-  bool have = false;           // mass is the last pass's sum of R
-  rows_of(0);
-  while (count < a.Lmax) {
-    int went = -1;
-    for (int base = (node + 1) & ~31; base < N && went < 0; base += 32) {
-      unsigned kids = __ballot_sync(0xffffffffu, base + lane < N && base + lane > node && par[base + lane] == node);
-      while (kids != 0 && went < 0) {
-        const int c = base + __ffs(kids) - 1;
-        kids &= kids - 1;
-        if (draft != nullptr) {
-          const double rx = fmax((double)pt[c] - A * (double)qt[c], 0.0);
-          if ((double)u[c] * (double)qt[c] * mass < rx) {
-            went = c;
-          } else {
-            A += mass;
-            mass = pass(A);
-            have = true;
-            if (!(mass > 0.0)) A = 0.0, mass = 1.0, have = false;
-          }
-        } else {
-          double rx = (double)pt[c];
-          for (int k = 0; k < count_refused; ++k)
-            if (refused[k] == tok[c]) rx = 0.0;
-          if ((double)u[c] * mass < rx) {
-            went = c;
-          } else {
-            mass -= rx;
-            __syncthreads();  // every thread is done with the list
-            if (tid == 0) refused[count_refused] = tok[c];
-            __syncthreads();
-            ++count_refused;
-          }
-        }
-      }
+    if (warp == 0) {
+      take();
+      tell();
     }
-    if (went < 0) break;
-    node = went;
-    if (tid == 0) path[count] = node;
-    ++count;
-    A = 0.0, mass = 1.0, have = false, count_refused = 0;
-    rows_of(node);
+    __syncthreads();
   }
-  // the token after the accepted ones
-  if (!have) mass = pass(A);
-  if (!(mass > 0.0) && (A != 0.0 || count_refused != 0)) {
-    A = 0.0, count_refused = 0;
-    mass = pass(A);
+  if (ask.draw < 0) {
+    if (rank == 0) {
+      for (int i = tid; i < a.Lmax; i += blockDim.x) a.path[(long long)b * a.Lmax + i] = -1;
+      if (tid == 0) a.len[b] = 0, a.next_token[b] = -1, a.err[b] = ask.draw;
+    }
+    return;
   }
-  if (!(mass > 0.0)) return fail(TV_ERR_BAD_PROBS);
-  const double want = (double)u[0] * mass;
-  double mine[kRuns / 32], before = 0.0;
+  if (rank == 0 && warp == 0) {
+    for (int i = lane; i < a.Lmax; i += 32) a.path[(long long)b * a.Lmax + i] = i < count ? path[i] : -1;
+    if (lane == 0) a.len[b] = count, a.err[b] = 0;
+  }
+  // The drawn token: the run's CTA cuts it among its warps in turn, and finds the warp whose part passes the number.
+  if (ask.run / kWarps != rank) return;
+  listen();
+  {
+    const int vecs = (V + r.phase + VE - 1) / VE;
+    const int per = ((vecs + kParts - 1) / kParts + kWarps - 1) / kWarps, cut = (per + kWarps - 1) / kWarps;
+    const int r0 = min(ask.run * per, vecs), r1 = min(r0 + per, vecs);
+    v0 = min(r0 + warp * cut, r1), v1 = min(v0 + cut, r1);
+    some = ask.refused > 0;
+  }
+  __shared__ Pair parts[kWarps];
+  Pair acc{0.f, 0.f};
+  for (int j = v0 + lane; j < v1; j += 32) {
+    Pair x[VE];
+    left(j, x);
 #pragma unroll
-  for (int k = 0; k < kRuns / 32; ++k) before += mine[k] = sums[parity][lane * (kRuns / 32) + k];
-  const double own_sum = before;
+    for (int i = 0; i < VE; ++i) add(acc, x[i]);
+  }
+  acc = warp_sum(acc);
+  if (lane == 0) parts[warp] = acc;
+  __syncthreads();
+  double ahead = ask.ahead;
+  const double want = ask.want;
+  if (warp == 0) {
+    const double own = lane < kWarps ? whole(parts[lane]) : 0.0;
+    double to = own;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
+    for (int o = 1; o < kWarps; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += y;
+    }
+    const unsigned hits = __ballot_sync(0xffffffffu, ask.found != 0 && own > 0.0 && ahead + to > want);
+    const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+    // no part passes it after all, by rounding: the last token of the last part with any
+    const int part = hits != 0 ? __ffs(hits) - 1 : 31 - __clz((int)any);
+    const double from = ahead + __shfl_sync(0xffffffffu, to - own, part);
+    if (lane == 0) ask.run = part, ask.ahead = from, ask.found = hits != 0;
   }
-  before -= own_sum;  // of the runs in front of this lane's four
-  int run = kRuns, last = -1;
-  double ahead = 0.0, upto = before;
+  __syncthreads();
+  if (ask.run != warp) return;
+  ahead = ask.ahead;
+  // Four steps of 32 vectors at a time, so that their loads are under way together; the step that passes the number from
+  // its lanes' sums, then the lane and the element.
+  int token = -1, last_token = -1;
+  for (int j0 = v0; j0 < v1 && token < 0; j0 += 128) {
+    Pair sum[4];
 #pragma unroll
-  for (int k = 0; k < kRuns / 32; ++k) {
-    if (mine[k] > 0.0) last = lane * (kRuns / 32) + k;
-    if (run == kRuns && mine[k] > 0.0 && upto + mine[k] > want) run = lane * (kRuns / 32) + k, ahead = upto;
-    upto += mine[k];
-  }
-  const unsigned found = __ballot_sync(0xffffffffu, run < kRuns);
-  if (found != 0) {
-    run = __shfl_sync(0xffffffffu, run, __ffs(found) - 1);
-    ahead = __shfl_sync(0xffffffffu, ahead, __ffs(found) - 1);
-  } else {  // rounding, or a number past 1: the last token with a probability
-    run = __reduce_max_sync(0xffffffffu, last);
-    ahead = 0.0;
-  }
-  if (run == rank * kWarps + warp) {
-    const Pair Ap{(float)A, (float)(A - (double)(float)A)};
-    const bool some = any_refused();
-    int token = -1, last_token = -1;
-    for (int j0 = v0; j0 < v1 && token < 0; j0 += 32) {
-      const int j = j0 + lane;
+    for (int s = 0; s < 4; ++s) {
+      const int j = j0 + s * 32 + lane;
       Pair x[VE];
 #pragma unroll
       for (int i = 0; i < VE; ++i) x[i] = Pair{0.f, 0.f};
-      if (j < v1) left(j, Ap, A != 0.0, some, x);
-      double sum = 0.0;
+      if (j < v1) left(j, x);
+      sum[s] = Pair{0.f, 0.f};
       int positive = -1;
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        sum += whole(x[i]);
         if (x[i].hi > 0.f || x[i].lo > 0.f) positive = j * VE - r.phase + i;
+        add(sum[s], x[i]);
       }
-      double to = sum;
+      last_token = max(last_token, __reduce_max_sync(0xffffffffu, positive));
+    }
+    if (ask.found == 0) continue;
+#pragma unroll 1
+    for (int s = 0; s < 4 && token < 0; ++s) {
+      const double own = whole(s == 0 ? sum[0] : s == 1 ? sum[1] : s == 2 ? sum[2] : sum[3]);
+      double to = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double y = __shfl_up_sync(0xffffffffu, to, o);
         if (lane >= o) to += y;
       }
-      const double from = ahead + (to - sum);
-      int hit = -1;
-      if (found != 0) {
-        double run_sum = from;
+      if (__any_sync(0xffffffffu, ahead + to > want)) {
+        const int j = j0 + s * 32 + lane;
+        Pair x[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) x[i] = Pair{0.f, 0.f};
+        if (j < v1) left(j, x);
+        double run_sum = ahead + (to - own);
+        int hit = -1;
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
           const double v = whole(x[i]);
           run_sum += v;
           if (hit < 0 && v > 0.0 && run_sum > want) hit = j * VE - r.phase + i;
         }
+        const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0);
+        if (hits != 0) token = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
       }
-      const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0);
-      if (hits != 0) token = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
-      last_token = max(last_token, __reduce_max_sync(0xffffffffu, positive));
       ahead += __shfl_sync(0xffffffffu, to, 31);
     }
-    if (lane == 0) a.next_token[b] = token >= 0 ? token : last_token;
   }
-  if (rank == 0) {
-    __syncthreads();
-    for (int i = tid; i < a.Lmax; i += blockDim.x) a.path[(long long)b * a.Lmax + i] = i < count ? path[i] : -1;
-    if (tid == 0) a.len[b] = count, a.err[b] = 0;
-  }
+  if (lane == 0) a.next_token[b] = token >= 0 ? token : last_token;
+}
+
+}  // namespace
+
+namespace {
+
+template <typename T>
+cudaError_t go(const SampleArgs& a, cudaStream_t s) {
+  // As many CTAs a sequence as are resident at once: two on an SM.
+  constexpr int kThreads = kWarps * 32;
+  const int room = 2 * device_sm_count();
+  if (a.B * 8LL <= room) accept_sample_kernel<T, 8><<<a.B * 8, kThreads, 0, s>>>(a);
+  else if (a.B * 4LL <= room) accept_sample_kernel<T, 4><<<a.B * 4, kThreads, 0, s>>>(a);
+  else if (a.B * 2LL <= room) accept_sample_kernel<T, 2><<<a.B * 2, kThreads, 0, s>>>(a);
+  else accept_sample_kernel<T, 1><<<a.B, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_accept_sample(const SampleArgs& a, cudaStream_t s) {
-  if (a.probs == TV_F32) accept_sample_kernel<float><<<a.B * kParts, kWarps * 32, 0, s>>>(a);
-  else accept_sample_kernel<bf16><<<a.B * kParts, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.probs == TV_F32 ? go<float>(a, s) : go<bf16>(a, s);
 }
 
 }  // namespace tv

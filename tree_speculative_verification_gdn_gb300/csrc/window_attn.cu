@@ -13,6 +13,7 @@ namespace {
 // A block a sequence.  shape.tokens = 0: its cost is its pages.
 __global__ void __launch_bounds__(256) window_plan_kernel(WinAttnArgs a, PagedCheck c, TileShape shape,
                                                           long long* __restrict__ cost, int* __restrict__ zeros, int count) {
+  plan_begun();
   const int b = blockIdx.x;
   for (long long i = (long long)b * 256 + threadIdx.x; i < count; i += (long long)a.B * 256) zeros[i] = 0;
   int n;

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kWhole = 16;     // pages of a sequence and head that are never cut
 constexpr int kLeast = 8;      // pages a run, at least: below, joining costs more than the pages
 constexpr float kRaise = 8.f;  // the running maximum is raised only by more than this (log2): sums grow by 2^8 at most
 
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int G = a.Hq / a.Hkv;
 
+  wait_for_plan();
   Run run;
   if (!find_run<kThreads>(a, cost, kLeast, run)) return;
   int b = run.b, start = run.start;
@@ -86,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
 
   const float scale = a.sm_scale * 1.4426950408889634f;
   const uint32_t my_ring = smem_addr(ring) + warp * (S::kStages * 2 * S::kPage);
+  bool used = false;
   for (long long x = x0; x < x1;) {
     if (x - base >= (long long)q.pages * a.Hkv) {
       base += (long long)q.pages * a.Hkv;
@@ -95,11 +98,18 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
     }
     const int kvh = (int)((x - base) / q.pages);
     const long long u0 = base + (long long)kvh * q.pages, u1 = u0 + q.pages;
-    const int p0 = (int)(x - u0), p1 = (int)(min(x1, u1) - u0);
+    // a short unit goes whole to the run that it starts in
+    const bool uncut = q.pages <= kWhole;
+    if (uncut && u0 < x0) {
+      x = u1;
+      continue;
+    }
+    const int p0 = (int)(x - u0), p1 = uncut ? q.pages : (int)(min(x1, u1) - u0);
     const int R = q.n * G;
     const int32_t* table = a.block_table + (long long)b * a.max_blocks;
 
-    if (x != x0) __syncthreads();  // the last unit's outputs have left shared memory
+    if (used) __syncthreads();  // the last unit's outputs have left shared memory
+    used = true;
     // the queries, zeros in place of rows past the last: in the first group of copies
     for (int i = tid; i < MT * 16 * CH; i += kThreads) {
       const int r = i / CH, c = i % CH;
@@ -356,8 +366,7 @@ cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float*
   auto kern = window_rows_kernel<HD, MT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<kSms * per_sm(HD, MT), kThreads, smem, s>>>(a, cost, slots, arrived);
-  return cudaGetLastError();
+  return launch_behind_plan(kern, kSms * per_sm(HD, MT), kThreads, smem, s, a, cost, slots, arrived);
 }
 
 }  // namespace

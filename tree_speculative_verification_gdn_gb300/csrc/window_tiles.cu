@@ -27,6 +27,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kThreads = 352;
 constexpr int kUnits = 4;       // units known ahead
+constexpr int kWhole = 6;       // key tiles of a unit that is never cut: a cut costs about as much
 constexpr int kLeast = 4;       // cost of a run, at least: a unit of two key tiles
 constexpr float kRaise = 8.0f;     // log2
 constexpr float kMost = 65536.f;   // of 64 weights, as sums against the maximum held
@@ -185,9 +186,13 @@ struct Walk {
     u.seen = seen_by(a, P + t, min(shape.tokens, n - t));
     u.token = start + t;
     u.tiles = (u.seen.pages * 16 + shape.keys - 1) / shape.keys;
-    const long long k0 = u0 + kUnitCost;
-    u.first = (int)min((long long)u.tiles, max(0LL, run.x0 - k0));
-    u.last = (int)max(0LL, min((long long)u.tiles, run.x1 - k0));
+    if (u.tiles <= kWhole) {  // to the run that it starts in
+      u.first = 0, u.last = u0 >= run.x0 && u0 < run.x1 ? u.tiles : 0;
+    } else {
+      const long long k0 = u0 + kUnitCost;
+      u.first = (int)min((long long)u.tiles, max(0LL, run.x0 - k0));
+      u.last = (int)max(0LL, min((long long)u.tiles, run.x1 - k0));
+    }
   }
   __device__ Walk(const WinAttnArgs& a_, const long long* cost_, const Run& run_, TileShape s)
       : a(a_), cost(cost_), run(run_), shape(s) {
@@ -258,8 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int G = a.Hq / a.Hkv;
 
-  Run run;
-  if (!find_run<kThreads>(a, cost, kLeast, run)) return;
   if (tid == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_free, 1);
@@ -292,6 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
+  wait_for_plan();
+  Run run;
+  if (!find_run<kThreads>(a, cost, kLeast, run)) {
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+    return;
+  }
   uint32_t k_loads = 0, v_loads = 0, q_loads = 0;  // what the producer has started
   // the k-th unit, once it is known; a warp hands it back when it needs no more of it
   auto known = [&](uint32_t k) -> bool {
@@ -750,8 +760,7 @@ cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float*
   auto kern = window_tiles_kernel<HD>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<kSms, kThreads, smem, s>>>(a, cost, arrived, slots, npt, mQ, mK, mV);
-  return cudaGetLastError();
+  return launch_behind_plan(kern, kSms, kThreads, smem, s, a, cost, arrived, slots, npt, mQ, mK, mV);
 }
 
 }  // namespace
