@@ -9,11 +9,13 @@
 // two bits and what is left, an eighth of a turn at most, goes to sincospi with its 24 bits whole.  They are made once
 // a token, by the threads of its heads, a token ahead of their use.
 //
-// Bound by HBM: q, k and v are read once and written once.  A block walks a run of tokens with the next one's vectors
-// already asked for; its place among the sequences is searched once, then counted on.
+// Bound by HBM: q, k and v are read once and written once.  A block walks a run of tokens, its place among the sequences
+// searched once, then counted on.  A thread's own vectors come through shared memory three tokens ahead, so that what is on
+// its way does not lie in registers; no other thread reads them, and no barrier stands between.
 #include <math.h>
 
 #include "paged_check.cuh"
+#include "tv_async.cuh"
 #include "tv_common.cuh"
 #include "tv_internal.h"
 
@@ -24,46 +26,49 @@ struct Turns {
   unsigned long long f[128];  // turns a position, in 2^-64
 };
 
-template <typename T>
-struct Vectors;  // two vectors of eight columns as they lie in memory
-template <>
-struct Vectors<bf16> {
-  uint4 a, b;
-  __device__ void load(const bf16* p, int second) {
-    a = *reinterpret_cast<const uint4*>(p);
-    b = *reinterpret_cast<const uint4*>(p + second);
-  }
-  __device__ void get(float* x) const { unpack8(a, x), unpack8(b, x + 8); }
-};
-template <>
-struct Vectors<float> {
-  float4 v[4];
-  __device__ void load(const float* p, int second) {
-    v[0] = reinterpret_cast<const float4*>(p)[0], v[1] = reinterpret_cast<const float4*>(p)[1];
-    v[2] = reinterpret_cast<const float4*>(p + second)[0], v[3] = reinterpret_cast<const float4*>(p + second)[1];
-  }
-  __device__ void get(float* x) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
-  }
-};
+constexpr int kAhead = 4;  // tokens of a thread's vectors on their way, the one in work among them
 
-// The sequence of a token, its position and the row of its keys in the cache.
-struct Place {
-  int b, end;        // sequence (-1: before the first, B: past the last), and the token past its last
-  int position;      // valid if go
-  long long row;     // block * Hkv * 16 + position % 16, in rows of hd
-  bool go;
+// Sixteen columns as pairs of neighbours: eight from the first vector, eight from the second.
+struct Columns {
+  float2 x[8];
+};
+__device__ __forceinline__ void widen(uint4 v, float2* o) {
+  o[0] = make_float2(bf16lo(v.x), bf16hi(v.x)), o[1] = make_float2(bf16lo(v.y), bf16hi(v.y));
+  o[2] = make_float2(bf16lo(v.z), bf16hi(v.z)), o[3] = make_float2(bf16lo(v.w), bf16hi(v.w));
+}
+// A thread's vectors lie in shared memory 16 bytes a thread, so that neighbours' accesses meet all banks.
+template <typename T>
+struct Own;
+template <>
+struct Own<bf16> {
+  static constexpr int kParts = 2;  // of 16 bytes
+  __device__ static const bf16* at(const bf16* p, int part, int second) { return p + part * second; }
+  __device__ static void widen16(const uint4* s, int step, Columns& c) { widen(s[0], c.x), widen(s[step], c.x + 4); }
+};
+template <>
+struct Own<float> {
+  static constexpr int kParts = 4;
+  __device__ static const float* at(const float* p, int part, int second) { return p + (part / 2) * second + (part % 2) * 4; }
+  __device__ static void widen16(const uint4* s, int step, Columns& c) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 v = s[k * step];
+      c.x[2 * k] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+      c.x[2 * k + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+  }
 };
 
 // tpb tokens side by side, ipb heads (queries, keys, and with a cache values) of each; per_block tokens a block.
 template <typename T, int HD>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, 2)
     qk_rope_kernel(const __grid_constant__ QkRopeArgs a, const __grid_constant__ Turns turns, int ipb, int tpb,
                    int per_block) {
   constexpr int L = HD / 16;
-  extern __shared__ float2 s_cs[];  // (cos, sin) [2][tpb][rotary / 2]
+  constexpr int kParts = Own<T>::kParts;
+  extern __shared__ uint4 s_own[];  // [kAhead][kParts][threads], then (cos, sin) [2][tpb][rotary / 2]
   const int half = a.rotary / 2;
+  float2* s_cs = reinterpret_cast<float2*>(s_own + kAhead * kParts * blockDim.x);
   const bool cache = a.k_cache != nullptr;
   const int items = a.Hq + (cache ? 2 : 1) * a.Hkv;
   const int u = threadIdx.x / L, l = threadIdx.x % L;
@@ -77,56 +82,86 @@ __global__ void __launch_bounds__(512)
   const int t1 = (int)min((long long)a.T, t0 + per_block);
   if (t0 >= t1) return;
 
-  // columns first .. first + 7 and second further on
+  // columns first .. first + 7, and as many `second` further on
   const bool turns_here = l < a.rotary / 16;
   const int first = turns_here ? 8 * l : a.rotary + 16 * (l - a.rotary / 16);
   const int second = turns_here ? half : 8;
-  const T* x_in = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
+  const T* x_in = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + head * HD + first;
   const long long x_stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
-  const T* weight = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
+  int t = (int)t0 + tl;
 
-  Place at;
-  at.b = -1, at.end = 0, at.go = false;
+  // Copies need no place among the sequences: they go ahead of everything.
+  auto copy = [&](int ahead, int stage) {  // token t + ahead * tpb
+    const long long token = (long long)t + (long long)ahead * tpb;
+    if (mine && token < t1) {
+      const T* p = x_in + token * x_stride;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+        cp_async_16_cg(s_own + (stage * kParts + i) * blockDim.x + threadIdx.x, Own<T>::at(p, i, second));
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) copy(k, k);
+
+  const T* weight = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
+  const bool scaled = a.norm && kind != 2, weighted = scaled && weight != nullptr && mine;
+  uint4 w[kParts];
+  if (weighted)
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) w[i] = *reinterpret_cast<const uint4*>(Own<T>::at(weight + first, i, second));
+
+  // The token's sequence (-1: before the first, B: past the last), the token past its last, what to add to a token's number
+  // for its position; the token's position and block.
+  int b = -1, end = 0, shift = 0, position = 0, block = 0;
+  bool open = false, go = false;  // the sequence's tokens are worked on; this token is
   if (a.cu != nullptr) {
-    if (a.err[0] == TV_ERR_BAD_SEQLEN) return;
+    if (a.err[0] == TV_ERR_BAD_SEQLEN) {
+      cp_async_wait<0>();
+      return;
+    }
     // the sequences that end at or before the block's first token lie behind it
     int n = 0;
     for (int i = threadIdx.x % 32; i <= a.B; i += 32) n += a.cu[i] <= t0;
     n = __reduce_add_sync(0xffffffffu, n);
-    at.b = n - 1;
-    at.end = n <= a.B ? a.cu[n] : 0x7fffffff;
+    b = n - 2;  // find() enters the sequence itself
+    end = n > 0 ? (int)t0 : a.cu[0];
   }
-  auto find = [&](int t) {  // tokens come in ascending order
-    at.go = false;
-    if (t >= t1 || !in) return;
+  auto find = [&](int token) {  // tokens come in ascending order
+    go = false;
+    if (token >= t1 || !in) return;
     if (a.cu != nullptr) {
-      while (at.b < a.B && t >= at.end) {
-        ++at.b;
-        at.end = at.b < a.B ? a.cu[at.b + 1] : 0x7fffffff;
+      while (b < a.B && token >= end) {
+        ++b;
+        end = b < a.B ? a.cu[b + 1] : 0x7fffffff;
+        open = false;
+        if (b >= 0 && b < a.B && token < end) {
+          shift = (a.prefix_len != nullptr ? a.prefix_len[b] : 0) - a.cu[b];
+          open = a.err[b] == 0 && (a.live == nullptr || a.live[b] != 0);
+        }
       }
-      if (at.b < 0 || at.b >= a.B || a.err[at.b] != 0 || (a.live != nullptr && a.live[at.b] == 0)) return;
-      at.position = (a.prefix_len != nullptr ? a.prefix_len[at.b] : 0) + t - a.cu[at.b];
+      if (!open) return;
+      position = token + shift;
     } else {
-      at.b = t;
+      b = token;
       int st = 0;
-      const bool live = a.live == nullptr || a.live[t] != 0;
-      at.position = a.prefix_len != nullptr ? a.prefix_len[t] : 0;
-      if (live && (at.position < 0 || at.position >= (cache ? a.max_blocks * 16 : 0x7fffffff))) st = TV_ERR_CAPACITY;
+      const bool live = a.live == nullptr || a.live[b] != 0;
+      position = a.prefix_len != nullptr ? a.prefix_len[b] : 0;
+      if (live && (position < 0 || position >= (cache ? a.max_blocks * 16 : 0x7fffffff))) st = TV_ERR_CAPACITY;
       if (live && st == 0 && cache &&
-          (unsigned)a.block_table[(long long)t * a.max_blocks + at.position / 16] >= (unsigned)a.num_blocks)
+          (unsigned)a.block_table[(long long)b * a.max_blocks + position / 16] >= (unsigned)a.num_blocks)
         st = TV_ERR_BAD_BLOCK;
-      if (item == 0 && l == 0) a.err[t] = st;
+      if (item == 0 && l == 0) a.err[b] = st;
       if (!live || st != 0) return;
     }
-    if (cache)
-      at.row = (long long)a.block_table[(long long)at.b * a.max_blocks + at.position / 16] * a.Hkv * 16 + at.position % 16;
-    at.go = true;
+    if (cache && kind != 0) block = a.block_table[(long long)b * a.max_blocks + position / 16];
+    go = true;
   };
   auto angles = [&](int buf) {
-    if (!at.go) return;
+    if (!go) return;
     float2* cs = s_cs + (buf * tpb + tl) * half;
     for (int c = (u - tl * ipb) * L + l; c < half; c += ipb * L) {
-      const unsigned long long turn = (unsigned long long)(unsigned)at.position * turns.f[c];
+      const unsigned long long turn = (unsigned long long)(unsigned)position * turns.f[c];
       const unsigned long long quarter = (turn + (1ull << 61)) >> 62;
       const int rest = (int)((long long)(turn - (quarter << 62)) >> 30);  // in 2^-34 of a turn
       float sn, cn;
@@ -138,63 +173,65 @@ __global__ void __launch_bounds__(512)
     }
   };
 
-  Vectors<T> now, next;
-  int t = (int)t0 + tl;
   find(t);
-  if (at.go && mine) now.load(x_in + t * x_stride + head * HD + first, second);
   angles(0);
-  __syncthreads();
-  int buf = 0;
-  for (int base = (int)t0; base < t1; base += tpb, buf ^= 1) {
-    const bool go = at.go && mine;
-    const long long row = at.row;
+  int buf = 0, k = 0;
+  for (int base = (int)t0; base < t1; base += tpb, buf ^= 1, ++k) {
+    const bool now = go && mine;
+    const int at = position, blk = block;
+    __syncthreads();  // this token's angles are there, the last one's are done with
+    copy(kAhead - 1, (k + kAhead - 1) % kAhead);
     find(t + tpb);
-    if (at.go && mine) next.load(x_in + (t + tpb) * x_stride + head * HD + first, second);
     angles(buf ^ 1);
-    float x[16];
-    float sum = 0.f;
-    if (go) {
-      now.get(x);
+    cp_async_wait<kAhead - 1>();
+    Columns c;
+    float2 sum2 = make_float2(0.f, 0.f);
+    if (now) {
+      Own<T>::widen16(s_own + k % kAhead * kParts * blockDim.x + threadIdx.x, blockDim.x, c);
+      if (scaled)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+        for (int i = 0; i < 8; ++i) sum2 = __ffma2_rn(c.x[i], c.x[i], sum2);
     }
-    sum = group_sum<L>(sum);
-    if (go) {
-      if (kind != 2 && a.norm) {
+    const float sum = group_sum<L>(sum2.x + sum2.y);
+    if (now) {
+      if (scaled) {
         const float inv = rsqrtf(sum / HD + a.eps);
+        const float2 inv2 = make_float2(inv, inv);
+        if (weighted) {
+          Columns wc;
+          Own<T>::widen16(w, 1, wc);
+          const float2 offset = make_float2(a.weight_offset, a.weight_offset);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= inv;
-        if (weight != nullptr) {
-          float w[16];
-          load_vec<8>(weight + first, w);
-          load_vec<8>(weight + first + second, w + 8);
+          for (int i = 0; i < 8; ++i) c.x[i] = __fmul2_rn(__fmul2_rn(c.x[i], inv2), __fadd2_rn(offset, wc.x[i]));
+        } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] *= a.weight_offset + w[i];
+          for (int i = 0; i < 8; ++i) c.x[i] = __fmul2_rn(c.x[i], inv2);
         }
       }
       if (kind != 2 && turns_here) {
         const float4* cs = reinterpret_cast<const float4*>(s_cs + (buf * tpb + tl) * half + 8 * l);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 w = cs[i];
-          const float p = x[2 * i], q = x[2 * i + 1], r = x[8 + 2 * i], s = x[9 + 2 * i];
-          x[2 * i] = p * w.x - r * w.y, x[8 + 2 * i] = r * w.x + p * w.y;
-          x[2 * i + 1] = q * w.z - s * w.w, x[9 + 2 * i] = s * w.z + q * w.w;
+          const float4 v = cs[i];  // of two columns
+          const float2 cos2 = make_float2(v.x, v.z), sin2 = make_float2(v.y, v.w), minus = make_float2(-v.y, -v.w);
+          const float2 p = c.x[i], q = c.x[4 + i];
+          c.x[i] = __ffma2_rn(q, minus, __fmul2_rn(p, cos2));
+          c.x[4 + i] = __ffma2_rn(p, sin2, __fmul2_rn(q, cos2));
         }
       }
       auto put = [&](void* base_ptr, long long offset) {
         T* p = static_cast<T*>(base_ptr) + offset + first;
-        store_vec<8>(p, x);
-        store_vec<8>(p + second, x + 8);
+        store_vec<8>(p, &c.x[0].x);
+        store_vec<8>(p + second, &c.x[4].x);
       };
-      if (kind == 0) put(a.q_out, t * a.q_out_stride + head * HD);
-      if (kind == 1 && a.k_out != nullptr) put(a.k_out, t * a.k_out_stride + head * HD);
-      if (kind == 1 && cache) put(a.k_cache, (row + head * 16) * HD);
-      if (kind == 2) put(a.v_cache, (row + head * 16) * HD);
+      if (kind == 0) {
+        put(a.q_out, t * a.q_out_stride + head * HD);
+      } else {
+        if (kind == 1 && a.k_out != nullptr) put(a.k_out, t * a.k_out_stride + head * HD);
+        if (cache) put(kind == 1 ? a.k_cache : a.v_cache, (((long long)blk * a.Hkv + head) * 16 + at % 16) * HD);
+      }
     }
-    now = next;
     t += tpb;
-    __syncthreads();
   }
 }
 
@@ -208,17 +245,23 @@ cudaError_t go(const QkRopeArgs& a, const Turns& turns, cudaStream_t s) {
   if (tpb > a.T) tpb = a.T;
   const int threads = (tpb * ipb * L + 31) / 32 * 32;
   const int groups = (items + ipb - 1) / ipb;
-  const size_t smem = (size_t)2 * tpb * (a.rotary / 2) * sizeof(float2);
-  // as many blocks as are resident at once, each a run of tokens
-  int resident = 2048 / threads;
-  if (resident > 8) resident = 8;
+  const size_t smem = (size_t)kAhead * Own<T>::kParts * threads * 16 + (size_t)2 * tpb * (a.rotary / 2) * sizeof(float2);
+  auto kern = qk_rope_kernel<T, HD>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  // as many blocks as are resident at once (64 registers a thread), each a run of tokens
+  int resident = 1024 / threads;
+  if (resident > (int)(200 * 1024 / smem)) resident = (int)(200 * 1024 / smem);
+  if (resident < 1) resident = 1;
   long long blocks = (long long)device_sm_count() * resident / groups;
   const long long rows = ((long long)a.T + tpb - 1) / tpb;
   if (blocks > rows) blocks = rows;
   if (blocks < 1) blocks = 1;
   const int per_block = (int)((rows + blocks - 1) / blocks) * tpb;
   const dim3 grid((unsigned)(((long long)a.T + per_block - 1) / per_block), groups);
-  qk_rope_kernel<T, HD><<<grid, threads, smem, s>>>(a, turns, ipb, tpb, per_block);
+  kern<<<grid, threads, smem, s>>>(a, turns, ipb, tpb, per_block);
   return cudaGetLastError();
 }
 
