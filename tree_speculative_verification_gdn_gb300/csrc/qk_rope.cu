@@ -7,7 +7,7 @@
 // Angles: theta^(-2c/r) / 2 pi is a fraction of a turn for each position.  In 64-bit fixed point position times that
 // fraction drops whole turns by its overflow, exactly, however far the position; the nearest quarter turn comes off as
 // two bits and what is left, an eighth of a turn at most, goes to sincospi with its 24 bits whole.  They are made once
-// a token, by the threads of its heads, a token ahead of their use.
+// a token, eight tokens at a time by the whole block: made a token at a time by two warps, the others waited for them.
 //
 // Bound by HBM: q, k and v are read once and written once.  A block walks a run of tokens, its place among the sequences
 // searched once, then counted on.  A thread's own vectors come through shared memory three tokens ahead, so that what is on
@@ -26,6 +26,7 @@ struct Turns {
   unsigned long long f[128];  // turns a position, in 2^-64
 };
 
+constexpr int kChunk = 8;  // tokens whose places and angles are made at a time, by the whole block
 constexpr int kAhead = 4;  // tokens of a thread's vectors on their way, the one in work among them
 
 // Sixteen columns as pairs of neighbours: eight from the first vector, eight from the second.
@@ -66,9 +67,13 @@ __global__ void __launch_bounds__(512, 2)
                    int per_block) {
   constexpr int L = HD / 16;
   constexpr int kParts = Own<T>::kParts;
-  extern __shared__ uint4 s_own[];  // [kAhead][kParts][threads], then (cos, sin) [2][tpb][rotary / 2]
+  // the threads' vectors [kAhead][kParts][threads]; (cos, sin) of a chunk and the next [2][chunk][rotary / 2]; places of a
+  // chunk and the next two [3][chunk]: position (-1: nothing to do) and block
+  extern __shared__ uint4 s_own[];
   const int half = a.rotary / 2;
+  const int rounds = tpb < kChunk ? kChunk / tpb : 1, chunk = rounds * tpb;
   float2* s_cs = reinterpret_cast<float2*>(s_own + kAhead * kParts * blockDim.x);
+  int2* s_place = reinterpret_cast<int2*>(s_cs + 2 * chunk * half);
   const bool cache = a.k_cache != nullptr;
   const int items = a.Hq + (cache ? 2 : 1) * a.Hkv;
   const int u = threadIdx.x / L, l = threadIdx.x % L;
@@ -111,10 +116,10 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
     for (int i = 0; i < kParts; ++i) w[i] = *reinterpret_cast<const uint4*>(Own<T>::at(weight + first, i, second));
 
-  // The token's sequence (-1: before the first, B: past the last), the token past its last, what to add to a token's number
-  // for its position; the token's position and block.
-  int b = -1, end = 0, shift = 0, position = 0, block = 0;
-  bool open = false, go = false;  // the sequence's tokens are worked on; this token is
+  // Thread i < chunk follows the i-th token of each chunk: its sequence (-1: before the first, B: past the last), the token
+  // past its last, what to add to a token's number for its position.
+  int b = -1, end = 0, shift = 0;
+  bool open = false;  // the sequence's tokens are worked on
   if (a.cu != nullptr) {
     if (a.err[0] == TV_ERR_BAD_SEQLEN) {
       cp_async_wait<0>();
@@ -127,9 +132,7 @@ __global__ void __launch_bounds__(512, 2)
     b = n - 2;  // find() enters the sequence itself
     end = n > 0 ? (int)t0 : a.cu[0];
   }
-  auto find = [&](int token) {  // tokens come in ascending order
-    go = false;
-    if (token >= t1 || !in) return;
+  auto find = [&](int token) -> int2 {  // tokens come in ascending order
     if (a.cu != nullptr) {
       while (b < a.B && token >= end) {
         ++b;
@@ -140,27 +143,33 @@ __global__ void __launch_bounds__(512, 2)
           open = a.err[b] == 0 && (a.live == nullptr || a.live[b] != 0);
         }
       }
-      if (!open) return;
-      position = token + shift;
-    } else {
-      b = token;
-      int st = 0;
-      const bool live = a.live == nullptr || a.live[b] != 0;
-      position = a.prefix_len != nullptr ? a.prefix_len[b] : 0;
-      if (live && (position < 0 || position >= (cache ? a.max_blocks * 16 : 0x7fffffff))) st = TV_ERR_CAPACITY;
-      if (live && st == 0 && cache &&
-          (unsigned)a.block_table[(long long)b * a.max_blocks + position / 16] >= (unsigned)a.num_blocks)
-        st = TV_ERR_BAD_BLOCK;
-      if (item == 0 && l == 0) a.err[b] = st;
-      if (!live || st != 0) return;
+      if (!open) return make_int2(-1, 0);
+      const int position = token + shift;
+      return make_int2(position, cache ? a.block_table[(long long)b * a.max_blocks + position / 16] : 0);
     }
-    if (cache && kind != 0) block = a.block_table[(long long)b * a.max_blocks + position / 16];
-    go = true;
+    // one token a sequence: checked here
+    int st = 0, block = 0;
+    const bool live = a.live == nullptr || a.live[token] != 0;
+    const int position = a.prefix_len != nullptr ? a.prefix_len[token] : 0;
+    if (live && (position < 0 || position >= (cache ? a.max_blocks * 16 : 0x7fffffff))) st = TV_ERR_CAPACITY;
+    if (live && st == 0 && cache) {
+      block = a.block_table[(long long)token * a.max_blocks + position / 16];
+      if ((unsigned)block >= (unsigned)a.num_blocks) st = TV_ERR_BAD_BLOCK;
+    }
+    if (blockIdx.y == 0) a.err[token] = st;
+    return make_int2(live && st == 0 ? position : -1, block);
   };
-  auto angles = [&](int buf) {
-    if (!go) return;
-    float2* cs = s_cs + (buf * tpb + tl) * half;
-    for (int c = (u - tl * ipb) * L + l; c < half; c += ipb * L) {
+  auto places = [&](int k) {  // of chunk k
+    const int i = threadIdx.x;
+    const long long token = t0 + (long long)k * chunk + i;
+    if (i < chunk) s_place[k % 3 * chunk + i] = token < t1 ? find((int)token) : make_int2(-1, 0);
+  };
+  // Pair i = 0 .. 3 of lane l's eight columns lies at [i][l], so that a head's lanes read side by side.
+  auto angles = [&](int k) {
+    for (int i = threadIdx.x; i < chunk * half; i += blockDim.x) {
+      const int token = i / half, c = i - token * half;
+      const int position = s_place[k % 3 * chunk + token].x;
+      if (position < 0) continue;
       const unsigned long long turn = (unsigned long long)(unsigned)position * turns.f[c];
       const unsigned long long quarter = (turn + (1ull << 61)) >> 62;
       const int rest = (int)((long long)(turn - (quarter << 62)) >> 30);  // in 2^-34 of a turn
@@ -169,20 +178,25 @@ __global__ void __launch_bounds__(512, 2)
       const float2 even = make_float2(cn, sn), odd = make_float2(-sn, cn);
       float2 v = quarter & 1 ? odd : even;
       if (quarter & 2) v.x = -v.x, v.y = -v.y;
-      cs[c] = v;
+      s_cs[((k & 1) * chunk + token) * half + (c % 8 / 2 * (half / 8) + c / 8) * 2 + c % 2] = v;
     }
   };
 
-  find(t);
+  places(0);
+  places(1);
+  __syncthreads();
   angles(0);
-  int buf = 0, k = 0;
-  for (int base = (int)t0; base < t1; base += tpb, buf ^= 1, ++k) {
-    const bool now = go && mine;
-    const int at = position, blk = block;
-    __syncthreads();  // this token's angles are there, the last one's are done with
+  int k = 0, round = 0, chunk_at = 0;
+  for (int base = (int)t0; base < t1; base += tpb, ++k) {
+    if (round == 0) {  // this chunk's angles are there, the last one's are done with
+      __syncthreads();
+      places(chunk_at + 2);
+      angles(chunk_at + 1);
+    }
     copy(kAhead - 1, (k + kAhead - 1) % kAhead);
-    find(t + tpb);
-    angles(buf ^ 1);
+    const int in_chunk = round * tpb + tl;
+    const int2 place = mine ? s_place[chunk_at % 3 * chunk + in_chunk] : make_int2(-1, 0);
+    const bool now = place.x >= 0;
     cp_async_wait<kAhead - 1>();
     Columns c;
     float2 sum2 = make_float2(0.f, 0.f);
@@ -209,10 +223,10 @@ __global__ void __launch_bounds__(512, 2)
         }
       }
       if (kind != 2 && turns_here) {
-        const float4* cs = reinterpret_cast<const float4*>(s_cs + (buf * tpb + tl) * half + 8 * l);
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + ((chunk_at & 1) * chunk + in_chunk) * half) + l;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 v = cs[i];  // of two columns
+          const float4 v = cs[i * (half / 8)];  // of two columns
           const float2 cos2 = make_float2(v.x, v.z), sin2 = make_float2(v.y, v.w), minus = make_float2(-v.y, -v.w);
           const float2 p = c.x[i], q = c.x[4 + i];
           c.x[i] = __ffma2_rn(q, minus, __fmul2_rn(p, cos2));
@@ -228,10 +242,11 @@ __global__ void __launch_bounds__(512, 2)
         put(a.q_out, t * a.q_out_stride + head * HD);
       } else {
         if (kind == 1 && a.k_out != nullptr) put(a.k_out, t * a.k_out_stride + head * HD);
-        if (cache) put(kind == 1 ? a.k_cache : a.v_cache, (((long long)blk * a.Hkv + head) * 16 + at % 16) * HD);
+        if (cache) put(kind == 1 ? a.k_cache : a.v_cache, (((long long)place.y * a.Hkv + head) * 16 + place.x % 16) * HD);
       }
     }
     t += tpb;
+    if (++round == rounds) round = 0, ++chunk_at;
   }
 }
 
@@ -245,7 +260,8 @@ cudaError_t go(const QkRopeArgs& a, const Turns& turns, cudaStream_t s) {
   if (tpb > a.T) tpb = a.T;
   const int threads = (tpb * ipb * L + 31) / 32 * 32;
   const int groups = (items + ipb - 1) / ipb;
-  const size_t smem = (size_t)kAhead * Own<T>::kParts * threads * 16 + (size_t)2 * tpb * (a.rotary / 2) * sizeof(float2);
+  const int chunk = tpb < kChunk ? kChunk / tpb * tpb : tpb;
+  const size_t smem = (size_t)kAhead * Own<T>::kParts * threads * 16 + (size_t)chunk * (a.rotary * sizeof(float2) + 3 * sizeof(int2));
   auto kern = qk_rope_kernel<T, HD>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
