@@ -1,9 +1,11 @@
 #include "paged_check.cuh"
+#include "tv_launch.cuh"
 
 namespace tv {
 namespace {
 
 __global__ void __launch_bounds__(256) paged_check_kernel(PagedCheck c, int32_t* __restrict__ err) {
+  plan_begun();
   int n;
   const int st = check_sequence(c, blockIdx.x, n);
   if (threadIdx.x == 0) err[blockIdx.x] = st;

@@ -18,6 +18,7 @@
 #include "tv_async.cuh"
 #include "tv_common.cuh"
 #include "tv_internal.h"
+#include "tv_launch.cuh"
 
 namespace tv {
 namespace {
@@ -43,13 +44,15 @@ struct Own;
 template <>
 struct Own<bf16> {
   static constexpr int kParts = 2;  // of 16 bytes
-  __device__ static const bf16* at(const bf16* p, int part, int second) { return p + part * second; }
+  template <typename P>
+  __device__ static P* at(P* p, int part, int second) { return p + part * second; }
   __device__ static void widen16(const uint4* s, int step, Columns& c) { widen(s[0], c.x), widen(s[step], c.x + 4); }
 };
 template <>
 struct Own<float> {
   static constexpr int kParts = 4;
-  __device__ static const float* at(const float* p, int part, int second) { return p + (part / 2) * second + (part % 2) * 4; }
+  template <typename P>
+  __device__ static P* at(P* p, int part, int second) { return p + (part / 2) * second + (part % 2) * 4; }
   __device__ static void widen16(const uint4* s, int step, Columns& c) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -68,12 +71,13 @@ __global__ void __launch_bounds__(512, 2)
   constexpr int L = HD / 16;
   constexpr int kParts = Own<T>::kParts;
   // the threads' vectors [kAhead][kParts][threads]; (cos, sin) of a chunk and the next [2][chunk][rotary / 2]; places of a
-  // chunk and the next two [3][chunk]: position (-1: nothing to do) and block
+  // chunk and the next two [3][chunk]: position (-1: nothing to do) and block; the heads' weights
   extern __shared__ uint4 s_own[];
   const int half = a.rotary / 2;
   const int rounds = tpb < kChunk ? kChunk / tpb : 1, chunk = rounds * tpb;
   float2* s_cs = reinterpret_cast<float2*>(s_own + kAhead * kParts * blockDim.x);
   int2* s_place = reinterpret_cast<int2*>(s_cs + 2 * chunk * half);
+  float2* s_w = reinterpret_cast<float2*>(s_place + 3 * chunk + (chunk & 1));  // offset + weight, of queries and of keys: [2][8][L]
   const bool cache = a.k_cache != nullptr;
   const int items = a.Hq + (cache ? 2 : 1) * a.Hkv;
   const int u = threadIdx.x / L, l = threadIdx.x % L;
@@ -91,31 +95,41 @@ __global__ void __launch_bounds__(512, 2)
   const bool turns_here = l < a.rotary / 16;
   const int first = turns_here ? 8 * l : a.rotary + 16 * (l - a.rotary / 16);
   const int second = turns_here ? half : 8;
-  const T* x_in = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + head * HD + first;
-  const long long x_stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+  const long long x_stride = (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * tpb;
   int t = (int)t0 + tl;
+  const T* from = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + t * (x_stride / tpb) + head * HD + first;
 
-  // Copies need no place among the sequences: they go ahead of everything.
-  auto copy = [&](int ahead, int stage) {  // token t + ahead * tpb
-    const long long token = (long long)t + (long long)ahead * tpb;
-    if (mine && token < t1) {
-      const T* p = x_in + token * x_stride;
+  // Copies need no place among the sequences: they go ahead of everything.  copied: the token that is copied next.
+  int copied = mine ? t : 0x7fffffff, to_stage = 0;
+  auto copy = [&]() {
+    if (copied < t1) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i)
-        cp_async_16_cg(s_own + (stage * kParts + i) * blockDim.x + threadIdx.x, Own<T>::at(p, i, second));
+        cp_async_16_cg(s_own + (to_stage * kParts + i) * blockDim.x + threadIdx.x, Own<T>::at(from, i, second));
+      from += x_stride;
+      copied = copied < 0x7fffffff - tpb ? copied + tpb : 0x7fffffff;
     }
+    to_stage = to_stage + 1 == kAhead ? 0 : to_stage + 1;
     cp_async_commit();
   };
 #pragma unroll
-  for (int k = 0; k < kAhead - 1; ++k) copy(k, k);
+  for (int k = 0; k < kAhead - 1; ++k) copy();
 
-  const T* weight = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
-  const bool scaled = a.norm && kind != 2, weighted = scaled && weight != nullptr && mine;
-  uint4 w[kParts];
-  if (weighted)
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) w[i] = *reinterpret_cast<const uint4*>(Own<T>::at(weight + first, i, second));
+  const bool scaled = a.norm && kind != 2;
+  const bool weighted = a.norm && (kind == 0 ? a.q_weight != nullptr : kind == 1 && a.k_weight != nullptr);
+  for (int i = threadIdx.x; i < 2 * HD; i += blockDim.x) {
+    const T* w = static_cast<const T*>(i < HD ? a.q_weight : a.k_weight);
+    if (w == nullptr) continue;
+    // column c of a head is its lane's l place e: as in first and second
+    const int c = i % HD;
+    int lane, e;
+    if (c < half) lane = c / 8, e = c % 8;
+    else if (c < 2 * half) lane = (c - half) / 8, e = 8 + (c - half) % 8;
+    else lane = half / 8 + (c - 2 * half) / 16, e = (c - 2 * half) % 16;
+    reinterpret_cast<float*>(s_w + (i / HD * 8 + e / 2) * L + lane)[e % 2] = a.weight_offset + to_f32(w[c]);
+  }
 
+  wait_for_plan();
   // Thread i < chunk follows the i-th token of each chunk: its sequence (-1: before the first, B: past the last), the token
   // past its last, what to add to a token's number for its position.
   int b = -1, end = 0, shift = 0;
@@ -178,7 +192,9 @@ __global__ void __launch_bounds__(512, 2)
       const float2 even = make_float2(cn, sn), odd = make_float2(-sn, cn);
       float2 v = quarter & 1 ? odd : even;
       if (quarter & 2) v.x = -v.x, v.y = -v.y;
-      s_cs[((k & 1) * chunk + token) * half + (c % 8 / 2 * (half / 8) + c / 8) * 2 + c % 2] = v;
+      // as two cosines and two sines: registers that lie side by side
+      float* to = reinterpret_cast<float*>(s_cs + ((k & 1) * chunk + token) * half + (c % 8 / 2 * (half / 8) + c / 8) * 2) + c % 2;
+      to[0] = v.x, to[2] = v.y;
     }
   };
 
@@ -186,66 +202,72 @@ __global__ void __launch_bounds__(512, 2)
   places(1);
   __syncthreads();
   angles(0);
-  int k = 0, round = 0, chunk_at = 0;
-  for (int base = (int)t0; base < t1; base += tpb, ++k) {
+  T* q_to = static_cast<T*>(a.q_out) + t * a.q_out_stride + head * HD + first;
+  T* k_to = a.k_out != nullptr ? static_cast<T*>(a.k_out) + t * a.k_out_stride + head * HD + first : nullptr;
+  int round = 0, chunk_at = 0, stage = 0;
+  const float2* w_own = s_w + (kind * 8) * L + l;
+  for (int base = (int)t0; base < t1; base += tpb) {
     if (round == 0) {  // this chunk's angles are there, the last one's are done with
       __syncthreads();
       places(chunk_at + 2);
       angles(chunk_at + 1);
     }
-    copy(kAhead - 1, (k + kAhead - 1) % kAhead);
+    copy();
     const int in_chunk = round * tpb + tl;
     const int2 place = mine ? s_place[chunk_at % 3 * chunk + in_chunk] : make_int2(-1, 0);
     const bool now = place.x >= 0;
     cp_async_wait<kAhead - 1>();
+    const uint4* own = s_own + stage * kParts * blockDim.x + threadIdx.x;
+    stage = stage + 1 == kAhead ? 0 : stage + 1;
+    const long long row = (((long long)place.y * a.Hkv + head) * 16 + (place.x & 15)) * HD + first;
     Columns c;
     float2 sum2 = make_float2(0.f, 0.f);
-    if (now) {
-      Own<T>::widen16(s_own + k % kAhead * kParts * blockDim.x + threadIdx.x, blockDim.x, c);
-      if (scaled)
+    if (now && kind != 2) {
+      Own<T>::widen16(own, blockDim.x, c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum2 = __ffma2_rn(c.x[i], c.x[i], sum2);
+      for (int i = 0; i < 8; ++i) sum2 = __ffma2_rn(c.x[i], c.x[i], sum2);
     }
     const float sum = group_sum<L>(sum2.x + sum2.y);
-    if (now) {
+    if (now && kind != 2) {
       if (scaled) {
         const float inv = rsqrtf(sum / HD + a.eps);
         const float2 inv2 = make_float2(inv, inv);
-        if (weighted) {
-          Columns wc;
-          Own<T>::widen16(w, 1, wc);
-          const float2 offset = make_float2(a.weight_offset, a.weight_offset);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) c.x[i] = __fmul2_rn(__fmul2_rn(c.x[i], inv2), __fadd2_rn(offset, wc.x[i]));
-        } else {
+        for (int i = 0; i < 8; ++i) c.x[i] = __fmul2_rn(c.x[i], inv2);
+        if (weighted)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) c.x[i] = __fmul2_rn(c.x[i], inv2);
-        }
+          for (int i = 0; i < 8; ++i) c.x[i] = __fmul2_rn(c.x[i], w_own[i * L]);
       }
-      if (kind != 2 && turns_here) {
+      if (turns_here) {
         const float4* cs = reinterpret_cast<const float4*>(s_cs + ((chunk_at & 1) * chunk + in_chunk) * half) + l;
+        const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 v = cs[i * (half / 8)];  // of two columns
-          const float2 cos2 = make_float2(v.x, v.z), sin2 = make_float2(v.y, v.w), minus = make_float2(-v.y, -v.w);
+          const float2 cos2 = make_float2(v.x, v.y), sin2 = make_float2(v.z, v.w);
           const float2 p = c.x[i], q = c.x[4 + i];
-          c.x[i] = __ffma2_rn(q, minus, __fmul2_rn(p, cos2));
+          c.x[i] = __ffma2_rn(p, cos2, __fmul2_rn(__fmul2_rn(q, sin2), minus));
           c.x[4 + i] = __ffma2_rn(p, sin2, __fmul2_rn(q, cos2));
         }
       }
-      auto put = [&](void* base_ptr, long long offset) {
-        T* p = static_cast<T*>(base_ptr) + offset + first;
+      auto put = [&](T* p) {
         store_vec<8>(p, &c.x[0].x);
         store_vec<8>(p + second, &c.x[4].x);
       };
       if (kind == 0) {
-        put(a.q_out, t * a.q_out_stride + head * HD);
+        put(q_to);
       } else {
-        if (kind == 1 && a.k_out != nullptr) put(a.k_out, t * a.k_out_stride + head * HD);
-        if (cache) put(kind == 1 ? a.k_cache : a.v_cache, (((long long)place.y * a.Hkv + head) * 16 + place.x % 16) * HD);
+        if (a.k_out != nullptr) put(k_to);
+        if (cache) put(static_cast<T*>(a.k_cache) + row);
       }
+    } else if (now) {
+      // a value goes as it is
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+        *reinterpret_cast<uint4*>(Own<T>::at(static_cast<T*>(a.v_cache) + row, i, second)) = own[i * blockDim.x];
     }
-    t += tpb;
+    q_to += a.q_out_stride * tpb;
+    if (a.k_out != nullptr) k_to += a.k_out_stride * tpb;
     if (++round == rounds) round = 0, ++chunk_at;
   }
 }
@@ -261,7 +283,7 @@ cudaError_t go(const QkRopeArgs& a, const Turns& turns, cudaStream_t s) {
   const int threads = (tpb * ipb * L + 31) / 32 * 32;
   const int groups = (items + ipb - 1) / ipb;
   const int chunk = tpb < kChunk ? kChunk / tpb * tpb : tpb;
-  const size_t smem = (size_t)kAhead * Own<T>::kParts * threads * 16 + (size_t)chunk * (a.rotary * sizeof(float2) + 3 * sizeof(int2));
+  const size_t smem = (size_t)kAhead * Own<T>::kParts * threads * 16 + (size_t)chunk * (a.rotary * sizeof(float2) + 3 * sizeof(int2)) + 8 + 2 * HD * sizeof(float);
   auto kern = qk_rope_kernel<T, HD>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -277,6 +299,7 @@ cudaError_t go(const QkRopeArgs& a, const Turns& turns, cudaStream_t s) {
   if (blocks < 1) blocks = 1;
   const int per_block = (int)((rows + blocks - 1) / blocks) * tpb;
   const dim3 grid((unsigned)(((long long)a.T + per_block - 1) / per_block), groups);
+  if (a.cu != nullptr) return launch_behind_plan(kern, grid, threads, smem, s, a, turns, ipb, tpb, per_block);
   kern<<<grid, threads, smem, s>>>(a, turns, ipb, tpb, per_block);
   return cudaGetLastError();
 }

@@ -3,6 +3,7 @@
 
 #include "tv_common.cuh"
 #include "tv_internal.h"
+#include "tv_launch.cuh"
 
 namespace tv {
 
@@ -27,21 +28,6 @@ __device__ __forceinline__ Seen seen_by(const WinAttnArgs& a, int P, int n) {
 }
 
 constexpr int kSms = 152;
-
-// The kernel behind the plan is launched before the plan has ended: plan_begun() in the plan lets it, and wait_for_plan()
-// in the kernel, before its first read of what the plan writes, waits until the plan's writes are there.
-__device__ __forceinline__ void plan_begun() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <typename... P, typename... A>
-cudaError_t launch_behind_plan(void (*kern)(P...), int grid, int block, size_t smem, cudaStream_t s, const A&... args) {
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid), c.blockDim = dim3(block), c.dynamicSmemBytes = smem, c.stream = s;
-  c.attrs = &early, c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, P(args)...);
-}
 
 // The costs of all sequences, Hkv times each, lie one behind the other; CTA i of the grid takes the i-th of equal runs of
 // at least `least`.
