@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) window_plan_kernel(WinAttnArgs a, PagedCh
 }
 
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
-bool few_rows(int max_len, int group, int hd) { return (long long)max_len * group <= rows_limit(hd); }
+bool few_rows(int max_len, int group) { return (long long)max_len * group <= kFewRows; }
 // workspace: costs, counters, slots of shared outputs
 int counters(int B, int Hkv, bool few) { return few ? B * Hkv : kSms * 8; }
 
@@ -50,13 +50,13 @@ int counters(int B, int Hkv, bool few) { return few ? B * Hkv : kSms * 8; }
 size_t window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, int hd, int max_blocks, int window,
                                   int sinks) {
   if (T == 0) return 0;
-  const bool few = few_rows(max_len, Hq / Hkv, hd);
+  const bool few = few_rows(max_len, Hq / Hkv);
   return align16((size_t)B * 8) + align16((size_t)counters(B, Hkv, few) * 4) +
-         (few ? window_rows_slots(max_len * (Hq / Hkv), hd) : window_tiles_slots(hd));
+         (few ? window_rows_slots(hd) : window_tiles_slots(hd));
 }
 
 cudaError_t launch_window_attn(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
-  const bool few = few_rows(a.max_len, a.Hq / a.Hkv, a.hd);
+  const bool few = few_rows(a.max_len, a.Hq / a.Hkv);
   const PagedCheck c{a.cu, a.prefix_len, a.live, a.block_table, a.B, a.T, a.max_len, a.max_blocks, a.num_blocks,
                      a.window, a.sinks};
   if (a.T == 0) return launch_paged_check(c, a.err, s);  // no workspace

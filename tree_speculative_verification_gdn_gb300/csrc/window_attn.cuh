@@ -106,10 +106,11 @@ __device__ __forceinline__ bool find_run(const WinAttnArgs& a, const long long* 
 }
 
 // Head dims 64, 128, 256; a.cu or one token a sequence.  cost [B]: of a sequence for one KV head.
-// Few rows: sequences of at most rows_limit(hd) query rows (new tokens x query heads of a KV head); cost: pages.
-constexpr int rows_limit(int hd) { return 4096 / hd; }
+// Few rows: at most 16 query rows (new tokens x query heads of a KV head) in a sequence; cost: pages.  With 32 rows of
+// head dim 128 (32 chains of eight tokens behind 8192) this kernel took 117 us, that for any number 91 us.
 // arrived [B * Hkv], zero; slots: bytes as window_rows_slots.
-size_t window_rows_slots(int rows, int hd);
+constexpr int kFewRows = 16;
+size_t window_rows_slots(int hd);
 cudaError_t launch_window_rows(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s);
 
 // Any number of rows: units of `tokens` tokens; cost: per unit its key tiles and kUnitCost more.

@@ -1,6 +1,6 @@
 // Windowed attention of few query rows -- single tokens, short drafted chains -- over long contexts.
 //
-// The rows of a sequence and KV head, (new token, query head of the group), are at most 4096 / hd, and every visible key and
+// The rows of a sequence and KV head, (new token, query head of the group), are at most 16, and every visible key and
 // value is read once for all of them: bound by HBM.  The visible pages of all sequences and KV heads, one behind the
 // other, are dealt out to the grid in equal runs, so that ragged lengths and few sequences spread alike.  A CTA's four warps
 // take the pages of its run in turn, each with its own ring of copies in flight, its own running maximum, sum and
@@ -18,11 +18,12 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;      // query rows of a unit
 constexpr int kWhole = 16;     // pages of a sequence and head that are never cut
 constexpr int kLeast = 8;      // pages a run, at least: below, joining costs more than the pages
 constexpr float kRaise = 8.f;  // the running maximum is raised only by more than this (log2): sums grow by 2^8 at most
 
-constexpr int per_sm(int hd, int tiles) { return hd == 256 ? 1 : hd == 128 || tiles == 4 ? 2 : 3; }
+constexpr int per_sm(int hd) { return hd == 256 ? 1 : hd == 128 ? 2 : 3; }
 
 template <int HD>
 struct Shape {
@@ -64,16 +65,16 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return row * (HD * 2) + ((c ^ (row & 7)) << 4);
 }
 
-template <int HD, int MT>
-__global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
+template <int HD>
+__global__ void __launch_bounds__(kThreads, per_sm(HD))
     window_rows_kernel(WinAttnArgs a, const long long* __restrict__ cost, float* __restrict__ slots,
                        int* __restrict__ arrived) {
   using S = Shape<HD>;
-  constexpr int kSlot = MT * 16 * (HD + 2);  // floats: outputs, then (maximum, sum) per row
+  constexpr int kSlot = kRows * (HD + 2);  // floats: outputs, then (maximum, sum) per row
   constexpr int CH = HD / 8;                 // 16-byte chunks of a row
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* sQ = smem;                          // MT * 16 rows
-  unsigned char* ring = smem + MT * 16 * HD * 2;
+  unsigned char* sQ = smem;                          // kRows rows
+  unsigned char* ring = smem + kRows * HD * 2;
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int G = a.Hq / a.Hkv;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
     if (used) __syncthreads();  // the last unit's outputs have left shared memory
     used = true;
     // the queries, zeros in place of rows past the last: in the first group of copies
-    for (int i = tid; i < MT * 16 * CH; i += kThreads) {
+    for (int i = tid; i < kRows * CH; i += kThreads) {
       const int r = i / CH, c = i % CH;
       const long long at = r < R ? (long long)(start + r / G) * a.q_stride + (long long)(kvh * G + r % G) * HD + c * 8 : 0;
       copy16(smem_addr(sQ) + chunk_at<HD>(r, c), static_cast<const bf16*>(a.q) + at, r < R);
@@ -149,21 +150,17 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
     cp_async_wait<S::kStages - 2>();
     __syncthreads();
 
-    // a thread's rows are lane / 4 and lane / 4 + 8 of each tile of 16
-    int pos[MT][2];
-    float m[MT][2], l[MT][2], o[MT][HD / 8][4];
+    // a thread's rows are lane / 4 and lane / 4 + 8
+    int pos[2];
+    float m[2], l[2], o[HD / 8][4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int h = 0; h < 2; ++h) {
+      pos[h] = q.P + min((lane / 4 + 8 * h) / G, q.n - 1);
+      m[h] = -INFINITY, l[h] = 0.f;
+    }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        pos[t][h] = q.P + min((t * 16 + lane / 4 + 8 * h) / G, q.n - 1);
-        m[t][h] = -INFINITY, l[t][h] = 0.f;
-      }
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int i = 0; i < HD / 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-    constexpr bool kHeld = MT == 1 && HD <= 128;  // queries stay in registers
+    for (int i = 0; i < HD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    constexpr bool kHeld = HD <= 128;  // queries stay in registers
     uint32_t qr[kHeld ? HD / 16 : 1][4];
     const uint32_t q_addr = smem_addr(sQ);
     if constexpr (kHeld) {
@@ -176,80 +173,68 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
       cp_async_wait<S::kStages - 1>();
       __syncwarp();
       const uint32_t kp = my_ring + (k % S::kStages) * 2 * S::kPage, vp = kp + S::kPage;
-      float s[MT][2][4];
+      float s[2][4];
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) s[t][i][0] = s[t][i][1] = s[t][i][2] = s[t][i][3] = 0.f;
+      for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < HD / 16; ++c) {
-        uint32_t kf[4];
+        uint32_t kf[4], qf[4];
         ldsm4(kp + chunk_at<HD>(lane % 8 + (lane / 16) * 8, 2 * c + (lane / 8) % 2), kf);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          uint32_t qf[4];
-          if constexpr (kHeld) {
-            qf[0] = qr[c][0], qf[1] = qr[c][1], qf[2] = qr[c][2], qf[3] = qr[c][3];
-          } else {
-            ldsm4(q_addr + t * 16 * HD * 2 + chunk_at<HD>(lane % 16, 2 * c + lane / 16), qf);
-          }
-          mma16816(s[t][0], qf, kf[0], kf[1]);
-          mma16816(s[t][1], qf, kf[2], kf[3]);
+        if constexpr (kHeld) {
+          qf[0] = qr[c][0], qf[1] = qr[c][1], qf[2] = qr[c][2], qf[3] = qr[c][3];
+        } else {
+          ldsm4(q_addr + chunk_at<HD>(lane % 16, 2 * c + lane / 16), qf);
         }
+        mma16816(s[0], qf, kf[0], kf[1]);
+        mma16816(s[1], qf, kf[2], kf[3]);
       }
       const int at = q.position(p0 + warp + k * kWarps);
       // every row sees the whole page: up to the first token, and within the last one's window or among the first tokens
       const bool open = at + 15 <= q.P && (a.window == 0 || at > last - a.window || at + 15 < a.sinks);
-      uint32_t pf[MT][4];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = s[t][i][e] * scale;
-            if (!open) {
-              const int j = at + i * 8 + (lane % 4) * 2 + (e & 1), p = pos[t][e / 2];
-              if (j > p || (a.window > 0 && p - j >= a.window && j >= a.sinks)) v = -INFINITY;
-            }
-            s[t][i][e] = v;
+        for (int e = 0; e < 4; ++e) {
+          float v = s[i][e] * scale;
+          if (!open) {
+            const int j = at + i * 8 + (lane % 4) * 2 + (e & 1), p = pos[e / 2];
+            if (j > p || (a.window > 0 && p - j >= a.window && j >= a.sinks)) v = -INFINITY;
           }
-        float mx[2];
+          s[i][e] = v;
+        }
+      float mx[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      }
+      if (__any_sync(0xffffffffu, mx[0] > m[0] + kRaise || mx[1] > m[1] + kRaise)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]), fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        }
-        if (__any_sync(0xffffffffu, mx[0] > m[t][0] + kRaise || mx[1] > m[t][1] + kRaise)) {
+          const float to = fmaxf(m[h], mx[h]);
+          const float f = m[h] == -INFINITY ? 0.f : ex2(m[h] - to);
+          m[h] = to;
+          l[h] *= f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float to = fmaxf(m[t][h], mx[h]);
-            const float f = m[t][h] == -INFINITY ? 0.f : ex2(m[t][h] - to);
-            m[t][h] = to;
-            l[t][h] *= f;
-#pragma unroll
-            for (int i = 0; i < HD / 8; ++i) o[t][i][2 * h] *= f, o[t][i][2 * h + 1] *= f;
-          }
+          for (int i = 0; i < HD / 8; ++i) o[i][2 * h] *= f, o[i][2 * h + 1] *= f;
         }
+      }
+      uint32_t pf[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float neg = m[t][h] == -INFINITY ? 0.f : -m[t][h];  // nothing seen yet: 2^-inf = 0
-          pf[t][h] = pack_bf16x2(ex2(s[t][0][2 * h] + neg), ex2(s[t][0][2 * h + 1] + neg));
-          pf[t][2 + h] = pack_bf16x2(ex2(s[t][1][2 * h] + neg), ex2(s[t][1][2 * h + 1] + neg));
-          // the sum of what the product with the values will use
-          l[t][h] += (bf16lo(pf[t][h]) + bf16hi(pf[t][h])) + (bf16lo(pf[t][2 + h]) + bf16hi(pf[t][2 + h]));
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float neg = m[h] == -INFINITY ? 0.f : -m[h];  // nothing seen yet: 2^-inf = 0
+        pf[h] = pack_bf16x2(ex2(s[0][2 * h] + neg), ex2(s[0][2 * h + 1] + neg));
+        pf[2 + h] = pack_bf16x2(ex2(s[1][2 * h] + neg), ex2(s[1][2 * h + 1] + neg));
+        // the sum of what the product with the values will use
+        l[h] += (bf16lo(pf[h]) + bf16hi(pf[h])) + (bf16lo(pf[2 + h]) + bf16hi(pf[2 + h]));
       }
 #pragma unroll
       for (int c = 0; c < CH; c += 2) {
         uint32_t vf[4];
         ldsm4_t(vp + chunk_at<HD>(lane % 16, c + lane / 16), vf);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          mma16816(o[t][c], pf[t], vf[0], vf[1]);
-          mma16816(o[t][c + 1], pf[t], vf[2], vf[3]);
-        }
+        mma16816(o[c], pf, vf[0], vf[1]);
+        mma16816(o[c + 1], pf, vf[2], vf[3]);
       }
       __syncwarp();  // the stage is free
     }
@@ -257,28 +242,26 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
 
     // The four warps' outputs meet in shared memory, over the rings.
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 1);
-        l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 2);
-      }
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
     __syncthreads();
-    float* acc = reinterpret_cast<float*>(ring);                 // [kWarps][MT * 16][HD]
-    float* ml = reinterpret_cast<float*>(sQ);                    // [kWarps][MT * 16][2]
-    static_assert(kWarps * MT * 16 * HD * 4 <= S::kRing, "outputs fit over the rings");
+    float* acc = reinterpret_cast<float*>(ring);  // [kWarps][16][HD]
+    float* ml = reinterpret_cast<float*>(sQ);     // [kWarps][16][2]
+    static_assert(kWarps * kRows * HD * 4 <= S::kRing, "outputs fit over the rings");
     static_assert(kWarps * 2 * 4 <= HD * 2, "maxima and sums fit over the queries");
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = t * 16 + lane / 4 + 8 * h;
-        float* row = acc + (warp * MT * 16 + r) * HD;
+    for (int h = 0; h < 2; ++h) {
+      const int r = lane / 4 + 8 * h;
+      if (r < R) {
+        float* row = acc + (warp * kRows + r) * HD;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i)
-          *reinterpret_cast<float2*>(row + i * 8 + (lane % 4) * 2) = make_float2(o[t][i][2 * h], o[t][i][2 * h + 1]);
-        if (lane % 4 == 0) ml[(warp * MT * 16 + r) * 2] = m[t][h], ml[(warp * MT * 16 + r) * 2 + 1] = l[t][h];
+          *reinterpret_cast<float2*>(row + i * 8 + (lane % 4) * 2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        if (lane % 4 == 0) ml[(warp * kRows + r) * 2] = m[h], ml[(warp * kRows + r) * 2 + 1] = l[h];
       }
+    }
     __syncthreads();
     const bool alone = p0 == 0 && p1 == q.pages;
     const long long c0 = u0 / per, c1 = (u1 - 1) / per;  // the CTAs that share the unit
@@ -293,13 +276,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
       const int r = i / (HD / 4), c = i % (HD / 4) * 4;
       float top = -INFINITY, f[kWarps], sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * MT * 16 + r) * 2]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = ml[(w * MT * 16 + r) * 2];
+        const float mw = ml[(w * kRows + r) * 2];
         f[w] = mw == -INFINITY ? 0.f : ex2(mw - top);
-        sum += f[w] * ml[(w * MT * 16 + r) * 2 + 1];
-        const float4 y = *reinterpret_cast<const float4*>(acc + (w * MT * 16 + r) * HD + c);
+        sum += f[w] * ml[(w * kRows + r) * 2 + 1];
+        const float4 y = *reinterpret_cast<const float4*>(acc + (w * kRows + r) * HD + c);
         v[0] += f[w] * y.x, v[1] += f[w] * y.y, v[2] += f[w] * y.z, v[3] += f[w] * y.w;
       }
       if (alone) {
@@ -309,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
       } else {
         float* slot = slot_of(blockIdx.x);
         *reinterpret_cast<float4*>(slot + r * HD + c) = make_float4(v[0], v[1], v[2], v[3]);
-        if (c == 0) slot[MT * 16 * HD + r * 2] = top, slot[MT * 16 * HD + r * 2 + 1] = sum;
+        if (c == 0) slot[kRows * HD + r * 2] = top, slot[kRows * HD + r * 2 + 1] = sum;
       }
     }
     if (!alone) {
@@ -333,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
               const float* slot = slot_of(c0 + min(k + j, parts - 1));
-              w[j] = __ldcg(reinterpret_cast<const float2*>(slot + MT * 16 * HD + r * 2));
+              w[j] = __ldcg(reinterpret_cast<const float2*>(slot + kRows * HD + r * 2));
               y[j] = __ldcg(reinterpret_cast<const float4*>(slot + r * HD + c));
             }
             float to = top;
@@ -359,28 +342,22 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD, MT))
   }
 }
 
-int tiles_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-template <int HD, int MT>
+template <int HD>
 cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
-  const size_t smem = MT * 16 * HD * 2 + Shape<HD>::kRing;
-  auto kern = window_rows_kernel<HD, MT>;
+  const size_t smem = kRows * HD * 2 + Shape<HD>::kRing;
+  auto kern = window_rows_kernel<HD>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_behind_plan(kern, kSms * per_sm(HD, MT), kThreads, smem, s, a, cost, slots, arrived);
+  return launch_behind_plan(kern, kSms * per_sm(HD), kThreads, smem, s, a, cost, slots, arrived);
 }
 
 }  // namespace
 
-size_t window_rows_slots(int rows, int hd) {
-  const int tiles = tiles_of(rows);
-  return (size_t)kSms * per_sm(hd, tiles) * 2 * tiles * 16 * (hd + 2) * sizeof(float);
-}
+size_t window_rows_slots(int hd) { return (size_t)kSms * per_sm(hd) * 2 * kRows * (hd + 2) * sizeof(float); }
 
 cudaError_t launch_window_rows(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
-  const int tiles = tiles_of(a.max_len * (a.Hq / a.Hkv));
-  if (a.hd == 256) return go<256, 1>(a, cost, arrived, slots, s);
-  if (a.hd == 128) return tiles == 1 ? go<128, 1>(a, cost, arrived, slots, s) : go<128, 2>(a, cost, arrived, slots, s);
-  return tiles == 1 ? go<64, 1>(a, cost, arrived, slots, s) : tiles == 2 ? go<64, 2>(a, cost, arrived, slots, s) : go<64, 4>(a, cost, arrived, slots, s);
+  if (a.hd == 64) return go<64>(a, cost, arrived, slots, s);
+  return a.hd == 128 ? go<128>(a, cost, arrived, slots, s) : go<256>(a, cost, arrived, slots, s);
 }
 
 }  // namespace tv
