@@ -40,8 +40,8 @@ struct Shape {
   static constexpr int VS = HD == 64 ? 4 : 2;           // V tiles in theirs
   static constexpr uint32_t QCHUNK = kRows * 128;       // 64 columns of a row tile
   static constexpr uint32_t QTILE = HD / 64 * QCHUNK;
-  static constexpr uint32_t KCHUNK = KT * 128;          // 64 columns of a key tile
-  static constexpr uint32_t STAGE = HD / 64 * KCHUNK;
+  static constexpr uint32_t EIGHT = HD * 16;            // eight keys: 1024 bytes for each 64 of their columns
+  static constexpr uint32_t STAGE = KT / 8 * EIGHT;
   static constexpr uint32_t K0 = NT * QTILE;
   static constexpr uint32_t V0 = K0 + KS * STAGE;
   static constexpr uint32_t BARS = V0 + VS * STAGE;
@@ -80,21 +80,24 @@ __device__ __forceinline__ uint32_t elect_lane() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e;
 }
-// Descriptors as sw128_desc and sw128_mn_desc make them, in two words: the second is always the same.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) {
-  return (saddr >> 4) | (leading >> 4) << 16;
+// Shared-memory descriptors of 128-byte swizzled operands, in two words: the start and the bytes from 64 columns to the
+// next 64 (operands with the columns outermost), and the bytes from eight rows to the next eight.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t columns) {
+  return (saddr >> 4) | (columns >> 4) << 16;
 }
+__host__ __device__ constexpr uint32_t desc_high(uint32_t eight_rows) { return (eight_rows >> 4) | (1u << 14) | (2u << 29); }
+template <uint32_t A_HIGH, uint32_t B_HIGH>
 __device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %7};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHigh)
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "n"(A_HIGH), "n"(B_HIGH)
       : "memory");
 }
+template <uint32_t B_HIGH>
 __device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -102,7 +105,7 @@ __device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a_
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
       "mov.b64 b, {%2, %6};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHigh)
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "n"(B_HIGH)
       : "memory");
 }
 __device__ __forceinline__ void commit_to(uint32_t elected, uint64_t* bar) {
@@ -343,8 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&fulls[st], L::STAGE);
         __syncwarp();
         if (lane < PAGES)
-          for (int c = 0; c < HD / 64; ++c)
-            tma_load_4d(sm + ring + st * L::STAGE + c * L::KCHUNK + lane * 2048, map, c * 64, 0, w.kvh, blk, &fulls[st]);
+          tma_load_4d(sm + ring + st * L::STAGE + lane * 2 * L::EIGHT, map, 0, 0, 0, (blk * a.Hkv + w.kvh) * 2, &fulls[st]);
         ++loads;
         return true;
       };
@@ -375,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idS = idesc_bf16_f32(128, KT), idO = idesc_bf16_f32(128, HD, true);
     const uint32_t elected = elect_lane();
     const uint32_t q_low = desc_low(smem_addr(sm), 16);
-    const uint32_t k_low = desc_low(smem_addr(sm + L::K0), 16), v_low = desc_low(smem_addr(sm + L::V0), L::KCHUNK);
+    const uint32_t k_low = desc_low(smem_addr(sm + L::K0), 16), v_low = desc_low(smem_addr(sm + L::V0), 1024);
+    constexpr uint32_t q_high = desc_high(1024), kv_high = desc_high(L::EIGHT);
     uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // stages and phases of the rings
     auto advance = [](uint32_t& st, uint32_t& ph, uint32_t stages) {
       if (++st == stages) st = 0, ph ^= 1;
@@ -394,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q = q_low + x * (L::QTILE >> 4), k = k_low + kst * (L::STAGE >> 4), d = tmem + L::S0 + sb * KT;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss(elected, d, q + ((kk / 4 * L::QCHUNK + kk % 4 * 32) >> 4), k + ((kk / 4 * L::KCHUNK + kk % 4 * 32) >> 4), idS,
+          mma_ss<q_high, kv_high>(elected, d, q + ((kk / 4 * L::QCHUNK + kk % 4 * 32) >> 4),
+                                  k + ((kk / 4 * 1024 + kk % 4 * 32) >> 4), idS,
                  kk ? 1u : 0u);
         commit_to(elected, &bar.s_full[sb]);
         if (done) {
@@ -414,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts(elected, tmem + x * HD, p + kk * 8, v + (kk * 2048 >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
+          mma_ts<kv_high>(elected, tmem + x * HD, p + kk * 8, v + (kk * 2 * L::EIGHT >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
         if constexpr (KT == 128) {
           commit_to(elected, &bar.pv_half[x]);
           if (more && !wait(&bar.k_full[kst], kph)) return false;
           if (!wait(&bar.p_full[sb], pph[sb])) return false;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 4; kk < 8; ++kk) mma_ts(elected, tmem + x * HD, p + kk * 8, v + (kk * 2048 >> 4), idO, 1u);
+          for (int kk = 4; kk < 8; ++kk) mma_ts<kv_high>(elected, tmem + x * HD, p + kk * 8, v + (kk * 2 * L::EIGHT >> 4), idO, 1u);
         }
         pph[sb] ^= 1;
         commit_to(elected, &bar.pv_done[x]);
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((c >= h0 && c < h1) || c >= end)
 #pragma unroll
                 for (int k = 0; k < HD / 64; ++k)
-                  *reinterpret_cast<uint4*>(v + k * L::KCHUNK + row * 128 + r % 8 * 16) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(v + row / 8 * L::EIGHT + k * 1024 + row % 8 * 128 + r % 8 * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async();
           }
@@ -750,9 +754,11 @@ cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float*
     if (!make_map_bf16_sw128(&mQ, a.q, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
   {
-    const cuuint64_t dims[4] = {(cuuint64_t)HD, 16, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_blocks};
-    const cuuint64_t strides[3] = {(cuuint64_t)HD * 2, (cuuint64_t)16 * HD * 2, (cuuint64_t)a.Hkv * 16 * HD * 2};
-    const cuuint32_t box[4] = {64, 16, 1, 1};
+    // A page of a head, 16 keys, in one copy: eight keys by eight keys, each 64 columns by 64 columns.  With a copy for
+    // each 64 columns the copies' number was the limit: 77 cycles each, 27 bytes a cycle on an SM; 4 KB at a time 38, 8 KB 50.
+    const cuuint64_t dims[4] = {64, 8, HD / 64, (cuuint64_t)a.num_blocks * a.Hkv * 2};
+    const cuuint64_t strides[3] = {(cuuint64_t)HD * 2, 128, (cuuint64_t)8 * HD * 2};
+    const cuuint32_t box[4] = {64, 8, HD / 64, 2};
     if (!make_map_bf16_sw128(&mK, a.k_cache, 4, dims, strides, box)) return cudaErrorInvalidValue;
     if (!make_map_bf16_sw128(&mV, a.v_cache, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
