@@ -29,6 +29,11 @@ __device__ __forceinline__ Seen seen_by(const WinAttnArgs& a, int P, int n) {
 
 constexpr int kSms = 152;
 
+// a / b of numbers that hardly ever need 64 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // The costs of all sequences, Hkv times each, lie one behind the other; CTA i of the grid takes the i-th of equal runs of
 // at least `least`.
 struct Run {
@@ -78,7 +83,7 @@ __device__ __forceinline__ bool find_run(const WinAttnArgs& a, const long long* 
     if (few) tokens_of(b, start, n, P);
   }
   const long long total = scan(mine, upto);
-  r.per = (total + gridDim.x - 1) / gridDim.x;
+  r.per = quotient(total + gridDim.x - 1, gridDim.x);
   if (r.per < least) r.per = least;
   r.x0 = blockIdx.x * r.per, r.x1 = min(total, r.x0 + r.per);
   if (r.x0 >= r.x1) return false;

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD))
       start = a.cu != nullptr ? a.cu[b] : b;
       q = seen_by(a, a.prefix_len[b], a.cu != nullptr ? a.cu[b + 1] - start : 1);
     }
-    const int kvh = (int)((x - base) / q.pages);
+    const int kvh = (int)quotient(x - base, q.pages);
     const long long u0 = base + (long long)kvh * q.pages, u1 = u0 + q.pages;
     // a short unit goes whole to the run that it starts in
     const bool uncut = q.pages <= kWhole;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD))
     }
     __syncthreads();
     const bool alone = p0 == 0 && p1 == q.pages;
-    const long long c0 = u0 / per, c1 = (u1 - 1) / per;  // the CTAs that share the unit
+    const long long c0 = quotient(u0, per), c1 = quotient(u1 - 1, per);  // the CTAs that share the unit
     // a CTA's first unit goes to its slot 0, a later one that runs past its end to slot 1
     auto slot_of = [&](long long c) { return slots + (2 * c + (c * per < u0 ? 1 : 0)) * kSlot; };
     auto put = [&](int r, int c, const float* v) {

@@ -28,7 +28,7 @@ constexpr int kRows = 128;
 constexpr int kThreads = 352;
 constexpr int kUnits = 4;       // units known ahead
 constexpr int kWhole = 6;       // key tiles of a unit that is never cut: a cut costs about as much
-constexpr int kLeast = 4;       // cost of a run, at least: a unit of two key tiles
+constexpr int kLeast = 3;       // cost of a run, at least: no two units begin in a shorter one
 constexpr float kRaise = 8.0f;     // log2
 constexpr float kMost = 65536.f;   // of 64 weights, as sums against the maximum held
 
@@ -202,7 +202,7 @@ struct Walk {
     u.b = run.b;
     start = run.start, n = run.n, P = run.P, t = 0;
     const long long c = cost[u.b];
-    u.kvh = (int)((run.x0 - run.base) / c);
+    u.kvh = (int)quotient(run.x0 - run.base, c);
     u0 = run.base + u.kvh * c;
     // a unit a lane, 32 at a time
     for (;;) {
@@ -228,7 +228,7 @@ struct Walk {
     while (u0 < run.x1 && u.first >= u.last) step();
     u.more = u0 < run.x1;
     const long long k0 = u0 + kUnitCost;
-    u.c0 = (int)(k0 / run.per), u.c1 = (int)((k0 + u.tiles - 1) / run.per);
+    u.c0 = (int)quotient(k0, run.per), u.c1 = (int)quotient(k0 + u.tiles - 1, run.per);
   }
   __device__ void step() {
     u0 += kUnitCost + u.tiles;
