@@ -177,6 +177,8 @@ def _rows(name: str, t, shape, dtype, row: int):
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else row
 
 
+# The current device without torch's check that CUDA is up (it is, where a tensor lies on it).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # The current stream's handle without building a Stream object (3 us of a small call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -505,21 +507,21 @@ def _dense(t, shape, dtype, device: int, name: str):
     """Pointer of a dense tensor on the current device (the calls launch on its stream)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
-        _refuse_here(name, t, shape, dtype, device)
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse_here(name, t, shape, dtype, device)
 
 
 def _heads(t, shape, dtype, device: int, row: int, name: str):
     """Pointer and token stride of [tokens, heads, hd] on the current device, the tokens' rows dense."""
     if t is None:
         return None, row
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
-        _refuse_here(name, t, shape, dtype, device)
-    stride = t.stride()
-    if stride[2] != 1 or stride[1] != shape[2]:
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape:
+        apart, head, column = t.stride()
+        if column == 1 and head == shape[2]:
+            return t.data_ptr(), apart if shape[0] > 1 else row
         return _rows(name, t, shape, dtype, row)
-    return t.data_ptr(), stride[0] if shape[0] > 1 else row
+    _refuse_here(name, t, shape, dtype, device)
 
 
 def _refuse_here(name: str, t, shape, dtype, device: int):
@@ -533,7 +535,7 @@ def _refuse_here(name: str, t, shape, dtype, device: int):
 def _current(t, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors passed to the library must be CUDA tensors")
-    return torch.cuda.current_device()
+    return _current_device()
 
 
 def tv_qk_norm_rope(q, k, q_out, prefix_len, err, *, k_out=None, v=None, k_cache=None, v_cache=None, block_table=None,
@@ -580,34 +582,6 @@ def tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, window
     return int(lib.tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, max_blocks, block_size, window, sinks))
 
 
-def _window_attn(name, q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, live, out, err, window, sinks, max_len,
-                 workspace, sm_scale, stream):
-    device, bf, whole = _current(q, "q"), torch.bfloat16, torch.int32
-    T, Hq, hd = q.shape
-    blocks, Hkv, bs, _ = k_cache.shape
-    B, most = block_table.shape
-    cache = (blocks, Hkv, bs, hd)
-    tokens = (T if cu_seqlens is not None else B, Hq, hd)
-    pq, sq = _heads(q, tokens, bf, device, Hq * hd, "q")
-    po, so = _heads(out, tokens, bf, device, Hq * hd, "out")
-    if workspace is None:
-        size = lib.tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, most, bs, window, sinks)
-        workspace = _scratch(size, q.device, stream)
-        room = None if workspace is None else workspace.data_ptr()
-    else:
-        size, room = workspace.numel() * workspace.element_size(), _ptr(workspace)
-    head = (pq, sq, _dense(k_cache, cache, bf, device, "k_cache"), _dense(v_cache, cache, bf, device, "v_cache"), blocks,
-            _dense(block_table, (B, most), whole, device, "block_table"), most)
-    prefix = _dense(prefix_len, (B,), whole, device, "prefix_len")
-    tail = (Hq, Hkv, hd, bs, window, sinks, hd ** -0.5 if sm_scale is None else sm_scale, po, so, room, size,
-            _dense(err, (B,), whole, device, "err"), _stream(stream))
-    if cu_seqlens is not None:
-        _check(lib.tv_window_attn_prompt(*head, _dense(cu_seqlens, (B + 1,), whole, device, "cu_seqlens"), prefix, B, T,
-                                         max_len, *tail), name)
-    else:
-        _check(lib.tv_window_attn_step(*head, prefix, _dense(live, (B,), whole, device, "live"), B, *tail), name)
-
-
 def tv_window_attn_prompt(q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, out, err, window: int = 0,
                           sinks: int = 0, max_len: int | None = None, workspace=None, sm_scale: float | None = None,
                           stream=None) -> None:
@@ -615,16 +589,55 @@ def tv_window_attn_prompt(q, k_cache, v_cache, block_table, cu_seqlens, prefix_l
     tokens, over the paged cache that already holds their keys: key j for the query at position p if j <= p and
     (p - j < window, or j < sinks); window 0: every j <= p.  out [T, Hq, hd]; token strides free.  Without a
     ``workspace`` one is taken from torch's allocator when the call needs it."""
-    _window_attn("tv_window_attn_prompt", q, k_cache, v_cache, block_table, cu_seqlens, prefix_len, None, out, err, window,
-                 sinks, q.shape[0] if max_len is None else int(max_len), workspace, sm_scale, stream)
+    device, bf, whole = _current(q, "q"), torch.bfloat16, torch.int32
+    tokens, cache = q.shape, k_cache.shape
+    T, Hq, hd = tokens
+    blocks, Hkv, bs, _ = cache
+    B, most = block_table.shape
+    if cache[3] != hd:
+        raise ValueError(f"k_cache: expected heads of {hd} columns, got {cache[3]}")
+    max_len = T if max_len is None else int(max_len)
+    if workspace is None:
+        size = lib.tv_window_attn_workspace_size(B, T, max_len, Hq, Hkv, hd, most, bs, window, sinks)
+        workspace = _scratch(size, q.device, stream)
+        room = None if workspace is None else workspace.data_ptr()
+    else:
+        size, room = workspace.numel() * workspace.element_size(), _ptr(workspace)
+    pq, sq = _heads(q, tokens, bf, device, Hq * hd, "q")
+    po, so = _heads(out, tokens, bf, device, Hq * hd, "out")
+    _check(lib.tv_window_attn_prompt(
+        pq, sq, _dense(k_cache, cache, bf, device, "k_cache"), _dense(v_cache, cache, bf, device, "v_cache"), blocks,
+        _dense(block_table, (B, most), whole, device, "block_table"), most,
+        _dense(cu_seqlens, (B + 1,), whole, device, "cu_seqlens"), _dense(prefix_len, (B,), whole, device, "prefix_len"), B, T,
+        max_len, Hq, Hkv, hd, bs, window, sinks, hd ** -0.5 if sm_scale is None else sm_scale, po, so, room, size,
+        _dense(err, (B,), whole, device, "err"), _stream(stream)), "tv_window_attn_prompt")
 
 
 def tv_window_attn_step(q, k_cache, v_cache, block_table, prefix_len, out, err, window: int = 0, sinks: int = 0,
                         live=None, workspace=None, sm_scale: float | None = None, stream=None) -> None:
     """The same for one new token of every sequence, q and out [B, Hq, hd], at position prefix_len [B]; sequences with
     live[b] = 0 are left alone."""
-    _window_attn("tv_window_attn_step", q, k_cache, v_cache, block_table, None, prefix_len, live, out, err, window, sinks, 1,
-                 workspace, sm_scale, stream)
+    device, bf, whole = _current(q, "q"), torch.bfloat16, torch.int32
+    tokens, cache = q.shape, k_cache.shape
+    B, Hq, hd = tokens
+    blocks, Hkv, bs, _ = cache
+    most = block_table.shape[1]
+    if cache[3] != hd:
+        raise ValueError(f"k_cache: expected heads of {hd} columns, got {cache[3]}")
+    if workspace is None:
+        size = lib.tv_window_attn_workspace_size(B, B, 1, Hq, Hkv, hd, most, bs, window, sinks)
+        workspace = _scratch(size, q.device, stream)
+        room = None if workspace is None else workspace.data_ptr()
+    else:
+        size, room = workspace.numel() * workspace.element_size(), _ptr(workspace)
+    pq, sq = _heads(q, tokens, bf, device, Hq * hd, "q")
+    po, so = _heads(out, tokens, bf, device, Hq * hd, "out")
+    _check(lib.tv_window_attn_step(
+        pq, sq, _dense(k_cache, cache, bf, device, "k_cache"), _dense(v_cache, cache, bf, device, "v_cache"), blocks,
+        _dense(block_table, (B, most), whole, device, "block_table"), most,
+        _dense(prefix_len, (B,), whole, device, "prefix_len"), _dense(live, (B,), whole, device, "live"), B, Hq, Hkv, hd, bs,
+        window, sinks, hd ** -0.5 if sm_scale is None else sm_scale, po, so, room, size,
+        _dense(err, (B,), whole, device, "err"), _stream(stream)), "tv_window_attn_step")
 
 
 def tv_accept_sample(parents, draft_tokens, target_probs, draft_probs, uniforms, accepted_path, accepted_len, next_token,
