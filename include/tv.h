@@ -697,8 +697,8 @@ TV_API int tv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64
  * some query sees may reach other queries of its sequence and KV head; one that no query of the
  * sequence sees reaches none.
  * Supported: hd in {64, 128, 256}; block_size = 16; Hq a multiple of Hkv, Hq / Hkv <= 128; window and
- * sinks from 0; sequences up to 2^30 tokens.  Strides: at least the dense row and whole multiples of
- * 16 bytes.  max_blocks * 16 <= 2^30.
+ * sinks from 0; sequences up to 2^30 tokens (max_blocks <= 2^26); num_blocks * Hkv <= 2^29;
+ * B * Hkv <= 2^24.  Strides: at least the dense row and whole multiples of 16 bytes.
  * ---------------------------------------------------------------------------------------- */
 TV_API size_t tv_window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, int hd, int max_blocks,
                                             int block_size, int window, int sinks);

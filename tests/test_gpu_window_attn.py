@@ -274,3 +274,61 @@ def test_units_of_one_and_two_row_tiles_side_by_side(hd, Hq):
         at = torch.tensor(rows, device=DEV)
         part = dict(c, q=c["q"][at], starts=list(range(len(rows))), lens=[1] * len(rows), before=before, real=c["real"][seq])
         check(part, out[at], window, sinks)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("shape", ["rising", "jumps", "falling"])
+@pytest.mark.parametrize("lens,prefix,Hq,step", [([300, 20], [100, 400], 4, False), ([2, 90], [700, 333], 8, False),
+                                                 ([1, 1, 1], [50, 500, 1000], 4, True)])
+def test_scores_that_outgrow_the_maximum_held(hd, shape, lens, prefix, Hq, step):
+    # scores that climb by more than fp32 could hold against an early maximum, by steps inside and between tiles
+    c = case(lens, prefix, Hq, 2, hd, seed=17, scale=0.1, step=step, poison=False)
+    u = torch.randn(hd, generator=torch.Generator().manual_seed(1)).sign()
+    c["q"] = (c["q"].float().cpu() + u).to(BF).to(DEV)
+    jumps = np.array([70, 100, 129, 200, 333, 600])
+    for b, (p, n) in enumerate(zip(prefix, lens)):
+        at = np.arange(p + n)
+        size = {"rising": at * 1.0, "falling": 1000.0 - at, "jumps": 40.0 * np.searchsorted(jumps, at)}[shape]
+        block, row = torch.tensor(c["real"][b][at // 16], device=DEV).long(), torch.tensor(at % 16, device=DEV).long()
+        k = 0.05 * torch.randn(len(at), 2, hd, generator=torch.Generator().manual_seed(b))
+        k += torch.tensor(size, dtype=torch.float32)[:, None, None] * hd ** -0.5 * u
+        c["k"][block, :, row] = k.to(BF).to(DEV)
+    for window, sinks in ((0, 0), (150, 70)):
+        out, err = attend(c, window, sinks)
+        assert not any(err)
+        check(c, out, window, sinks)
+
+
+@pytest.mark.parametrize("step", [True, False])
+def test_more_sequences_than_threads(step):
+    rng = np.random.default_rng(18)
+    B = 500
+    lens = [1] * B if step else [int(x) for x in rng.choice([0, 1, 3, 5], size=B)]
+    prefix = [int(x) for x in rng.integers(0, 200, size=B)]
+    live = rng.random(B) < 0.8
+    c = case(lens, prefix, 16, 2, 64, seed=18, step=step)
+    out, err = attend(c, 90, 2, live=whole(live) if step else None, max_len=max(lens))
+    assert not any(err)
+    want = oracle(c, 90, 2)
+    rows = np.nonzero(live)[0] if step else np.arange(sum(lens))
+    check(c, out, 90, 2, rows=rows, want=want)
+    if step:
+        assert (out[torch.tensor(~live, device=DEV)] == 7).all()
+
+
+def test_two_calls_on_two_streams_at_once():
+    cases = [case([200, 40], [60, 300], 8, 2, 128, seed=19), case([1] * 4, [900, 20, 1500, 333], 8, 2, 128, seed=20, step=True)]
+    want = [attend(c, 400, 3)[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [torch.full_like(w, 7.0) for w in want]
+    errs = [torch.full((len(c["lens"]),), 9, dtype=torch.int32, device=DEV) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, out, err in zip(cases, streams, outs, errs):
+            if c["step"]:
+                tv.tv_window_attn_step(c["q"], c["k"], c["v"], c["table"], c["prefix"], out, err, window=400, sinks=3, stream=s)
+            else:
+                tv.tv_window_attn_prompt(c["q"], c["k"], c["v"], c["table"], c["cu"], c["prefix"], out, err, window=400, sinks=3,
+                                         stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want)) and not any(e.any() for e in errs)

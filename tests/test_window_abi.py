@@ -54,7 +54,7 @@ COMMON = [
     (BAD, dict(prefix=None)), (BAD, dict(B=0)), (BAD, dict(Hq=5)), (BAD, dict(Hkv=0)), (NONE, dict(hd=96)), (NONE, dict(bs=8)),
     (BAD, dict(window=-1)), (BAD, dict(sinks=-1)), (BAD, dict(scale=NAN)), (BAD, dict(scale=INF)), (BAD, dict(out=None)),
     (BAD, dict(qs=511)), (BAD, dict(qs=516)), (BAD, dict(os=256)), (BAD, dict(err=None)),
-    (NONE, dict(Hq=258, qs=1 << 16, os=1 << 16)), (NONE, dict(Hq=1 << 17, Hkv=1 << 17, qs=1 << 25, os=1 << 25)),
+    (NONE, dict(Hq=258, qs=1 << 16, os=1 << 16)), (NONE, dict(blocks=1 << 30)), (NONE, dict(B=1 << 24)), (NONE, dict(Hq=1 << 17, Hkv=1 << 17, qs=1 << 25, os=1 << 25)),
 ]
 
 

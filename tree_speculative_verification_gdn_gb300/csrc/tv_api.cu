@@ -511,7 +511,8 @@ int window_attn_common(const void* q, int64_t q_stride, const void* k_cache, con
       !isfinite(sm_scale))
     return TV_ERR_INVALID_ARG;
   if (!head_ok(hd) || block_size != TV_BLOCK_SIZE || Hq / Hkv > 128 || max_blocks > (1 << 26)) return TV_ERR_UNSUPPORTED;
-  if (Hq > (1 << 16) || (long long)B * Hkv > (1 << 24)) return TV_ERR_UNSUPPORTED;
+  if (Hq > (1 << 16) || (long long)B * Hkv > (1 << 24) || (long long)num_blocks * Hkv > (1 << 29))
+    return TV_ERR_UNSUPPORTED;
   if (!rows_ok(q_stride, (int64_t)Hq * hd, TV_BF16) || !rows_ok(out_stride, (int64_t)Hq * hd, TV_BF16))
     return TV_ERR_INVALID_ARG;
   return TV_OK;
