@@ -743,7 +743,7 @@ TV_API int tv_window_attn_step(const void* q, int64_t q_stride, const void* k_ca
  * Without a child accepted, or once Lmax nodes are, next_token is the smallest x with
  *     R(0) + ... + R(x) > uniforms[0] * sum R        (R is p where nothing was refused, or sum R = 0).
  * Probabilities are taken as they are, negative ones and NaN as 0.  A token outside [0, V) is never
- * accepted.  All sums are carried to 2^-44 of their value or better.  A chain is a tree too, and N = 1
+ * accepted.  All sums, and products of numbers above 2^-100, are carried to 2^-44 or better.  A chain is a tree too, and N = 1
  * draws one token from target_probs.
  *
  *   parents, draft_tokens [B, N] int32     in   as tv_accept_walk

@@ -5,9 +5,9 @@
 // A_k = M_0 + ... + M_{k-1}: one scalar stands for the state, and a refusal costs one pass over the rows p and q.
 // Where q is not known, refused tokens are left out of p instead, and no pass is needed before the draw.
 //
-// A token next to a border decides, so sums are carried as two floats each (p - A q by exact differences and products,
-// sums by exact additions, about 2^-46), joined in doubles; a double per element would cost more than the row's bytes:
-// this chip adds two doubles a clock on an SM.
+// A token next to a border decides, so sums are carried as two floats each: p - A q by exact differences and products, sums
+// by exact additions, about 2^-46.  Doubles would cost more than the row's bytes, two additions a clock on an SM, and their
+// latency most of a short call.
 //
 // A cluster of up to eight CTAs takes a sequence, each an equal part of a row, each of its 16 warps a run of that part.
 // Every CTA walks the tree by itself on the same sums.  The draw finds the warp's run from the runs' sums, and its
@@ -33,27 +33,72 @@ __device__ __forceinline__ void add(Pair& acc, Pair x) {
   acc.hi = t;
   acc.lo = __fadd_rn(acc.lo, __fadd_rn(e, x.lo));
 }
+__device__ __forceinline__ Pair sum_of(Pair a, Pair b) {  // with lo small against hi again
+  add(a, b);
+  const float t = __fadd_rn(a.hi, a.lo);
+  return Pair{t, __fsub_rn(a.lo, __fsub_rn(t, a.hi))};
+}
+__device__ __forceinline__ Pair product(float f, Pair x) {
+  const float y = __fmul_rn(f, x.hi);
+  return Pair{y, __fadd_rn(__fmaf_rn(f, x.hi, -y), __fmul_rn(f, x.lo))};
+}
+__device__ __forceinline__ bool less(Pair a, Pair b) {
+  const float d = __fsub_rn(a.hi, b.hi);
+  const float t = __fsub_rn(d, a.hi);
+  const float e = __fsub_rn(__fsub_rn(a.hi, __fsub_rn(d, t)), __fadd_rn(b.hi, t));
+  return __fadd_rn(d, __fadd_rn(e, __fsub_rn(a.lo, b.lo))) < 0.f;
+}
 // max(p - A q, 0)
 __device__ __forceinline__ Pair left_of(float p, float q, Pair A) {
-  const float y = __fmul_rn(A.hi, q);
-  const float ye = __fadd_rn(__fmaf_rn(A.hi, q, -y), __fmul_rn(A.lo, q));
-  const float d = __fsub_rn(p, y);
+  const Pair y = product(q, A);
+  const float d = __fsub_rn(p, y.hi);
   const float b = __fsub_rn(d, p);
-  const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(y, b)), ye);
+  const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(y.hi, b)), y.lo);
   return __fadd_rn(d, e) > 0.f ? Pair{d, e} : Pair{0.f, 0.f};
 }
-__device__ __forceinline__ double whole(Pair x) { return (double)x.hi + (double)x.lo; }
-
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+// The first refusal at a node, A = 1: where p > q the error of p - q takes two steps, and elsewhere nothing is left.
+__device__ __forceinline__ Pair left_of(float p, float q) {
+  const float d = __fsub_rn(p, q);
+  const float e = __fsub_rn(__fsub_rn(p, d), q);
+  return d > 0.f ? Pair{d, e} : Pair{0.f, 0.f};
 }
+// Two sums side by side in packed registers.
+struct Pair2 {
+  float2 hi, lo;
+};
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
+__device__ __forceinline__ void add(Pair2& acc, Pair x, Pair y) {
+  const float2 v = make_float2(x.hi, y.hi);
+  const float2 t = __fadd2_rn(acc.hi, v);
+  const float2 b = minus(t, acc.hi);
+  const float2 e = __fadd2_rn(minus(acc.hi, minus(t, b)), minus(v, b));
+  acc.hi = t;
+  acc.lo = __fadd2_rn(acc.lo, __fadd2_rn(e, make_float2(x.lo, y.lo)));
+}
+
 __device__ __forceinline__ Pair warp_sum(Pair x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
   return x;
+}
+// Over the lanes up to this one.
+template <int LANES>
+__device__ __forceinline__ Pair warp_scan(Pair x) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    const Pair y{__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+    if ((int)(threadIdx.x % 32) >= o) x = sum_of(y, x);
+  }
+  return x;
+}
+__device__ __forceinline__ Pair of_lane(Pair x, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, x.hi, lane), __shfl_sync(0xffffffffu, x.lo, lane)};
+}
+// Of the lane before, 0 in the first.
+__device__ __forceinline__ Pair before_lane(Pair x) {
+  const Pair y{__shfl_up_sync(0xffffffffu, x.hi, 1), __shfl_up_sync(0xffffffffu, x.lo, 1)};
+  return threadIdx.x % 32 == 0 ? Pair{0.f, 0.f} : y;
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -75,8 +120,6 @@ struct Rows {  // rows p and q of a node, in vectors of 16 bytes from the bounda
 #pragma unroll
       for (int i = 0; i < VE; ++i) x[i] = e + i >= 0 && e + i < V ? to_f32(row[e + i]) : 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = fmaxf(x[i], 0.f);  // NaN too
   }
 };
 
@@ -87,11 +130,11 @@ struct Ask {
   int refused;  // tokens left out
   int draw;     // 0: another pass; 1: the draw, from the last pass's sums; < 0: a status to report
   int run;      // the draw's run; the sum in front of it, and the number to pass (none: the last token with any)
-  double ahead, want;
+  Pair ahead, want;
   int found;
 };
 
-// kParts CTAs a sequence.  All doubles are one warp's: sixteen warps' would take longer than the row.
+// kParts CTAs a sequence.
 template <typename T, int kParts>
 __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2) accept_sample_kernel(SampleArgs a) {
   constexpr int VE = Rows<T>::VE;
@@ -123,7 +166,7 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
   // The walk: the whole of warp 0 keeps the same state.
   int node = 0, count = 1, at = 0;     // at: the last child looked at
   int left_out = 0, parity = 0;
-  double A = 0.0, mass = 1.0;
+  Pair A{0.f, 0.f}, mass{1.f, 0.f};
   bool have = false;  // mass is the sum of the last pass
   if (tid == 0) path[0] = 0;
   // On to the next pass, or to the draw.
@@ -136,23 +179,23 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
           const int c = base + __ffs(kids) - 1;
           kids &= kids - 1;
           if (draft != nullptr) {
-            if ((double)u[c] * (double)qt[c] * mass < fmax((double)pt[c] - A * (double)qt[c], 0.0)) {
+            if (less(product(u[c], product(qt[c], mass)), left_of(pt[c], qt[c], A))) {
               went = c;
               break;
             }
             at = c;
-            A += mass;
+            A = sum_of(A, mass);
             ask.draw = 0;
             return;  // for the sum of what is left
           }
           bool twice = false;
           for (int k = lane; k < left_out; k += 32) twice |= refused[k] == tok[c];
-          const double rx = __any_sync(0xffffffffu, twice) ? 0.0 : (double)pt[c];
-          if ((double)u[c] * mass < rx) {
+          const float rx = __any_sync(0xffffffffu, twice) ? 0.f : pt[c];
+          if (less(product(u[c], mass), Pair{rx, 0.f})) {
             went = c;
             break;
           }
-          mass -= rx;
+          mass = sum_of(mass, Pair{-rx, 0.f});
           if (lane == 0) refused[left_out] = tok[c];
           __syncwarp();
           ++left_out;
@@ -162,23 +205,27 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
       node = at = went;
       if (lane == 0) path[count] = node;
       ++count;
-      A = 0.0, mass = 1.0, have = false, left_out = 0;
+      A = Pair{0.f, 0.f}, mass = Pair{1.f, 0.f}, have = false, left_out = 0;
     }
     ask.draw = have ? 1 : 0;
     at = N;  // no child is left to look at
   };
   // With the last pass's sums: goes on, or finds the run that the drawn token lies in.
   auto take = [&]() {
-    double own[kOwn], before = 0.0;
+    Pair own[kOwn], all{0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) before += own[k] = lane * kOwn + k < kRuns ? whole(sums[parity][lane * kOwn + k]) : 0.0;
-    mass = warp_sum(before);
+    for (int k = 0; k < kOwn; ++k) {
+      own[k] = lane * kOwn + k < kRuns ? sums[parity][lane * kOwn + k] : Pair{0.f, 0.f};
+      all = sum_of(all, own[k]);
+    }
+    const Pair upto = warp_scan<32>(all);
+    mass = of_lane(upto, 31);
     have = true;
-    if (!(mass > 0.0)) {
+    if (!(mass.hi > 0.f)) {
       if (at < N) {  // nothing is left: the next child is held against p again
-        A = 0.0, mass = 1.0, have = false;
-      } else if (A != 0.0 || left_out != 0) {
-        A = 0.0, left_out = 0;
+        A = Pair{0.f, 0.f}, mass = Pair{1.f, 0.f}, have = false;
+      } else if (A.hi != 0.f || left_out != 0) {
+        A = Pair{0.f, 0.f}, left_out = 0;
         ask.draw = 0;
         return;
       } else {
@@ -191,40 +238,33 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
       if (at < N || !have) return;
       ask.draw = 1;
     }
-    const double want = (double)u[0] * mass, all = before;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += x;
-    }
-    double upto = before - all, ahead = 0.0;  // of the runs in front of this lane's
+    const Pair want = product(u[0], mass);
+    Pair to = before_lane(upto), ahead{0.f, 0.f};
     int run = kRuns, last = -1;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-      if (own[k] > 0.0) last = lane * kOwn + k;
-      if (run == kRuns && own[k] > 0.0 && upto + own[k] > want) run = lane * kOwn + k, ahead = upto;
-      upto += own[k];
+      const Pair next = sum_of(to, own[k]);
+      if (own[k].hi > 0.f) last = lane * kOwn + k;
+      if (run == kRuns && own[k].hi > 0.f && less(want, next)) run = lane * kOwn + k, ahead = to;
+      to = next;
     }
     const unsigned found = __ballot_sync(0xffffffffu, run < kRuns);
     if (found != 0) {
       run = __shfl_sync(0xffffffffu, run, __ffs(found) - 1);
-      ahead = __shfl_sync(0xffffffffu, ahead, __ffs(found) - 1);
+      ahead = of_lane(ahead, __ffs(found) - 1);
     } else {  // rounding, or a number past 1: the last token with a probability
       run = __reduce_max_sync(0xffffffffu, last);
     }
     ask.run = run, ask.ahead = ahead, ask.want = want, ask.found = found != 0;
   };
-  auto tell = [&]() {
-    ask.node = node, ask.refused = left_out;
-    ask.A = Pair{(float)A, (float)(A - (double)(float)A)};
-  };
+  auto tell = [&]() { ask.node = node, ask.refused = left_out, ask.A = A; };
 
   Rows<T> r;
   r.V = V;
   int v0 = 0, v1 = 0;  // this warp's run of vectors
   bool some = false;   // it holds a token that was left out of p
   Pair Ap{0.f, 0.f};
-  bool use_q = false;
+  int form = 0;        // of what is left: p, p - q, p - A q
   auto listen = [&]() {
     r.p = target + (long long)ask.node * V;
     r.q = draft != nullptr ? draft + (long long)ask.node * V : nullptr;
@@ -239,22 +279,40 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
     }
     some = __any_sync(0xffffffffu, in);
     Ap = ask.A;
-    use_q = Ap.hi != 0.f;
+    form = Ap.hi == 0.f ? 0 : Ap.hi == 1.f && Ap.lo == 0.f ? 1 : 2;
   };
-  // R of vector j, as pairs
-  auto left = [&](int j, Pair* x) {
+  // R of vector j, as pairs; negative probabilities and NaN count as 0
+  auto left = [&](int form, int j, Pair* x) {
     const int e = j * VE - r.phase;
     float p[VE], q[VE];
     Rows<T>::vector(r.p, e, V, p);
-    if (use_q) Rows<T>::vector(r.q, e, V, q);
+    if (form != 0) Rows<T>::vector(r.q, e, V, q);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = use_q ? left_of(p[i], q[i], Ap) : Pair{p[i], 0.f};
+    for (int i = 0; i < VE; ++i)
+      x[i] = form == 0 ? Pair{fmaxf(p[i], 0.f), 0.f}
+             : form == 1 ? left_of(p[i], fmaxf(q[i], 0.f)) : left_of(p[i], fmaxf(q[i], 0.f), Ap);
     for (int k = 0; some && k < ask.refused; ++k) {
       const int at = refused[k] - e;
 #pragma unroll
       for (int i = 0; i < VE; ++i)
         if (i == at) x[i] = Pair{0.f, 0.f};
     }
+  };
+  // The sum of a run, in each of the three forms a loop of its own.
+  auto run_sum = [&]() -> Pair {
+    auto loop = [&](auto form) -> Pair {
+      Pair2 acc{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 4
+      for (int j = v0 + lane; j < v1; j += 32) {
+        Pair x[VE];
+        left(form(), j, x);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) add(acc, x[i], x[i + 1]);
+      }
+      return warp_sum(sum_of(Pair{acc.hi.x, acc.lo.x}, Pair{acc.hi.y, acc.lo.y}));
+    };
+    if (form == 0) return loop([] { return 0; });
+    return form == 1 ? loop([] { return 1; }) : loop([] { return 2; });
   };
 
   if (warp == 0) {
@@ -269,15 +327,7 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
   // Every CTA of the cluster makes the same passes, on the same sums.
   while (ask.draw == 0) {
     listen();
-    Pair acc{0.f, 0.f};
-#pragma unroll 4
-    for (int j = v0 + lane; j < v1; j += 32) {
-      Pair x[VE];
-      left(j, x);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) add(acc, x[i]);
-    }
-    acc = warp_sum(acc);
+    const Pair acc = run_sum();
     parity ^= 1;
     if (lane < kParts) cluster_st_pair(cluster_map(smem_addr(&sums[parity][rank * kWarps + warp]), lane), acc);
     cluster_sync();
@@ -309,38 +359,27 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
     some = ask.refused > 0;
   }
   __shared__ Pair parts[kWarps];
-  Pair acc{0.f, 0.f};
-  for (int j = v0 + lane; j < v1; j += 32) {
-    Pair x[VE];
-    left(j, x);
-#pragma unroll
-    for (int i = 0; i < VE; ++i) add(acc, x[i]);
-  }
-  acc = warp_sum(acc);
+  const Pair acc = run_sum();
   if (lane == 0) parts[warp] = acc;
   __syncthreads();
-  double ahead = ask.ahead;
-  const double want = ask.want;
+  const Pair want = ask.want;
   if (warp == 0) {
-    const double own = lane < kWarps ? whole(parts[lane]) : 0.0;
-    double to = own;
-#pragma unroll
-    for (int o = 1; o < kWarps; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, to, o);
-      if (lane >= o) to += y;
-    }
-    const unsigned hits = __ballot_sync(0xffffffffu, ask.found != 0 && own > 0.0 && ahead + to > want);
-    const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+    const Pair own = lane < kWarps ? parts[lane] : Pair{0.f, 0.f};
+    const Pair scan = warp_scan<kWarps>(own);
+    const Pair to = sum_of(ask.ahead, scan), from = sum_of(ask.ahead, before_lane(scan));
+    const unsigned hits = __ballot_sync(0xffffffffu, ask.found != 0 && own.hi > 0.f && less(want, to));
+    const unsigned any = __ballot_sync(0xffffffffu, own.hi > 0.f);
     // no part passes it after all, by rounding: the last token of the last part with any
     const int part = hits != 0 ? __ffs(hits) - 1 : 31 - __clz((int)any);
-    const double from = ahead + __shfl_sync(0xffffffffu, to - own, part);
-    if (lane == 0) ask.run = part, ask.ahead = from, ask.found = hits != 0;
+    const Pair ahead = of_lane(from, part);
+    __syncwarp();
+    if (lane == 0) ask.run = part, ask.ahead = ahead, ask.found = hits != 0;
   }
   __syncthreads();
   if (ask.run != warp) return;
-  ahead = ask.ahead;
   // Four steps of 32 vectors at a time, so that their loads are under way together; the step that passes the number from
   // its lanes' sums, then the lane and the element.
+  Pair ahead = ask.ahead;
   int token = -1, last_token = -1;
   for (int j0 = v0; j0 < v1 && token < 0; j0 += 128) {
     Pair sum[4];
@@ -350,12 +389,12 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
       Pair x[VE];
 #pragma unroll
       for (int i = 0; i < VE; ++i) x[i] = Pair{0.f, 0.f};
-      if (j < v1) left(j, x);
+      if (j < v1) left(form, j, x);
       sum[s] = Pair{0.f, 0.f};
       int positive = -1;
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        if (x[i].hi > 0.f || x[i].lo > 0.f) positive = j * VE - r.phase + i;
+        if (x[i].hi > 0.f) positive = j * VE - r.phase + i;
         add(sum[s], x[i]);
       }
       last_token = max(last_token, __reduce_max_sync(0xffffffffu, positive));
@@ -363,31 +402,24 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kWarps * 32, 2)
     if (ask.found == 0) continue;
 #pragma unroll 1
     for (int s = 0; s < 4 && token < 0; ++s) {
-      const double own = whole(s == 0 ? sum[0] : s == 1 ? sum[1] : s == 2 ? sum[2] : sum[3]);
-      double to = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, to, o);
-        if (lane >= o) to += y;
-      }
-      if (__any_sync(0xffffffffu, ahead + to > want)) {
+      const Pair scan = warp_scan<32>(s == 0 ? sum[0] : s == 1 ? sum[1] : s == 2 ? sum[2] : sum[3]);
+      if (__any_sync(0xffffffffu, less(want, sum_of(ahead, scan)))) {
         const int j = j0 + s * 32 + lane;
         Pair x[VE];
 #pragma unroll
         for (int i = 0; i < VE; ++i) x[i] = Pair{0.f, 0.f};
-        if (j < v1) left(j, x);
-        double run_sum = ahead + (to - own);
+        if (j < v1) left(form, j, x);
+        Pair to = sum_of(ahead, before_lane(scan));
         int hit = -1;
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
-          const double v = whole(x[i]);
-          run_sum += v;
-          if (hit < 0 && v > 0.0 && run_sum > want) hit = j * VE - r.phase + i;
+          to = sum_of(to, x[i]);
+          if (hit < 0 && x[i].hi > 0.f && less(want, to)) hit = j * VE - r.phase + i;
         }
         const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0);
         if (hits != 0) token = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
       }
-      ahead += __shfl_sync(0xffffffffu, to, 31);
+      ahead = sum_of(ahead, of_lane(scan, 31));
     }
   }
   if (lane == 0) a.next_token[b] = token >= 0 ? token : last_token;
