@@ -642,11 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto slot_of = [&](int c) { return slots + (long long)(2 * c + (c == c0 ? 1 : 0)) * L::SLOT + warp * 32 * (HD + 2); };
           const float inv = 1.f / l;
           float* mine = slot_of(blockIdx.x);
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            uint32_t o[32];
-            tmem_ld32_nowait(tmem + wg * HD + lanes + c, o);
-            tmem_wait_ld();
+          auto put = [&](const uint32_t* o, int c) {
             if (!whole) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -661,6 +657,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(out + c + 8 * k) = pack8(y);
               }
             }
+          };
+          // 32 columns on their way while 32 are stored
+          const uint32_t from = tmem + wg * HD + lanes;
+          uint32_t o0[32], o1[32];
+          tmem_ld32_nowait(from, o0);
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 64) {
+            tmem_wait_ld();
+            tmem_ld32_nowait(from + c + 32, o1);
+            put(o0, c);
+            tmem_wait_ld();
+            if (c + 64 < HD) tmem_ld32_nowait(from + c + 64, o0);
+            put(o1, c + 32);
           }
           tc_fence_before();
           __syncwarp();
