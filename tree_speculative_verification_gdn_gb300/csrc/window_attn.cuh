@@ -123,7 +123,7 @@ struct TileShape {
   int tokens;  // of a unit
   int keys;    // of a tile
 };
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 4;
 TileShape window_tile_shape(int Hq, int Hkv, int hd);
 // arrived [kSms * 8], zero; slots: bytes as window_tiles_slots.
 size_t window_tiles_slots(int hd);

@@ -1,20 +1,20 @@
 // Windowed attention of many query rows -- prompts -- on the 5th-generation tensor cores.
 //
 // A unit is a run of new tokens of one sequence for one KV head; its query rows, (token, query head of the group), fill
-// tiles of 128.  Head dims 64 and 128: two tiles, 128 keys at a time, the scores of one tile made while the softmax
-// of the other runs.  Head dim 256: one tile, 64 keys at a time, scores in two buffers.  Every unit walks its visible
-// pages alone, sixteen tokens each, hidden pages between the first tokens and the window left out.  Units of all
-// sequences and KV heads lie one behind the other, each as long as its key tiles and kUnitCost more, and a persistent grid
-// takes equal runs of that, so that ragged and causal work ends together; a unit cut by a run's end leaves maximum, sum and
-// unnormalised output per row in the workspace, and the last of its CTAs joins them in the order of the runs.
+// tiles of 128: two of head dims 64 and 128, one of 256.  Every unit walks its visible pages alone, sixteen tokens each,
+// hidden pages between the first tokens and the window left out, 64 keys at a time.  Units of all sequences and KV heads lie
+// one behind the other, each as long as its key tiles and kUnitCost more, and a persistent grid takes equal runs of that, so
+// that ragged and causal work ends together; a long unit cut by a run's end leaves maximum, sum and unnormalised output per
+// row in the workspace, and the last of its CTAs joins them in the order of the runs.
 //
-// Scores S = Q K^T go to tensor memory; a thread takes a row (TMEM lane), 2^(S scale - m) as bf16 goes back over the
-// scores' columns, and O += P V reads it from there, half a tile at a time.  The sum is of the fp32 weights before their
-// rounding, whose errors average out.
-//   warps 0-3, 4-7   softmax of tile 0 and tile 1, output of each
+// Scores S = Q K^T go to tensor memory; a thread takes a row (TMEM lane) of 64 to registers and gives the buffer back, so
+// that the next scores are made while it works; 2^(S scale - m) as bf16 goes to a buffer of its own in tensor memory, and
+// O += P V reads it there.  MMAs with different accumulators need not run in order, so no buffer is written before
+// the reader of what it held has ended.  The sum is of the fp32 weights before their rounding, whose errors average out.
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, output of each (one row tile: two buffers in turn, warps 0-3)
 //   warp 8           TMA: queries, K and V tiles through a ring each
+//   warp 9, 11       MMAs of scores, of outputs: one warp for both spent longer on its waits and commits than the MMAs took
 //   warp 10          the run's units, up to four ahead
-//   warp 9           MMAs: item e of a unit is (key tile, row tile); S(e + 2) follows P V(e)
 // Values that no token of the unit sees may be anything, and 0 times that is not 0: their rows are cleared in
 // shared memory before P V.  Every wait is bounded; a role that gives up makes all leave.
 #include "tv_tma_host.h"
@@ -25,19 +25,19 @@ namespace tv {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kUnits = 4;       // units known ahead
-constexpr int kWhole = 6;       // key tiles of a unit that is never cut: a cut costs about as much
-constexpr int kLeast = 3;       // cost of a run, at least: no two units begin in a shorter one
+constexpr int kWhole = 8;       // key tiles of a unit that is never cut: a cut costs about as much
+constexpr int kLeast = kUnitCost + 1;  // cost of a run, at least: no two units begin in a shorter one
 constexpr float kRaise = 8.0f;     // log2
 constexpr float kMost = 65536.f;   // of 64 weights, as sums against the maximum held
 
 template <int HD>
 struct Shape {
   static constexpr int NT = HD == 256 ? 1 : 2;          // row tiles
-  static constexpr int KT = HD == 256 ? 64 : 128;       // keys of a tile
-  static constexpr int KS = HD == 64 ? 4 : 3;           // K tiles in their ring
-  static constexpr int VS = HD == 64 ? 4 : 2;           // V tiles in theirs
+  static constexpr int KT = 64;                         // keys of a tile
+  static constexpr int KS = HD == 64 ? 8 : HD == 128 ? 6 : 3;  // K tiles in their ring
+  static constexpr int VS = HD == 64 ? 8 : HD == 128 ? 4 : 2;  // V tiles in theirs
   static constexpr uint32_t QCHUNK = kRows * 128;       // 64 columns of a row tile
   static constexpr uint32_t QTILE = HD / 64 * QCHUNK;
   static constexpr uint32_t EIGHT = HD * 16;            // eight keys: 1024 bytes for each 64 of their columns
@@ -46,9 +46,10 @@ struct Shape {
   static constexpr uint32_t V0 = K0 + KS * STAGE;
   static constexpr uint32_t BARS = V0 + VS * STAGE;
   static constexpr uint32_t TOTAL = BARS + 1024;
-  static constexpr uint32_t S0 = NT * HD;               // TMEM: outputs, then two buffers of scores
+  static constexpr uint32_t S0 = NT * HD;               // TMEM: outputs, two buffers of scores, two of weights a row tile
+  static constexpr uint32_t P0 = S0 + 2 * KT;
   static constexpr int SLOT = NT * kRows * (HD + 2);    // floats of a cut unit
-  static_assert(S0 + 2 * KT <= 512, "tensor memory");
+  static_assert(P0 + NT * KT <= 512, "tensor memory");
   static_assert(TOTAL + 1024 <= 232448, "shared memory");
 };
 
@@ -108,6 +109,14 @@ __device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a_
       "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(elected), "n"(B_HIGH)
       : "memory");
 }
+// One arrival of a warp.
+__device__ __forceinline__ void arrive_of(int lane, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lane)
+      : "memory");
+}
 __device__ __forceinline__ void commit_to(uint32_t elected, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
@@ -126,15 +135,16 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
-      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
-      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
+// until loads have landed; r is theirs, and not used before
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :: "memory");
 }
 __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -156,8 +166,8 @@ struct Unit {
 
 struct Bars {
   uint64_t q_full, q_free;
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_half[2], p_full[2], pv_half[2], pv_done[2], o_free[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t s_full[3], s_read[2], p_full[4], pv_done[4], o_free[2];
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t drain;
   uint32_t tmem;
@@ -279,17 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1);
-      mbar_init(&bar.p_half[s], 4);
+      mbar_init(&bar.s_read[s], 4);
       mbar_init(&bar.p_full[s], 4);
-      mbar_init(&bar.pv_half[s], 1);
+      mbar_init(&bar.p_full[s + 2], 4);
       mbar_init(&bar.pv_done[s], 1);
+      mbar_init(&bar.pv_done[s + 2], 1);
       mbar_init(&bar.o_free[s], 4);
     }
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(&bar.unit_full[s], 1);
-      mbar_init(&bar.unit_empty[s], 10);
+      mbar_init(&bar.unit_empty[s], 11);
     }
-    mbar_init(&bar.drain, 1);
+    mbar_init(&bar.s_full[2], 1);
+    mbar_init(&bar.drain, 2);
     bar.abort = 0;
     mbar_fence_init();
   }
@@ -313,6 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto hand_back = [&](uint32_t k) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.unit_empty[k % kUnits]);
+  };
+
+  auto advance = [](uint32_t& st, uint32_t& ph, uint32_t stages) {
+    if (++st == stages) st = 0, ph ^= 1;
   };
 
   if (warp == 10) {
@@ -350,12 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++loads;
         return true;
       };
-      // keys run a tile ahead of values: scores are made that much earlier than outputs
-      int blk = block_of(w.first), ahead = block_of(w.first + 1);
-      ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, blk);
+      // keys run two tiles ahead of values: scores are made that much earlier than outputs
+      int blk[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) blk[k] = block_of(w.first + k);
+      ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, blk[0]);
+      if (ok && w.first + 1 < w.last) ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, blk[1]);
       for (int i = w.first; ok && i < w.last; ++i) {
-        const int after = block_of(i + 2);
-        if (i + 1 < w.last) ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, ahead);
+        const int after = block_of(i + 3);
+        if (i + 2 < w.last) ok = load(&mK, L::K0, KS, bar.k_full, bar.k_empty, k_loads, blk[2]);
         if (ok && i == w.first) {  // queries behind the first keys, which need not wait for the last unit's queries
           if (unit > 0) ok = __all_sync(0xffffffffu, wait_for(&bar.q_free, (unit - 1) & 1, abort));
           if (!ok) break;
@@ -368,22 +387,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++q_loads;
         }
-        ok = ok && load(&mV, L::V0, VS, bar.v_full, bar.v_empty, v_loads, blk);
-        blk = ahead, ahead = after;
+        ok = ok && load(&mV, L::V0, VS, bar.v_full, bar.v_empty, v_loads, blk[0]);
+        blk[0] = blk[1], blk[1] = blk[2], blk[2] = after;
       }
     }
   } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMAs
-    constexpr uint32_t idS = idesc_bf16_f32(128, KT), idO = idesc_bf16_f32(128, HD, true);
+    // ---------------------------------------------------------------- scores
+    constexpr uint32_t idS = idesc_bf16_f32(128, KT);
     const uint32_t elected = elect_lane();
-    const uint32_t q_low = desc_low(smem_addr(sm), 16);
-    const uint32_t k_low = desc_low(smem_addr(sm + L::K0), 16), v_low = desc_low(smem_addr(sm + L::V0), 1024);
-    constexpr uint32_t q_high = desc_high(1024), kv_high = desc_high(L::EIGHT);
-    uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // stages and phases of the rings
-    auto advance = [](uint32_t& st, uint32_t& ph, uint32_t stages) {
-      if (++st == stages) st = 0, ph ^= 1;
-    };
-    uint32_t pph[2] = {0, 0}, units[2] = {0, 0};
+    const uint32_t q_low = desc_low(smem_addr(sm), 16), k_low = desc_low(smem_addr(sm + L::K0), 16);
+    constexpr uint32_t q_high = desc_high(1024), k_high = desc_high(L::EIGHT);
+    uint32_t kst = 0, kph = 0;             // stage and phase of the ring
+    uint32_t used = 0, read_phase = 0;     // a bit a buffer: whether any scores were made in it, the phase of their reading
     bool ok = true;
     auto wait = [&](uint64_t* w, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(w, parity, abort)); };
     for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
@@ -392,74 +407,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.seen.n, 0) > npt;
       const int tiles = __shfl_sync(0xffffffffu, w.last - w.first, 0);
       ok = wait(&bar.q_full, unit & 1);
-      // scores of row tile x from the next keys, which have landed, into buffer sb
-      auto scores = [&](int x, int sb, bool done, bool last) {
+      // Scores of row tile x from the keys of the stage into buffer sb.  A waiter has to see every phase of a barrier, none of
+      // them two late, so each warpgroup has barriers that only its own scores complete: 0 and 2 the first, 1 the second.
+      auto scores = [&](int x, int sb) -> bool {
+        if (used >> sb & 1) {
+          if (!wait(&bar.s_read[sb], read_phase >> sb & 1)) return false;
+          read_phase ^= 1u << sb;
+        }
+        used |= 1u << sb;
+        tc_fence_after();
         const uint32_t q = q_low + x * (L::QTILE >> 4), k = k_low + kst * (L::STAGE >> 4), d = tmem + L::S0 + sb * KT;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss<q_high, kv_high>(elected, d, q + ((kk / 4 * L::QCHUNK + kk % 4 * 32) >> 4),
-                                  k + ((kk / 4 * 1024 + kk % 4 * 32) >> 4), idS,
-                 kk ? 1u : 0u);
-        commit_to(elected, &bar.s_full[sb]);
-        if (done) {
-          commit_to(elected, &bar.k_empty[kst]);
-          advance(kst, kph, KS);
-        }
-        if (last) commit_to(elected, &bar.q_free);
-      };
-      // Output of row tile x from the next values and the weights in buffer sb.  Whatever else is needed, the next keys too, is
-      // waited for first: the weights are what comes last.
-      auto outputs = [&](int x, int sb, bool fresh, bool done, bool more) -> bool {
-        if (!wait(&bar.v_full[vst], vph)) return false;
-        if (fresh && units[x] > 0 && !wait(&bar.o_free[x], (units[x] - 1) & 1)) return false;
-        const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::S0 + sb * KT;
-        if (KT == 64 && more && !wait(&bar.k_full[kst], kph)) return false;
-        if (!wait(KT == 128 ? &bar.p_half[sb] : &bar.p_full[sb], pph[sb])) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts<kv_high>(elected, tmem + x * HD, p + kk * 8, v + (kk * 2 * L::EIGHT >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
-        if constexpr (KT == 128) {
-          commit_to(elected, &bar.pv_half[x]);
-          if (more && !wait(&bar.k_full[kst], kph)) return false;
-          if (!wait(&bar.p_full[sb], pph[sb])) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4; kk < 8; ++kk) mma_ts<kv_high>(elected, tmem + x * HD, p + kk * 8, v + (kk * 2 * L::EIGHT >> 4), idO, 1u);
-        }
-        pph[sb] ^= 1;
-        commit_to(elected, &bar.pv_done[x]);
-        if (done) {
-          commit_to(elected, &bar.v_empty[vst]);
-          advance(vst, vph, VS);
-        }
+          mma_ss<q_high, k_high>(elected, d, q + ((kk / 4 * L::QCHUNK + kk % 4 * 32) >> 4),
+                                 k + ((kk / 4 * 1024 + kk % 4 * 32) >> 4), idS, kk ? 1u : 0u);
+        commit_to(elected, &bar.s_full[x == 0 ? 2 * sb : 1]);
         return true;
       };
-      ok = ok && wait(&bar.k_full[kst], kph);
-      if (!ok) break;
-      tc_fence_after();
-      if (two) {
-        scores(0, 0, false, false);
-        scores(1, 1, true, tiles == 1);
-        for (int j = 0; ok && j < tiles; ++j) {
-          const bool more = j + 1 < tiles;
-          ok = outputs(0, 0, j == 0, false, more);
-          if (ok && more) scores(0, 0, false, false);
-          ok = ok && outputs(1, 1, j == 0, true, more);
-          if (ok && more) scores(1, 1, true, j + 2 == tiles);
-        }
-      } else {
-        scores(0, 0, true, tiles == 1);
-        if (tiles > 1) {
-          ok = wait(&bar.k_full[kst], kph);
-          if (!ok) break;
-          tc_fence_after();
-          scores(0, 1, true, tiles == 2);
-        }
-        for (int j = 0; ok && j < tiles; ++j) {
-          ok = outputs(0, j & 1, j == 0, true, j + 2 < tiles);
-          if (ok && j + 2 < tiles) scores(0, j & 1, true, j + 3 == tiles);
-        }
+      // two row tiles have a buffer each, one row tile uses them in turn
+      for (int j = 0; ok && j < tiles; ++j) {
+        ok = wait(&bar.k_full[kst], kph) && scores(0, two ? 0 : j & 1) && (!two || scores(1, 1));
+        commit_to(elected, &bar.k_empty[kst]);
+        advance(kst, kph, KS);
+      }
+      commit_to(elected, &bar.q_free);
+    }
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- outputs
+    constexpr uint32_t idO = idesc_bf16_f32(128, HD, true);
+    const uint32_t elected = elect_lane();
+    const uint32_t v_low = desc_low(smem_addr(sm + L::V0), 1024);
+    constexpr uint32_t v_high = desc_high(L::EIGHT);
+    uint32_t vst = 0, vph = 0;             // stage and phase of the ring
+    uint32_t p_phase = 0, units[2] = {0, 0};  // p_phase: a bit a buffer of weights
+    bool ok = true;
+    auto wait = [&](uint64_t* w, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(w, parity, abort)); };
+    for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
+      const Unit& w = bar.units[unit % kUnits];
+      if (!w.more) break;
+      const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.seen.n, 0) > npt;
+      const int tiles = __shfl_sync(0xffffffffu, w.last - w.first, 0);
+      // output of row tile x from the values of the stage and the weights in buffer pb
+      auto outputs = [&](int x, int pb, bool fresh) -> bool {
+        if (fresh && units[x] > 0 && !wait(&bar.o_free[x], (units[x] - 1) & 1)) return false;
+        if (!wait(&bar.p_full[pb], p_phase >> pb & 1)) return false;
+        p_phase ^= 1u << pb;
+        tc_fence_after();
+        const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::P0 + pb * (KT / 2);
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          mma_ts<v_high>(elected, tmem + x * HD, p + kk * 8, v + (kk * 2 * L::EIGHT >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
+        commit_to(elected, &bar.pv_done[pb]);
+        return true;
+      };
+      for (int j = 0; ok && j < tiles; ++j) {
+        ok = wait(&bar.v_full[vst], vph) && outputs(0, j & 1, j == 0) && (!two || outputs(1, 2 + (j & 1), j == 0));
+        commit_to(elected, &bar.v_empty[vst]);
+        advance(vst, vph, VS);
       }
       ++units[0];
       if (two) ++units[1];
@@ -472,13 +476,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sign = a.sm_scale < 0.f ? -1.f : 1.f;
     // a scale of 0 has to leave hidden keys at -inf: the smallest number serves
     const float scale = fmaxf(fabsf(a.sm_scale) * 1.4426950408889634f, 1.17549435e-38f);
-    uint32_t s_phase = 0, npv = 0, seq = 0;  // s_phase: a bit a buffer of scores
+    uint32_t s_phase = 0, seq = 0;          // s_phase: a bit a barrier of scores
+    uint32_t weighed = 0, pv_phase = 0;     // a bit a buffer of weights: outputs from it not seen to be over; their phase
     bool ok = true;
+    // until the outputs from this row tile's buffer b of weights are over; `over`: what a look at the barrier said
+    auto look = [&](int b) -> bool { return !(weighed >> b & 1) || mbar_test(&bar.pv_done[2 * wg + b], pv_phase >> b & 1); };
+    auto outputs_over = [&](int b, bool over) -> bool {
+      if (!__all_sync(0xffffffffu, over) &&
+          !__all_sync(0xffffffffu, wait_long(&bar.pv_done[2 * wg + b], pv_phase >> b & 1, abort)))
+        return false;
+      pv_phase ^= weighed & 1u << b, weighed &= ~(1u << b);
+      return true;
+    };
     for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
       const Unit& w = bar.units[unit % kUnits];
       if (!w.more) break;
       const bool two = NT == 2 && w.seen.n > npt;
-      const int tiles = w.last - w.first, items = two ? 2 * tiles : tiles;
+      const int tiles = w.last - w.first;
       if (wg == 0 || two) {
         const Seen& q = w.seen;
         const int token = wg * npt + i_row;  // in the unit
@@ -500,29 +514,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.f;
         bool begun = false;  // every row of the warp has an m
         int c0 = w.first * KT;
+        auto look_at_scores = [&](int j) -> bool {
+          const int sf = wg == 1 ? 1 : two || (j & 1) == 0 ? 0 : 2;
+          return mbar_test(&bar.s_full[sf], s_phase >> sf & 1);
+        };
+        bool there = look_at_scores(0);
         for (int j = 0; j < tiles; ++j, c0 += KT) {
-          const int e = two ? 2 * j + wg : j, sb = e & 1;
-          ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[sb], ((s_phase >> sb) ^ (two ? j : j >> 1)) & 1, abort));
-          if (!ok) break;
+          // Each look at a barrier is made a while before its answer is needed: it takes some hundred cycles.
+          const int sb = two ? wg : j & 1, sf = wg == 0 ? 2 * sb : 1;
+          if (!__all_sync(0xffffffffu, there) &&
+              !(ok = __all_sync(0xffffffffu, wait_long(&bar.s_full[sf], s_phase >> sf & 1, abort))))
+            break;
+          s_phase ^= 1u << sf;
           tc_fence_after();
-          const uint32_t ts = tmem + L::S0 + sb * KT + lanes;
+          // the scores to registers, and their buffer back
+          uint32_t s0[32], s1[32];
+          tmem_ld32_nowait(tmem + L::S0 + sb * KT + lanes, s0);
+          tmem_ld32_nowait(tmem + L::S0 + sb * KT + lanes + 32, s1);
+          const bool over = look(j & 1);
+          tmem_landed(s0);
+          tmem_landed(s1);
+          tc_fence_before();
+          __syncwarp();
+          arrive_of(lane, &bar.s_read[sb]);
           if (sign < 0.f || !((c0 >= all_va && c0 + KT <= all_ve) || c0 + KT <= all_vs)) {
-            // hidden keys to -inf, in place
-            auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
-#pragma unroll 1
-            for (int c = 0; c < KT; c += 32) {
-              const int at = c0 + c;
-              const uint32_t bits = below(vs - at) | (below(ve - at) & ~below(va - at));
-              uint32_t x[32];
-              tmem_ld32_nowait(ts + c, x);
-              tmem_wait_ld();
+            // hidden keys to -inf
+            auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+            const uint32_t b0 = below(vs - c0) | (below(ve - c0) & ~below(va - c0));
+            const uint32_t b1 = below(vs - c0 - 32) | (below(ve - c0 - 32) & ~below(va - c0 - 32));
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                x[k] = (bits >> k) & 1u ? __float_as_uint(__uint_as_float(x[k]) * sign) : 0xff800000u;
-              tmem_st32_nowait(ts + c, x);
+            for (int k = 0; k < 32; ++k) {
+              s0[k] = (b0 >> k) & 1u ? __float_as_uint(__uint_as_float(s0[k]) * sign) : 0xff800000u;
+              s1[k] = (b1 >> k) & 1u ? __float_as_uint(__uint_as_float(s1[k]) * sign) : 0xff800000u;
             }
-            tmem_wait_st();
           }
+          // the weights that lay in their place have been read
+          ok = outputs_over(j & 1, over);
+          if (!ok) break;
+          const int pb = 2 * wg + (j & 1);
+          const uint32_t tp = tmem + L::P0 + pb * (KT / 2) + lanes;
           if (wg == 0 && ((h0 < h1 && h0 < c0 + KT && h1 > c0) || end < c0 + KT)) {
             const uint32_t vq = seq + j, vst = vq % VS;
             ok = __all_sync(0xffffffffu, wait_for(&bar.v_full[vst], vq / VS & 1, abort));
@@ -538,100 +568,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async();
           }
-          // The weights of 64 keys, scores x (the first 32) and y, to columns `to` on.  The maximum need not be looked for:
-          // m is that of some earlier keys of the row, and weights up to 2^kMost of the largest of those do no harm
-          // in fp32 and bf16.  Where a row has no m yet, or its sum shows a larger weight, the maximum is taken, O and l are
-          // scaled to it, and the weights are made again.
-          auto weigh = [&](const uint32_t* x, const uint32_t* y, uint32_t to, int half) -> bool {
-            for (bool again = false;; again = true) {
-              if (again || !begun) {
-                tmem_wait_ld();
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // The maximum need not be looked for: m is that of some earlier keys of the row, and weights up to kMost times the
+          // largest of those do no harm in fp32 and bf16.  Where a row has no m yet, or its sum shows a larger weight, the
+          // maximum is taken, O and l are scaled to it, and the weights are made again.
+          for (bool again = false;; again = true) {
+            if (again || !begun) {
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; c += 4)
+              for (int c = 0; c < 32; c += 4)
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[c + k]), __uint_as_float(y[c + k])));
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-                const bool raise = active && mx > m + kRaise;
-                const bool rescale = raise && m != -INFINITY;
-                if (__any_sync(0xffffffffu, rescale)) {
-                  // O holds earlier keys: their products have to be done before this warp's rows are scaled
-                  if (j > 0 && !__all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv + j - 1) & 1, abort))) return false;
-                  if (half > 0 && !__all_sync(0xffffffffu, wait_for(&bar.pv_half[wg], (npv + j) & 1, abort))) return false;
-                  tc_fence_after();
-                  const float f = rescale ? ex2_approx(m - mx) : 1.f;
-                  l *= f;
+                for (int k = 0; k < 4; ++k)
+                  top[k] = fmaxf(top[k], fmaxf(__uint_as_float(s0[c + k]), __uint_as_float(s1[c + k])));
+              const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+              const bool raise = active && mx > m + kRaise;
+              const bool rescale = raise && m != -INFINITY;
+              if (__any_sync(0xffffffffu, rescale)) {
+                // O holds earlier keys: their products have to be done before this warp's rows are scaled
+                ok = outputs_over(~j & 1, look(~j & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const float f = rescale ? ex2_approx(m - mx) : 1.f;
+                l *= f;
 #pragma unroll 1
-                  for (int c = 0; c < HD; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16_nowait(tmem + wg * HD + lanes + c, o);
-                    tmem_wait_ld();
+                for (int c = 0; c < HD; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16_nowait(tmem + wg * HD + lanes + c, o);
+                  tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st16_nowait(tmem + wg * HD + lanes + c, o);
-                  }
-                  tmem_wait_st();
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tmem_st16_nowait(tmem + wg * HD + lanes + c, o);
                 }
-                if (raise) m = mx;
-                begun = __all_sync(0xffffffffu, m != -INFINITY || !active);
+                tmem_wait_st();
               }
-              // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
-              const float neg = m == -INFINITY ? 0.f : -m;
-              const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
-              float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-              auto part = [&](const uint32_t* v, uint32_t at) {
-                uint32_t p[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float2 e = __ffma2_rn(
-                      make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), scale2, neg2);
-                  const float2 w2 = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                  p[k] = pack_bf16x2(w2.x, w2.y);
-                  if (k & 1) sum1 = __fadd2_rn(sum1, w2);
-                  else sum0 = __fadd2_rn(sum0, w2);
-                }
-                tmem_st16_nowait(at, p);
-              };
-              part(x, to);
-              tmem_wait_ld();
-              part(y, to + 16);
-              sum0 = __fadd2_rn(sum0, sum1);
-              const float sum = sum0.x + sum0.y;
-              if (again || !__any_sync(0xffffffffu, active && !(sum < kMost))) {
-                l += sum;
-                break;
-              }
+              if (raise) m = mx;
+              begun = __all_sync(0xffffffffu, m != -INFINITY || !active);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            return true;
-          };
-          uint32_t s0[32], s1[32], s2[32];
-          tmem_ld32_nowait(ts, s0);
-          tmem_ld32_nowait(ts + 32, s1);
-          tmem_wait_ld();
-          if constexpr (KT == 128) {
-            // the second half: its first scores are on their way while the first half's weights are made
-            tmem_ld32_nowait(ts + 64, s2);
-            ok = weigh(s0, s1, ts, 0);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(&bar.p_half[sb]);
-            tmem_ld32_nowait(ts + 96, s1);
-            ok = weigh(s2, s1, ts + 32, 1);
-          } else {
-            ok = weigh(s0, s1, ts, 0);
+            // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
+            const float neg = m == -INFINITY ? 0.f : -m;
+            const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            auto part = [&](const uint32_t* v, uint32_t at) {
+              uint32_t p[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 e = __ffma2_rn(
+                    make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), scale2, neg2);
+                const float2 w2 = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                p[k] = pack_bf16x2(w2.x, w2.y);
+                if (k & 1) sum1 = __fadd2_rn(sum1, w2);
+                else sum0 = __fadd2_rn(sum0, w2);
+              }
+              tmem_st16_nowait(at, p);
+            };
+            part(s0, tp);
+            part(s1, tp + 16);
+            sum0 = __fadd2_rn(sum0, sum1);
+            const float sum = sum0.x + sum0.y;
+            if (again || !__any_sync(0xffffffffu, active && !(sum < kMost))) {
+              l += sum;
+              break;
+            }
           }
           if (!ok) break;
-          if (lane == 0) mbar_arrive(&bar.p_full[sb]);
+          there = look_at_scores(j + 1);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          arrive_of(lane, &bar.p_full[pb]);
+          weighed |= 1u << (j & 1);
         }
-        npv += tiles;
-        // With one row tile the scores of the last key tile came before the P V of the one in front of it: a wait for the
-        // last P V alone would take the phase before for its own.
-        if (!two && tiles > 1)
-          ok = ok && __all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv - 2) & 1, abort));
-        ok = ok && __all_sync(0xffffffffu, wait_for(&bar.pv_done[wg], (npv - 1) & 1, abort));
+        ok = ok && outputs_over(0, look(0)) && outputs_over(1, look(1));
         if (ok) {
           tc_fence_after();
           const bool whole = tiles == w.tiles;
@@ -664,10 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32_nowait(from, o0);
 #pragma unroll 1
           for (int c = 0; c < HD; c += 64) {
-            tmem_wait_ld();
+            tmem_landed(o0);
             tmem_ld32_nowait(from + c + 32, o1);
             put(o0, c);
-            tmem_wait_ld();
+            tmem_landed(o1);
             if (c + 64 < HD) tmem_ld32_nowait(from + c + 64, o0);
             put(o1, c + 32);
           }
@@ -716,19 +722,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-      } else {
-        // Every phase of its buffer is seen in turn, the ones for the other row tile too: a wait that is two phases ahead
-        // would be over before its time.
-        for (int k = 0; NT == 2 && ok && k < items / 2; ++k)
-          ok = __all_sync(0xffffffffu, wait_for(&bar.s_full[1], ((s_phase >> 1) ^ k) & 1, abort));
       }
-      s_phase ^= ((items + 1) / 2 & 1) | (items / 2 & 1) << 1;
       seq += tiles;
     }
   }
   __syncthreads();
   if (bar.abort) {  // what this CTA started ends before its memory goes away
-    if (warp == 9) {
+    if (warp == 9 || warp == 11) {
       commit_to(elect_lane(), &bar.drain);
       mbar_wait(&bar.drain, 0);
     }
@@ -782,7 +782,7 @@ cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float*
 
 TileShape window_tile_shape(int Hq, int Hkv, int hd) {
   const int npt = kRows / (Hq / Hkv);
-  return hd == 256 ? TileShape{npt, 64} : TileShape{2 * npt, 128};
+  return TileShape{hd == 256 ? npt : 2 * npt, 64};
 }
 
 size_t window_tiles_slots(int hd) {
