@@ -7,10 +7,10 @@
 // that ragged and causal work ends together; a long unit cut by a run's end leaves maximum, sum and unnormalised output per
 // row in the workspace, and the last of its CTAs joins them in the order of the runs.
 //
-// Scores S = Q K^T go to tensor memory; a thread takes a row (TMEM lane) of 64 to registers and gives the buffer back, so
-// that the next scores are made while it works; 2^(S scale - m) as bf16 goes to a buffer of its own in tensor memory, and
-// O += P V reads it there.  MMAs with different accumulators need not run in order, so no buffer is written before
-// the reader of what it held has ended.  The sum is of the fp32 weights before their rounding, whose errors average out.
+// Scores S = Q K^T go to tensor memory, two buffers a row tile; a thread takes a row (TMEM lane) of 64 to registers, and
+// 2^(S scale - m) goes back as bf16, to a buffer that O += P V reads.  MMAs with different accumulators need not run in
+// order, so nothing is written before the reader of what was there has ended.  The sum is of the fp32 weights before their
+// rounding, whose errors average out.
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, output of each (one row tile: two buffers in turn, warps 0-3)
 //   warp 8           TMA: queries, K and V tiles through a ring each
 //   warp 9, 11       MMAs of scores, of outputs: one warp for both spent longer on its waits and commits than the MMAs took
@@ -30,7 +30,6 @@ constexpr int kUnits = 4;       // units known ahead
 constexpr int kWhole = 8;       // key tiles of a unit that is never cut: a cut costs about as much
 constexpr int kLeast = kUnitCost + 1;  // cost of a run, at least: no two units begin in a shorter one
 constexpr float kRaise = 8.0f;     // log2
-constexpr float kMost = 65536.f;   // of 64 weights, as sums against the maximum held
 
 template <int HD>
 struct Shape {
@@ -46,10 +45,12 @@ struct Shape {
   static constexpr uint32_t V0 = K0 + KS * STAGE;
   static constexpr uint32_t BARS = V0 + VS * STAGE;
   static constexpr uint32_t TOTAL = BARS + 1024;
-  static constexpr uint32_t S0 = NT * HD;               // TMEM: outputs, two buffers of scores, two of weights a row tile
-  static constexpr uint32_t P0 = S0 + 2 * KT;
+  // TMEM: outputs, two buffers of scores a row tile, and as many of weights; head dim 128 leaves no columns for those, and
+  // weights lie where their scores were.
+  static constexpr bool OVER = HD == 128;
+  static constexpr uint32_t S0 = NT * HD, P0 = OVER ? S0 : S0 + NT * 2 * KT, PSTEP = OVER ? KT : KT / 2;
   static constexpr int SLOT = NT * kRows * (HD + 2);    // floats of a cut unit
-  static_assert(P0 + NT * KT <= 512, "tensor memory");
+  static_assert(P0 + NT * 2 * PSTEP <= 512, "tensor memory");
   static_assert(TOTAL + 1024 <= 232448, "shared memory");
 };
 
@@ -167,7 +168,7 @@ struct Unit {
 struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
-  uint64_t s_full[3], s_read[2], p_full[4], pv_done[4], o_free[2];
+  uint64_t s_full[4], s_read[4], p_full[4], pv_done[4], o_free[2];
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t drain;
   uint32_t tmem;
@@ -287,20 +288,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.v_full[s], 1);
       mbar_init(&bar.v_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&bar.s_full[s], 1);
       mbar_init(&bar.s_read[s], 4);
       mbar_init(&bar.p_full[s], 4);
-      mbar_init(&bar.p_full[s + 2], 4);
       mbar_init(&bar.pv_done[s], 1);
-      mbar_init(&bar.pv_done[s + 2], 1);
-      mbar_init(&bar.o_free[s], 4);
     }
+    mbar_init(&bar.o_free[0], 4);
+    mbar_init(&bar.o_free[1], 4);
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(&bar.unit_full[s], 1);
       mbar_init(&bar.unit_empty[s], 11);
     }
-    mbar_init(&bar.s_full[2], 1);
     mbar_init(&bar.drain, 2);
     bar.abort = 0;
     mbar_fence_init();
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_low = desc_low(smem_addr(sm), 16), k_low = desc_low(smem_addr(sm + L::K0), 16);
     constexpr uint32_t q_high = desc_high(1024), k_high = desc_high(L::EIGHT);
     uint32_t kst = 0, kph = 0;             // stage and phase of the ring
-    uint32_t used = 0, read_phase = 0;     // a bit a buffer: whether any scores were made in it, the phase of their reading
+    uint32_t used = 0, free_phase = 0;     // a bit a buffer: whether any scores were made in it; the phase of its being free
     bool ok = true;
     auto wait = [&](uint64_t* w, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(w, parity, abort)); };
     for (uint32_t unit = 0; ok && known(unit); hand_back(unit), ++unit) {
@@ -407,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.seen.n, 0) > npt;
       const int tiles = __shfl_sync(0xffffffffu, w.last - w.first, 0);
       ok = wait(&bar.q_full, unit & 1);
-      // Scores of row tile x from the keys of the stage into buffer sb.  A waiter has to see every phase of a barrier, none of
-      // them two late, so each warpgroup has barriers that only its own scores complete: 0 and 2 the first, 1 the second.
+      // Scores of row tile x from the keys of the stage into buffer sb, once its scores have been read, and the weights over
+      // them too.  A waiter has to see every phase of a barrier, none of them two late: each barrier here is for one buffer.
       auto scores = [&](int x, int sb) -> bool {
         if (used >> sb & 1) {
-          if (!wait(&bar.s_read[sb], read_phase >> sb & 1)) return false;
-          read_phase ^= 1u << sb;
+          if (!wait(L::OVER ? &bar.pv_done[sb] : &bar.s_read[sb], free_phase >> sb & 1)) return false;
+          free_phase ^= 1u << sb;
         }
         used |= 1u << sb;
         tc_fence_after();
@@ -421,12 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < HD / 16; ++kk)
           mma_ss<q_high, k_high>(elected, d, q + ((kk / 4 * L::QCHUNK + kk % 4 * 32) >> 4),
                                  k + ((kk / 4 * 1024 + kk % 4 * 32) >> 4), idS, kk ? 1u : 0u);
-        commit_to(elected, &bar.s_full[x == 0 ? 2 * sb : 1]);
+        commit_to(elected, &bar.s_full[sb]);
         return true;
       };
-      // two row tiles have a buffer each, one row tile uses them in turn
       for (int j = 0; ok && j < tiles; ++j) {
-        ok = wait(&bar.k_full[kst], kph) && scores(0, two ? 0 : j & 1) && (!two || scores(1, 1));
+        ok = wait(&bar.k_full[kst], kph) && scores(0, j & 1) && (!two || scores(1, 2 + (j & 1)));
         commit_to(elected, &bar.k_empty[kst]);
         advance(kst, kph, KS);
       }
@@ -453,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bar.p_full[pb], p_phase >> pb & 1)) return false;
         p_phase ^= 1u << pb;
         tc_fence_after();
-        const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::P0 + pb * (KT / 2);
+        const uint32_t v = v_low + vst * (L::STAGE >> 4), p = tmem + L::P0 + pb * L::PSTEP;
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
           mma_ts<v_high>(elected, tmem + x * HD, p + kk * 8, v + (kk * 2 * L::EIGHT >> 4), idO, (!fresh || kk > 0) ? 1u : 0u);
@@ -512,31 +510,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                   all_va = __reduce_max_sync(0xffffffffu, active ? va : 0),
                   all_ve = __reduce_min_sync(0xffffffffu, active ? ve : 0x7fffffff);
         float m = -INFINITY, l = 0.f;
-        bool begun = false;  // every row of the warp has an m
         int c0 = w.first * KT;
         auto look_at_scores = [&](int j) -> bool {
-          const int sf = wg == 1 ? 1 : two || (j & 1) == 0 ? 0 : 2;
-          return mbar_test(&bar.s_full[sf], s_phase >> sf & 1);
+          const int sb = 2 * wg + (j & 1);
+          return mbar_test(&bar.s_full[sb], s_phase >> sb & 1);
         };
         bool there = look_at_scores(0);
         for (int j = 0; j < tiles; ++j, c0 += KT) {
           // Each look at a barrier is made a while before its answer is needed: it takes some hundred cycles.
-          const int sb = two ? wg : j & 1, sf = wg == 0 ? 2 * sb : 1;
+          const int sb = 2 * wg + (j & 1);
           if (!__all_sync(0xffffffffu, there) &&
-              !(ok = __all_sync(0xffffffffu, wait_long(&bar.s_full[sf], s_phase >> sf & 1, abort))))
+              !(ok = __all_sync(0xffffffffu, wait_long(&bar.s_full[sb], s_phase >> sb & 1, abort))))
             break;
-          s_phase ^= 1u << sf;
+          s_phase ^= 1u << sb;
           tc_fence_after();
           // the scores to registers, and their buffer back
           uint32_t s0[32], s1[32];
           tmem_ld32_nowait(tmem + L::S0 + sb * KT + lanes, s0);
           tmem_ld32_nowait(tmem + L::S0 + sb * KT + lanes + 32, s1);
-          const bool over = look(j & 1);
+          const bool over = L::OVER || look(j & 1);  // OVER: the scores were not made before
           tmem_landed(s0);
           tmem_landed(s1);
           tc_fence_before();
           __syncwarp();
-          arrive_of(lane, &bar.s_read[sb]);
+          if (!L::OVER) arrive_of(lane, &bar.s_read[sb]);
           if (sign < 0.f || !((c0 >= all_va && c0 + KT <= all_ve) || c0 + KT <= all_vs)) {
             // hidden keys to -inf
             auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
@@ -551,8 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the weights that lay in their place have been read
           ok = outputs_over(j & 1, over);
           if (!ok) break;
-          const int pb = 2 * wg + (j & 1);
-          const uint32_t tp = tmem + L::P0 + pb * (KT / 2) + lanes;
+          const uint32_t tp = tmem + L::P0 + sb * L::PSTEP + lanes;
           if (wg == 0 && ((h0 < h1 && h0 < c0 + KT && h1 > c0) || end < c0 + KT)) {
             const uint32_t vq = seq + j, vst = vq % VS;
             ok = __all_sync(0xffffffffu, wait_for(&bar.v_full[vst], vq / VS & 1, abort));
@@ -568,19 +564,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async();
           }
-          // The maximum need not be looked for: m is that of some earlier keys of the row, and weights up to kMost times the
-          // largest of those do no harm in fp32 and bf16.  Where a row has no m yet, or its sum shows a larger weight, the
-          // maximum is taken, O and l are scaled to it, and the weights are made again.
-          for (bool again = false;; again = true) {
-            if (again || !begun) {
-              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // m is the maximum of some earlier keys of the row; it is raised, and O and l scaled to it, when these keys' is
+          // larger by more than 2^kRaise, which is rare: weights up to that do no harm in fp32 and bf16.  With the maximum
+          // known first, weights take the scores' place in registers.  Weights made first, and again where their sum showed a
+          // larger score, kept both: the compiler then waited for each pair, 1030 cycles for 64 of two warps and not 710.
+          {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int c = 0; c < 32; c += 4)
+            for (int c = 0; c < 32; c += 4)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  top[k] = fmaxf(top[k], fmaxf(__uint_as_float(s0[c + k]), __uint_as_float(s1[c + k])));
-              const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-              const bool raise = active && mx > m + kRaise;
+              for (int k = 0; k < 4; ++k)
+                top[k] = fmaxf(fmaxf(top[k], __uint_as_float(s0[c + k])), __uint_as_float(s1[c + k]));
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            const bool raise = active && mx > m + kRaise;
+            if (__any_sync(0xffffffffu, raise)) {
               const bool rescale = raise && m != -INFINITY;
               if (__any_sync(0xffffffffu, rescale)) {
                 // O holds earlier keys: their products have to be done before this warp's rows are scaled
@@ -601,7 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
               }
               if (raise) m = mx;
-              begun = __all_sync(0xffffffffu, m != -INFINITY || !active);
             }
             // 2^(s scale - m); a row that has seen nothing yet keeps m = -inf, and 2^-inf = 0
             const float neg = m == -INFINITY ? 0.f : -m;
@@ -623,18 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             part(s0, tp);
             part(s1, tp + 16);
             sum0 = __fadd2_rn(sum0, sum1);
-            const float sum = sum0.x + sum0.y;
-            if (again || !__any_sync(0xffffffffu, active && !(sum < kMost))) {
-              l += sum;
-              break;
-            }
+            l += sum0.x + sum0.y;
           }
-          if (!ok) break;
           there = look_at_scores(j + 1);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          arrive_of(lane, &bar.p_full[pb]);
+          arrive_of(lane, &bar.p_full[sb]);
           weighed |= 1u << (j & 1);
         }
         ok = ok && outputs_over(0, look(0)) && outputs_over(1, look(1));
