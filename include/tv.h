@@ -693,7 +693,7 @@ TV_API int tv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64
  *                TV_ERR_TIMEOUT (a bounded device wait gave up; that sequence's outputs are then
  *                unspecified)
  * Scores, softmax statistics and sums are fp32; the weights enter the product with the values as bf16.
- * Results depend on the sizes and on no other sequence of the call.  A non-finite key or value that
+ * Results depend on the lengths of all sequences (where work is cut), on no other's data.  A non-finite key or value that
  * some query sees may reach other queries of its sequence and KV head; one that no query of the
  * sequence sees reaches none.
  * Supported: hd in {64, 128, 256}; block_size = 16; Hq a multiple of Hkv, Hq / Hkv <= 128; window and

@@ -7,7 +7,8 @@
 //
 // A token next to a border decides, so sums are carried as two floats each: p - A q by exact differences and products, sums
 // by exact additions, about 2^-46.  Doubles would cost more than the row's bytes, two additions a clock on an SM, and their
-// latency most of a short call.
+// latency most of a short call: 64 chains of four tokens, 131072 values of fp32, took 76 us in doubles, 25 with pairs for
+// the values alone, 17 with pairs throughout.
 //
 // A cluster of up to eight CTAs takes a sequence, each an equal part of a row, each of its 16 warps a run of that part.
 // Every CTA walks the tree by itself on the same sums.  The draw finds the warp's run from the runs' sums, and its

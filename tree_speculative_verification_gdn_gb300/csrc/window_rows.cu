@@ -10,6 +10,9 @@
 //
 // A (sequence, KV head) that lies in several CTAs' runs leaves maximum, sum and unnormalised output per CTA in the
 // workspace; the last of them to finish joins them in the order of the runs, so the result does not depend on which that is.
+//
+// 64 sequences behind 8192 tokens, 16 heads on 4 of 128 columns: 1.07 GB in 171 us, none of it in L2, 6.3 TB/s.  One sequence
+// behind 4096: 15 us, the plan, a run's copies and the joining one behind the other.
 #include "tv_async.cuh"
 #include "window_attn.cuh"
 
