@@ -332,3 +332,28 @@ def test_two_calls_on_two_streams_at_once():
                                          stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want)) and not any(e.any() for e in errs)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (6, 1)])
+@pytest.mark.parametrize("climb", [False, True])
+def test_units_cut_among_several_ctas(hd, Hq, Hkv, climb):
+    # units of so many keys that their parts meet in the workspace: whole ones, one row tile, ragged ends; and scores that
+    # climb, so that a part's maximum tells nothing about the next one's
+    lens, prefix = [130, 5, 64, 2], [4100, 2900, 1800, 40]
+    c = case(lens, prefix, Hq, Hkv, hd, seed=19, scale=0.1 if climb else 1.5, poison=not climb)
+    if climb:
+        u = torch.randn(hd, generator=torch.Generator().manual_seed(2)).sign()
+        c["q"] = (c["q"].float().cpu() + u).to(BF).to(DEV)
+        for b, (p, n) in enumerate(zip(prefix, lens)):
+            at = np.arange(p + n)
+            block, row = torch.tensor(c["real"][b][at // 16], device=DEV).long(), torch.tensor(at % 16, device=DEV).long()
+            k = 0.05 * torch.randn(len(at), Hkv, hd, generator=torch.Generator().manual_seed(b))
+            k += torch.tensor(30.0 * (at // 333), dtype=torch.float32)[:, None, None] * hd ** -0.5 * u
+            c["k"][block, :, row] = k.to(BF).to(DEV)
+    for window, sinks in ((0, 0), (2500, 40)):
+        out, err = attend(c, window, sinks)
+        assert not any(err)
+        check(c, out, window, sinks)
+        again, _ = attend(c, window, sinks)
+        assert torch.equal(out, again)

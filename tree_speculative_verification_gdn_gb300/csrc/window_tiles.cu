@@ -34,7 +34,9 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kThreads = 384;
 constexpr int kUnits = 4;       // units known ahead
-constexpr int kWhole = 8;       // key tiles of a unit that is never cut: a cut costs about as much
+// Key tiles of a unit that is never cut: a cut costs about as much.  8 prompts of 500 tokens on the average, window 1024, head dim
+// 256: 96 us with 8 for the limit, 84 with 20; 900 tokens alone 46 and 34; two or three units a CTA: up to 5 % the other way.
+constexpr int kWhole = 20;
 constexpr int kLeast = kUnitCost + 1;  // cost of a run, at least: no two units begin in a shorter one
 constexpr float kRaise = 8.0f;     // log2
 
