@@ -118,7 +118,8 @@ constexpr int kFewRows = 16;
 size_t window_rows_slots(int hd);
 cudaError_t launch_window_rows(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s);
 
-// Any number of rows: units of `tokens` tokens; cost: per unit its key tiles and kUnitCost more.
+// Any number of rows: units of `tokens` tokens; cost: per unit its key tiles and kUnitCost more.  One prompt of 4096 tokens, 32
+// heads on 8 of 128: 153 us with 2 for that, 134 with 4, 135 with 7.
 struct TileShape {
   int tokens;  // of a unit
   int keys;    // of a tile
