@@ -77,12 +77,6 @@ __device__ __forceinline__ void add(Pair2& acc, Pair x, Pair y) {
   acc.lo = __fadd2_rn(acc.lo, __fadd2_rn(e, make_float2(x.lo, y.lo)));
 }
 
-__device__ __forceinline__ Pair warp_sum(Pair x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
-  return x;
-}
 // Over the lanes up to this one.
 template <int LANES>
 __device__ __forceinline__ Pair warp_scan(Pair x) {
@@ -95,6 +89,14 @@ __device__ __forceinline__ Pair warp_scan(Pair x) {
 }
 __device__ __forceinline__ Pair of_lane(Pair x, int lane) {
   return Pair{__shfl_sync(0xffffffffu, x.hi, lane), __shfl_sync(0xffffffffu, x.lo, lane)};
+}
+// The first lane's, in every lane: add() rounds lo by the order of its two numbers, so that the lanes of a butterfly end up
+// to a rounding of lo apart, and a CTA that decided on another lane's number might walk or draw apart from its cluster.
+__device__ __forceinline__ Pair warp_sum(Pair x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    add(x, Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
+  return of_lane(x, 0);
 }
 // Of the lane before, 0 in the first.
 __device__ __forceinline__ Pair before_lane(Pair x) {
