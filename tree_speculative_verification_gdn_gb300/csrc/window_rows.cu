@@ -70,8 +70,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, per_sm(HD))
-    window_rows_kernel(WinAttnArgs a, const long long* __restrict__ cost, float* __restrict__ slots,
-                       int* __restrict__ arrived) {
+    window_rows_kernel(WinAttnArgs a, const long long* cost, float* slots, int* arrived) {
   using S = Shape<HD>;
   constexpr int kSlot = kRows * (HD + 2);  // floats: outputs, then (maximum, sum) per row
   constexpr int CH = HD / 8;                 // 16-byte chunks of a row

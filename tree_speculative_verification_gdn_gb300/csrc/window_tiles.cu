@@ -272,8 +272,7 @@ struct Walk {
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-    window_tiles_kernel(const __grid_constant__ WinAttnArgs a, const long long* __restrict__ cost,
-                        int* __restrict__ arrived, float* __restrict__ slots, int npt,
+    window_tiles_kernel(const __grid_constant__ WinAttnArgs a, const long long* cost, int* arrived, float* slots, int npt,
                         const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                         const __grid_constant__ CUtensorMap mV) {
   using L = Shape<HD>;
