@@ -6,7 +6,8 @@
 //
 // Angles: theta^(-2c/r) / 2 pi is a fraction of a turn for each position.  In 64-bit fixed point position times that
 // fraction drops whole turns by its overflow, exactly, however far the position; the nearest quarter turn comes off as
-// two bits and what is left, an eighth of a turn at most, goes to sincospi with its 24 bits whole.  They are made once
+// two bits and what is left, an eighth of a turn at most, goes to sincospi rounded to 24 bits, 2^-28 of a turn.  The fraction
+// is right to half of 2^-64 (tv_turns.h), so a position of 2^31 adds 2^-34 to that.  Angles are made once
 // a token, eight tokens at a time by the whole block: made a token at a time by two warps, the others waited for them.
 //
 // Bound by HBM: q, k and v are read once and written once.  A block walks a run of tokens, its place among the sequences
@@ -15,13 +16,12 @@
 //
 // 14000 tokens, 32 + 8 + 8 heads of 128 columns: 344 MB in 63 us, 0.80 of the copy rate with 62 % of the issue slots taken; 64
 // tokens behind a decode step 4.5 us.
-#include <math.h>
-
 #include "paged_check.cuh"
 #include "tv_async.cuh"
 #include "tv_common.cuh"
 #include "tv_internal.h"
 #include "tv_launch.cuh"
+#include "tv_turns.h"
 
 namespace tv {
 namespace {
@@ -318,8 +318,7 @@ cudaError_t launch_qk_norm_rope(const QkRopeArgs& a, cudaStream_t s) {
   }
   if (a.T == 0) return cudaSuccess;
   Turns turns;
-  for (int c = 0; c < a.rotary / 2; ++c)
-    turns.f[c] = (unsigned long long)ldexp(pow((double)a.theta, -2.0 * c / a.rotary) / 6.283185307179586476925286766559, 64);
+  turns_of(a.theta, a.rotary, turns.f);
   if (a.io == TV_F32) {
     if (a.hd == 64) return go<float, 64>(a, turns, s);
     return a.hd == 128 ? go<float, 128>(a, turns, s) : go<float, 256>(a, turns, s);
