@@ -312,8 +312,8 @@ cudaError_t go(const QkRopeArgs& a, const Turns& turns, cudaStream_t s) {
 cudaError_t launch_qk_norm_rope(const QkRopeArgs& a, cudaStream_t s) {
   if (a.cu != nullptr) {
     const PagedCheck c{a.cu, a.prefix_len, a.live, a.k_cache != nullptr ? a.block_table : nullptr,
-                       a.B, a.T, a.T, a.max_blocks, a.num_blocks, -1, 0};
-    const cudaError_t e = launch_paged_check(c, a.err, s);
+                       a.B, a.T, a.T, a.max_blocks, a.num_blocks, -1, 0, a.err};
+    const cudaError_t e = launch_paged_check(c, s);
     if (e != cudaSuccess) return e;
   }
   if (a.T == 0) return cudaSuccess;

@@ -58,14 +58,16 @@ size_t window_attn_workspace_size(int B, int T, int max_len, int Hq, int Hkv, in
 cudaError_t launch_window_attn(const WinAttnArgs& a, void* workspace, cudaStream_t s) {
   const bool few = few_rows(a.max_len, a.Hq / a.Hkv);
   const PagedCheck c{a.cu, a.prefix_len, a.live, a.block_table, a.B, a.T, a.max_len, a.max_blocks, a.num_blocks,
-                     a.window, a.sinks};
-  if (a.T == 0) return launch_paged_check(c, a.err, s);  // no workspace
+                     a.window, a.sinks, a.err};
+  if (a.T == 0) return launch_paged_check(c, s);  // no workspace
   long long* cost = static_cast<long long*>(workspace);
   int* zeros = reinterpret_cast<int*>(static_cast<char*>(workspace) + align16((size_t)a.B * 8));
   const int count = counters(a.B, a.Hkv, few);
   const TileShape shape = few ? TileShape{0, 0} : window_tile_shape(a.Hq, a.Hkv, a.hd);
+  cudaError_t e = check_lengths(c, s);
+  if (e != cudaSuccess) return e;
   window_plan_kernel<<<a.B, 256, 0, s>>>(a, c, shape, cost, zeros, count);
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   float* slots = reinterpret_cast<float*>(reinterpret_cast<char*>(zeros) + align16((size_t)count * 4));
   return few ? launch_window_rows(a, cost, zeros, slots, s) : launch_window_tiles(a, cost, zeros, slots, s);
