@@ -31,6 +31,7 @@ struct Turns {
 };
 
 constexpr int kChunk = 8;  // tokens whose places and angles are made at a time, by the whole block
+constexpr int kShared = 200 * 1024;  // of an SM for its blocks; one takes 147 KB at most (fp32, hd 256, 32 heads a block)
 constexpr int kAhead = 4;  // tokens of a thread's vectors on their way, the one in work among them
 
 // Sixteen columns as pairs of neighbours: eight from the first vector, eight from the second.
@@ -288,13 +289,14 @@ cudaError_t go(const QkRopeArgs& a, const Turns& turns, cudaStream_t s) {
   const int chunk = tpb < kChunk ? kChunk / tpb * tpb : tpb;
   const size_t smem = (size_t)kAhead * Own<T>::kParts * threads * 16 + (size_t)chunk * (a.rotary * sizeof(float2) + 3 * sizeof(int2)) + 8 + 2 * HD * sizeof(float);
   auto kern = qk_rope_kernel<T, HD>;
+  // One limit for all shapes: with each call's own, another thread's call might lower it before this one's launch.
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
     if (e != cudaSuccess) return e;
   }
   // as many blocks as are resident at once (64 registers a thread), each a run of tokens
   int resident = 1024 / threads;
-  if (resident > (int)(200 * 1024 / smem)) resident = (int)(200 * 1024 / smem);
+  if (resident > (int)(kShared / smem)) resident = (int)(kShared / smem);
   if (resident < 1) resident = 1;
   long long blocks = (long long)device_sm_count() * resident / groups;
   const long long rows = ((long long)a.T + tpb - 1) / tpb;
