@@ -63,10 +63,13 @@ struct Shape {
   static_assert(TOTAL + 1024 <= 232448, "shared memory");
 };
 
-// A phase of the barrier, or false after some seconds at most, or once another role has given up.  Looks once, then
-// tries, each try asleep in the barrier unit for about a microsecond.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t it = 0; it < (1u << 20); ++it) {
+// A phase of the barrier, or false after `tries`, or once another role has given up.  Looks once, then tries, each try asleep
+// in the barrier unit for 4 us at most (whatever the hint; measured).  A wait inside a unit is over after some key tiles, one
+// for another unit after a whole one: up to 2^24 tiles of 0.8 us, 14 s, so that those waits last up to 33 s and the others
+// 4 s.  A role that gives up makes the others leave within a try, whichever they are in.
+constexpr uint32_t kTries = 1u << 20, kUnitTries = 1u << 23;
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t tries = kTries) {
+  for (uint32_t it = 0; it < tries; ++it) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -81,8 +84,8 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
   *abort = 1;
   return false;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_test(bar, parity) || wait_long(bar, parity, abort);
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t tries = kTries) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, abort, tries);
 }
 
 // The MMA warp runs as one, so that addresses stay in uniform registers; one elected lane issues.
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t k_loads = 0, v_loads = 0, q_loads = 0;  // what the producer has started
   // the k-th unit, once it is known; a warp hands it back when it needs no more of it
   auto known = [&](uint32_t k) -> bool {
-    return __all_sync(0xffffffffu, wait_for(&bar.unit_full[k % kUnits], k / kUnits & 1, abort));
+    return __all_sync(0xffffffffu, wait_for(&bar.unit_full[k % kUnits], k / kUnits & 1, abort, kUnitTries));
   };
   auto hand_back = [&](uint32_t k) {
     __syncwarp();
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w(a, cost, run, TileShape{NT * npt, KT});
     if (lane == 0) {
       for (uint32_t k = 0;; ++k) {
-        if (k >= kUnits && !wait_for(&bar.unit_empty[k % kUnits], (k / kUnits - 1) & 1, abort)) break;
+        if (k >= kUnits && !wait_for(&bar.unit_empty[k % kUnits], (k / kUnits - 1) & 1, abort, kUnitTries)) break;
         bar.units[k % kUnits] = w.u;
         mbar_arrive(&bar.unit_full[k % kUnits]);
         if (!w.u.more) break;
