@@ -24,6 +24,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;      // query rows of a unit
 constexpr int kWhole = 16;     // pages of a sequence and head that are never cut
 constexpr int kLeast = 8;      // pages a run, at least: below, joining costs more than the pages
+// Pages after which a CTA joins its warps' outputs, in the workspace: the matrix units cut what they add to a sum, which left
+// outputs 5e-3 short with 2^20 keys a warp.  Parts of 2^15 keys a warp, joined in fp32, lose 2e-4, a tenth of the
+// store's rounding.
+constexpr int kSpan = 8192;
 constexpr float kRaise = 8.f;  // the running maximum is raised only by more than this (log2): sums grow by 2^8 at most
 
 constexpr int per_sm(int hd) { return hd == 256 ? 1 : hd == 128 ? 2 : 3; }
@@ -72,7 +76,7 @@ template <int HD>
 __global__ void __launch_bounds__(kThreads, per_sm(HD))
     window_rows_kernel(WinAttnArgs a, const long long* cost, float* slots, int* arrived) {
   using S = Shape<HD>;
-  constexpr int kSlot = kRows * (HD + 2);  // floats: outputs, then (maximum, sum) per row
+  constexpr int kSlot = kRows * (HD + 4);  // floats: outputs, then (maximum, sum) per row, twice: to read and to write
   constexpr int CH = HD / 8;                 // 16-byte chunks of a row
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* sQ = smem;                          // kRows rows
@@ -107,7 +111,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD))
       x = u1;
       continue;
     }
-    const int p0 = (int)(x - u0), p1 = uncut ? q.pages : (int)(min(x1, u1) - u0);
+    const int begin = (int)(max(x0, u0) - u0), end = uncut ? q.pages : (int)(min(x1, u1) - u0);  // the run's part of it
+    const int p0 = (int)(x - u0), p1 = min(end, p0 + kSpan);
     const int R = q.n * G;
     const int32_t* table = a.block_table + (long long)b * a.max_blocks;
 
@@ -265,17 +270,20 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD))
       }
     }
     __syncthreads();
-    const bool alone = p0 == 0 && p1 == q.pages;
+    const bool alone = begin == 0 && end == q.pages;
     const long long c0 = quotient(u0, per), c1 = quotient(u1 - 1, per);  // the CTAs that share the unit
-    // a CTA's first unit goes to its slot 0, a later one that runs past its end to slot 1
+    // a CTA's first unit goes to its slot 0, a later one that runs past its end to slot 1, others' parts before that one too
     auto slot_of = [&](long long c) { return slots + (2 * c + (c * per < u0 ? 1 : 0)) * kSlot; };
     auto put = [&](int r, int c, const float* v) {
       uint2 w = pack4(v);
       *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (long long)(start + r / G) * a.out_stride +
                                 (long long)(kvh * G + r % G) * HD + c) = w;
     };
+    const int after = (end - p1 + kSpan - 1) / kSpan;  // parts to come; the last one's maxima and sums are the first copy
     for (int i = tid; i < R * (HD / 4); i += kThreads) {
       const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+      float* slot = slot_of(blockIdx.x);
+      float* slot_ml = slot + kRows * HD + r * 2;
       float top = -INFINITY, f[kWarps], sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
@@ -287,17 +295,26 @@ __global__ void __launch_bounds__(kThreads, per_sm(HD))
         const float4 y = *reinterpret_cast<const float4*>(acc + (w * kRows + r) * HD + c);
         v[0] += f[w] * y.x, v[1] += f[w] * y.y, v[2] += f[w] * y.z, v[3] += f[w] * y.w;
       }
-      if (alone) {
+      if (p0 > begin) {  // with the parts before it
+        const float2 w = *reinterpret_cast<const float2*>(slot_ml + ((after + 1) & 1) * 2 * kRows);
+        const float4 y = *reinterpret_cast<const float4*>(slot + r * HD + c);
+        const float to = fmaxf(top, w.x);
+        const float f0 = top == -INFINITY ? 0.f : ex2(top - to), f1 = w.x == -INFINITY ? 0.f : ex2(w.x - to);
+        top = to;
+        sum = f0 * sum + f1 * w.y;
+        v[0] = f0 * v[0] + f1 * y.x, v[1] = f0 * v[1] + f1 * y.y;
+        v[2] = f0 * v[2] + f1 * y.z, v[3] = f0 * v[3] + f1 * y.w;
+      }
+      if (alone && after == 0) {
         const float inv = 1.f / sum;
         v[0] *= inv, v[1] *= inv, v[2] *= inv, v[3] *= inv;
         put(r, c, v);
       } else {
-        float* slot = slot_of(blockIdx.x);
         *reinterpret_cast<float4*>(slot + r * HD + c) = make_float4(v[0], v[1], v[2], v[3]);
-        if (c == 0) slot[kRows * HD + r * 2] = top, slot[kRows * HD + r * 2 + 1] = sum;
+        if (c == 0) *reinterpret_cast<float2*>(slot_ml + (after & 1) * 2 * kRows) = make_float2(top, sum);
       }
     }
-    if (!alone) {
+    if (!alone && after == 0) {
       __syncthreads();
       if (tid == 0) {
         __threadfence();
@@ -355,7 +372,7 @@ cudaError_t go(const WinAttnArgs& a, const long long* cost, int* arrived, float*
 
 }  // namespace
 
-size_t window_rows_slots(int hd) { return (size_t)kSms * per_sm(hd) * 2 * kRows * (hd + 2) * sizeof(float); }
+size_t window_rows_slots(int hd) { return (size_t)kSms * per_sm(hd) * 2 * kRows * (hd + 4) * sizeof(float); }
 
 cudaError_t launch_window_rows(const WinAttnArgs& a, const long long* cost, int* arrived, float* slots, cudaStream_t s) {
   if (a.hd == 64) return go<64>(a, cost, arrived, slots, s);

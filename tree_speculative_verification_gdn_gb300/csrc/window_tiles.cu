@@ -38,6 +38,11 @@ constexpr int kUnits = 4;       // units known ahead
 // 256: 96 us with 8 for the limit, 84 with 20; 900 tokens alone 46 and 34; two or three units a CTA: up to 5 % the other way.
 constexpr int kWhole = 20;
 constexpr int kLeast = kUnitCost + 1;  // cost of a run, at least: no two units begin in a shorter one
+// Key tiles of a part: the run's share of a unit comes to the roles in parts, whose outputs are joined in the run's slot of
+// the workspace.  The matrix units cut what they add to an output, which leaves a sum over n keys short by about n 2^-27.4
+// of it: 6e-3 with 2^20, 2.5e-2 with 2^22.  Parts of 2^15, joined in fp32, lose 2e-4, a tenth of the store's rounding; one
+// takes some 400 us, its start and output 4.
+constexpr int kPart = 512;
 constexpr float kRaise = 8.0f;     // log2
 
 template <int HD>
@@ -63,13 +68,11 @@ struct Shape {
   static_assert(TOTAL + 1024 <= 232448, "shared memory");
 };
 
-// A phase of the barrier, or false after `tries`, or once another role has given up.  Looks once, then tries, each try asleep
-// in the barrier unit for 4 us at most (whatever the hint; measured).  A wait inside a unit is over after some key tiles, one
-// for another unit after a whole one: up to 2^24 tiles of 0.8 us, 14 s, so that those waits last up to 33 s and the others
-// 4 s.  A role that gives up makes the others leave within a try, whichever they are in.
-constexpr uint32_t kTries = 1u << 20, kUnitTries = 1u << 23;
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t tries = kTries) {
-  for (uint32_t it = 0; it < tries; ++it) {
+// A phase of the barrier, or false after 4 s at most, or once another role has given up.  Looks once, then tries, each try
+// asleep in the barrier unit for 4 us at most (whatever the hint; measured).  No wait outlasts a part by much, 0.4 ms.
+constexpr uint32_t kTries = 1u << 20;
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t it = 0; it < kTries; ++it) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -84,8 +87,8 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
   *abort = 1;
   return false;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t tries = kTries) {
-  return mbar_test(bar, parity) || wait_long(bar, parity, abort, tries);
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, abort);
 }
 
 // The MMA warp runs as one, so that addresses stay in uniform registers; one elected lane issues.
@@ -159,6 +162,12 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :: "memory");
 }
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+}
 __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -168,11 +177,12 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t*
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A unit, or the part of its key tiles that lies in the CTA's run.
+// A unit, or a part of its key tiles that lie in the CTA's run.
 struct Unit {
   int more;                // 0: the run has ended
   int b, kvh, token;       // sequence, KV head, first token's row
-  int tiles, first, last;  // key tiles of the unit, the run's part of them
+  int tiles, begin, end;   // key tiles of the unit, the run's share of them
+  int first, last;         // the part's
   int c0, c1;              // the CTAs that share it
   Seen seen;
 };
@@ -213,13 +223,14 @@ struct Walk {
     u.token = start + t;
     u.tiles = (u.seen.pages * 16 + shape.keys - 1) / shape.keys;
     if (u.tiles <= kWhole) {  // to the run that it starts in
-      u.first = 0, u.last = u0 >= run.x0 && u0 < run.x1 ? u.tiles : 0;
+      u.begin = 0, u.end = u0 >= run.x0 && u0 < run.x1 ? u.tiles : 0;
     } else {
       const long long k0 = u0 + kUnitCost;
-      u.first = (int)min((long long)u.tiles, max(0LL, run.x0 - k0));
-      u.last = (int)max(0LL, min((long long)u.tiles, run.x1 - k0));
+      u.begin = (int)min((long long)u.tiles, max(0LL, run.x0 - k0));
+      u.end = (int)max(0LL, min((long long)u.tiles, run.x1 - k0));
     }
   }
+  __device__ void part(int first) { u.first = first, u.last = min(u.end, first + kPart); }
   __device__ Walk(const WinAttnArgs& a_, const long long* cost_, const Run& run_, TileShape s)
       : a(a_), cost(cost_), run(run_), shape(s) {
     u.b = run.b;
@@ -248,8 +259,9 @@ struct Walk {
   }
   // On from a unit that has no key tile in the run.
   __device__ void settle() {
-    while (u0 < run.x1 && u.first >= u.last) step();
+    while (u0 < run.x1 && u.begin >= u.end) step();
     u.more = u0 < run.x1;
+    part(u.begin);
     const long long k0 = u0 + kUnitCost;
     u.c0 = (int)quotient(k0, run.per), u.c1 = (int)quotient(k0 + u.tiles - 1, run.per);
   }
@@ -268,6 +280,7 @@ struct Walk {
     unit();
   }
   __device__ void next() {
+    if (u.last < u.end) return part(u.last);
     step();
     settle();
   }
@@ -330,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t k_loads = 0, v_loads = 0, q_loads = 0;  // what the producer has started
   // the k-th unit, once it is known; a warp hands it back when it needs no more of it
   auto known = [&](uint32_t k) -> bool {
-    return __all_sync(0xffffffffu, wait_for(&bar.unit_full[k % kUnits], k / kUnits & 1, abort, kUnitTries));
+    return __all_sync(0xffffffffu, wait_for(&bar.unit_full[k % kUnits], k / kUnits & 1, abort));
   };
   auto hand_back = [&](uint32_t k) {
     __syncwarp();
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w(a, cost, run, TileShape{NT * npt, KT});
     if (lane == 0) {
       for (uint32_t k = 0;; ++k) {
-        if (k >= kUnits && !wait_for(&bar.unit_empty[k % kUnits], (k / kUnits - 1) & 1, abort, kUnitTries)) break;
+        if (k >= kUnits && !wait_for(&bar.unit_empty[k % kUnits], (k / kUnits - 1) & 1, abort)) break;
         bar.units[k % kUnits] = w.u;
         mbar_arrive(&bar.unit_full[k % kUnits]);
         if (!w.u.more) break;
@@ -601,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < HD; c += 16) {
                   uint32_t o[16];
                   tmem_ld16_nowait(tmem + wg * HD + lanes + c, o);
-                  tmem_wait_ld();
+                  tmem_landed(o);
 #pragma unroll
                   for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                   tmem_st16_nowait(tmem + wg * HD + lanes + c, o);
@@ -642,16 +655,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && outputs_over(0, look(0)) && outputs_over(1, look(1));
         if (ok) {
           tc_fence_after();
-          const bool whole = tiles == w.tiles;
+          const bool whole = w.end - w.begin == w.tiles, done = w.last == w.end;
           bf16* out = static_cast<bf16*>(a.out) + (long long)(w.token + token) * a.out_stride +
                       (long long)(w.kvh * G + g) * HD;
           const int c0 = w.c0, c1 = w.c1;
-          // a unit that ends in a later run lies in its first CTA's slot 1, in the others' slot 0
+          // a unit that ends in a later run lies in its first CTA's slot 1, in the others' slot 0; parts of whole ones before it
+          // pass through slot 1
           auto slot_of = [&](int c) { return slots + (long long)(2 * c + (c == c0 ? 1 : 0)) * L::SLOT + warp * 32 * (HD + 2); };
-          const float inv = 1.f / l;
           float* mine = slot_of(blockIdx.x);
+          const uint32_t from = tmem + wg * HD + lanes;
+          if (w.first > w.begin) {  // with the parts before it
+            const float2 ml = *reinterpret_cast<const float2*>(mine + 32 * HD + lane * 2);
+            const float top = fmaxf(m, ml.x);
+            const float f0 = m == -INFINITY ? 0.f : ex2_approx(m - top), f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+            m = top, l = fmaf(l, f0, ml.y * f1);
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              uint32_t o[16];
+              tmem_ld16_nowait(from + c, o);
+              tmem_landed(o);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float4 y = *reinterpret_cast<const float4*>(mine + (c / 4 + k) * 128 + lane * 4);
+                o[4 * k] = __float_as_uint(fmaf(__uint_as_float(o[4 * k]), f0, y.x * f1));
+                o[4 * k + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * k + 1]), f0, y.y * f1));
+                o[4 * k + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * k + 2]), f0, y.z * f1));
+                o[4 * k + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * k + 3]), f0, y.w * f1));
+              }
+              tmem_st16_nowait(from + c, o);
+            }
+            tmem_wait_st();
+          }
+          const float inv = 1.f / l;
           auto put = [&](const uint32_t* o, int c) {
-            if (!whole) {
+            if (!whole || !done) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 *reinterpret_cast<uint4*>(mine + (c / 4 + k) * 128 + lane * 4) =
@@ -667,7 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
           // 32 columns on their way while 32 are stored
-          const uint32_t from = tmem + wg * HD + lanes;
           uint32_t o0[32], o1[32];
           tmem_ld32_nowait(from, o0);
 #pragma unroll 1
@@ -682,8 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.o_free[wg]);
-          if (!whole) {
-            *reinterpret_cast<float2*>(mine + 32 * HD + lane * 2) = make_float2(m, l);
+          if (!whole || !done) *reinterpret_cast<float2*>(mine + 32 * HD + lane * 2) = make_float2(m, l);
+          if (!whole && done) {
             __threadfence();
             __syncwarp();
             int before = 0;
