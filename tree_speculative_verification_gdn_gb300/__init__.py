@@ -503,6 +503,13 @@ def _scratch(size: int, device, stream):
         return torch.empty(size, dtype=torch.uint8, device=device)
 
 
+def _room(workspace, device: int):
+    """Pointer and bytes of a caller's workspace on the current device."""
+    if workspace.is_cuda and workspace.get_device() != device:
+        raise ValueError(f"workspace lies on {workspace.device} while cuda:{device} is the current device")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
 def _dense(t, shape, dtype, device: int, name: str):
     """Pointer of a dense tensor on the current device (the calls launch on its stream)."""
     if t is None:
@@ -602,7 +609,7 @@ def tv_window_attn_prompt(q, k_cache, v_cache, block_table, cu_seqlens, prefix_l
         workspace = _scratch(size, q.device, stream)
         room = None if workspace is None else workspace.data_ptr()
     else:
-        size, room = workspace.numel() * workspace.element_size(), _ptr(workspace)
+        room, size = _room(workspace, device)
     pq, sq = _heads(q, tokens, bf, device, Hq * hd, "q")
     po, so = _heads(out, tokens, bf, device, Hq * hd, "out")
     _check(lib.tv_window_attn_prompt(
@@ -629,7 +636,7 @@ def tv_window_attn_step(q, k_cache, v_cache, block_table, prefix_len, out, err, 
         workspace = _scratch(size, q.device, stream)
         room = None if workspace is None else workspace.data_ptr()
     else:
-        size, room = workspace.numel() * workspace.element_size(), _ptr(workspace)
+        room, size = _room(workspace, device)
     pq, sq = _heads(q, tokens, bf, device, Hq * hd, "q")
     po, so = _heads(out, tokens, bf, device, Hq * hd, "out")
     _check(lib.tv_window_attn_step(
