@@ -9,15 +9,17 @@
 //
 // Scores S = Q K^T go to tensor memory, two buffers a row tile; a thread takes a row (TMEM lane) of 64 to registers, and
 // 2^(S scale - m) goes back as bf16, to a buffer that O += P V reads.  MMAs with different accumulators need not run in
-// order, so nothing is written before the reader of what was there has ended.  The sum is of the fp32 weights before their
-// rounding, whose errors average out.
+// order, so nothing is written before the reader of what was there has ended.  Weights in fp32 would be a second product.  The
+// sum is of the fp32 weights before their rounding; a sum of the rounded ones is nearer where few keys carry a row (scores of
+// sigma 4: outputs off by 0.0019 of their norm in place of 0.0021, the store alone 0.0017; sigma 1: 0.0023 both), but took
+// 1.64 ms for 16384 tokens at head dim 128 in place of 1.51.
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, output of each (one row tile: two buffers in turn, warps 0-3)
 //   warp 8           TMA: queries, K and V tiles through a ring each
 //   warp 9, 11       MMAs of scores, of outputs: one warp for both spent longer on its waits and commits than the MMAs took
 //   warp 10          the run's units, up to four ahead
 //
 // Bound by the matrix units and by tensor memory, which they share with the loads and stores of scores and weights.  16384
-// tokens, 32 query heads on 8: head dim 64 1.34 ms, 128 1.52 ms (1.45 PFLOP/s), 256 2.82 ms (1.56 PFLOP/s).  The same copies and
+// tokens, 32 query heads on 8: head dim 64 1.34 ms, 128 1.51 ms (1.46 PFLOP/s), 256 2.82 ms (1.56 PFLOP/s).  The same copies and
 // MMAs without the softmax take 1.14, 1.30 and 2.65 ms; without its arithmetic, but with its loads and stores, 1.29, 1.55
 // and 2.80.  Tiles of 96 keys, fewer and longer MMAs with one buffer of weights, took 1.40 and 1.57 ms (64, 128); tiles of
 // 128, scores and weights in one buffer and a wait between, 1.49 and 1.70.
